@@ -42,9 +42,9 @@ def listed():
         # a full batch's next tokens
         {"name": "step batch", "op": "step", "n": 256, "heads": 48, "dtype": "bfloat16"},
         # the new tokens of one decode step enter the cache
-        {"name": "cache step", "op": "cache", "tokens": 64, "heads": 8, "page": 64, "kind": 8},
-        # a prompt's tokens enter the cache
-        {"name": "cache prompt", "op": "cache", "tokens": 16391, "heads": 8, "page": 64, "kind": 8},
+        {"name": "cache step", "op": "cache", "n": 64, "tokens": 64, "heads": 8, "page": 64, "kind": 8},
+        # the tokens of a batch of prompts enter the cache
+        {"name": "cache prompt", "op": "cache", "n": 5, "tokens": 16391, "heads": 8, "page": 64, "kind": 8},
         # one request's next token over a short context
         {"name": "attend one", "op": "attend", "n": 1, "new": 1, "context": 777, "q_heads": 8, "heads": 2, "page": 32, "kind": 16, "ragged": 0},
         # a batch's next tokens over 8-bit caches
@@ -70,7 +70,8 @@ def draw(rng):
     if op == "step":
         return {"op": op, "n": _between(rng, 1, 256), "heads": _between(rng, 1, 48), "dtype": rng.choice(("float32", "bfloat16"))}
     if op == "cache":
-        return {"op": op, "tokens": _between(rng, 1, 16384), "heads": _between(rng, 1, 16),
+        tokens = _between(rng, 1, 16384)
+        return {"op": op, "n": _between(rng, 1, min(tokens, 64)), "tokens": tokens, "heads": _between(rng, 1, 16),
                 "page": rng.choice((32, 64, 128, 256)), "kind": rng.choice((8, 16))}
     heads = rng.choice((1, 2, 4, 8))
     group = rng.choice((1, 2, 3, 4, 7, 8, 16))
@@ -165,13 +166,12 @@ def _inputs(case, seed):
         x[:, :, ::37] *= 3
         return x.to(bf16)
     page, h = case["page"], case["heads"]
-    if op == "cache":
-        t = case["tokens"]
-        pages = -(-t // page) + 1
-        slots = torch.randperm(pages * page, generator=g, device="cuda")[:t].to(torch.int32)
-        return {"pages": pages, "slots": slots, "k": vectors(t, h), "v": vectors(t, h),
-                "k_out": torch.empty((t, h, D), dtype=bf16, device="cuda"), "v_out": torch.empty((t, h, D), dtype=bf16, device="cuda")}
-    both = _contexts(case)
+    if op == "cache":  # each request writes behind what it has cached before
+        n, t, r = case["n"], case["tokens"], random.Random(case["tokens"])
+        new = [t // n + (i < t % n) for i in range(n)]
+        both = [(m, m + r.randrange(0, 300)) for m in new]
+    else:
+        both = _contexts(case)
     need = [-(-c // page) for _, c in both]
     pages, most = sum(need) + 3, max(need)
     order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
@@ -181,12 +181,14 @@ def _inputs(case, seed):
         table[b, :m] = order[at:at + m]
         at += m
     t = sum(new for new, _ in both)
+    s = {"both": both, "pages": pages, "table": table, "context": torch.tensor([c for _, c in both], dtype=torch.int32, device="cuda"),
+         "cu": torch.tensor([0] + [new for new, _ in both], device="cuda").cumsum(0).to(torch.int32)}
+    if op == "cache":
+        return {**s, "k": vectors(t, h), "v": vectors(t, h), "k_out": torch.empty((t, h, D), dtype=bf16, device="cuda"),
+                "v_out": torch.empty((t, h, D), dtype=bf16, device="cuda")}
     kv = sum(c for _, c in both)
-    slots = torch.cat([table[b].long().repeat_interleave(page)[:c] * page + torch.arange(c, device="cuda") % page for b, (_, c) in enumerate(both)])
-    return {"both": both, "pages": pages, "table": table, "slots": slots.to(torch.int32), "k": vectors(kv, h), "v": vectors(kv, h),
-            "cu": torch.tensor([0] + [new for new, _ in both], device="cuda").cumsum(0).to(torch.int32),
-            "context": torch.tensor([c for _, c in both], dtype=torch.int32, device="cuda"),
-            "q": _normal(g, t, case["q_heads"], D).to(bf16),
+    return {**s, "k": vectors(kv, h), "v": vectors(kv, h), "q": _normal(g, t, case["q_heads"], D).to(bf16),
+            "whole": torch.tensor([0] + [c for _, c in both], device="cuda").cumsum(0).to(torch.int32),
             "o": torch.empty((t, case["q_heads"], D), dtype=bf16, device="cuda"), "scale": 1 / math.sqrt(D)}
 
 
@@ -210,7 +212,7 @@ def prepare(case, seed):
         from quantized_delta_rule_decode_amd import qdr
         s["cache"] = qdr.KVCache(s["pages"], case["page"], case["heads"], case["kind"])
         if op == "attend":
-            s["cache"].qdr_kv_write(s["slots"], s.pop("k"), s.pop("v"))
+            s["cache"].qdr_kv_write(s["table"], s["whole"], s["context"], s.pop("k"), s.pop("v"))
             s["workspace"] = torch.empty(s["cache"].qdr_kv_attend_workspace(case["n"], s["q"].shape[0], case["q_heads"], s["table"].shape[1]), dtype=torch.uint8, device="cuda")
         return s
     shape = (s["pages"] * case["page"], case["heads"])
@@ -220,7 +222,7 @@ def prepare(case, seed):
     else:
         s["values"] = [torch.zeros(shape + (D,), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     if op == "attend":
-        _store(s, s["slots"], s.pop("k"), s.pop("v"))
+        _store(s, _places(s, s["whole"]), s.pop("k"), s.pop("v"))
     return s
 
 
@@ -243,11 +245,12 @@ def run(state):
         return _plain_step(state)
     if op == "cache":
         if own:
-            state["cache"].qdr_kv_write(state["slots"], state["k"], state["v"])
-            state["cache"].qdr_kv_read(state["slots"], state["k_out"], state["v_out"])
+            state["cache"].qdr_kv_write(state["table"], state["cu"], state["context"], state["k"], state["v"])
+            state["cache"].qdr_kv_read(state["table"], state["cu"], state["context"], state["k_out"], state["v_out"])
             return {"k": state["k_out"], "v": state["v_out"]}
-        _store(state, state["slots"], state["k"], state["v"])
-        k, v = _load(state, state["slots"].long())
+        at = _places(state, state["cu"])
+        _store(state, at, state["k"], state["v"])
+        k, v = _load(state, at)
         return {"k": k.to(torch.bfloat16), "v": v.to(torch.bfloat16)}
     if own:
         state["cache"].qdr_kv_attend(state["table"], state["cu"], state["context"], state["q"], state["o"], scale=state["scale"],
@@ -316,8 +319,16 @@ def _plain_step(s):
     return {"o": (q[..., :, None] * S).sum(-2).to(s["q"].dtype), "S": s["S"].view(*S.shape[:2], D // 4, 4, D)}
 
 
-def _store(s, slots, k, v):
-    at = slots.long()
+def _places(s, cu):
+    """Where the last tokens of each request are in the cache: page and row of every token that `cu` counts."""
+    cu, page = cu.long(), s["case"]["page"]
+    token = torch.arange(s["k"].shape[0], device="cuda")
+    row = torch.searchsorted(cu[1:].contiguous(), token, right=True)
+    pos = s["context"].long()[row] - cu[row + 1] + token
+    return s["table"].long()[row, pos // page] * page + pos % page
+
+
+def _store(s, at, k, v):
     for i, x in enumerate((k, v)):
         if s["case"]["kind"] == 16:
             s["values"][i][at] = x
