@@ -1,7 +1,7 @@
 """Build libqdr.so (HIP kernels for gfx950 + host runtime) in the package directory.
 
 Each translation unit (one per whole-head storage kind, the row-unit kernels,
-the dispatch and the host runtime) compiles to an object in parallel; the
+the token mixers, the dispatch and the host runtime) compiles to an object in parallel; the
 objects are then linked into one shared library.
 """
 from __future__ import annotations
@@ -27,7 +27,9 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 SOURCES = ["qdr_head_int_step.hip", "qdr_head_int_pack.hip", "qdr_head_int_unpack.hip",
            "qdr_head_int_reset.hip", "qdr_head_int_readout.hip", "qdr_head_int_step_bf16.hip", "qdr_head_int_writeback.hip", "qdr_head_fp16.hip", "qdr_head_fp32.hip", "qdr_rows.hip", "qdr_dispatch.cpp",
            "qdr_runtime.cpp", "qdr_clock.hip"]
-# every file the device code is built from (a change to any of them changes the kernels)
+# the token mixers beside the step (prompt form, additive step, key/value cache)
+MIXER_SOURCES = ["qdr_prompt.hip", "qdr_linear.hip", "qdr_kv.hip", "qdr_attend.hip", "qdr_mixer.cpp"]
+# every file the step's device code is built from (a change to any of them changes its kernels)
 # (the clock probe is a diagnostic kernel of its own, not part of the step)
 DEVICE_SOURCES = ["qdr_device.h", "qdr_internal.h"] + [s for s in SOURCES
                                                       if s.endswith(".hip") and s != "qdr_clock.hip"]
@@ -60,9 +62,10 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
-    jobs = jobs or min(len(SOURCES), os.cpu_count() or 1, 16)
+    sources = SOURCES + MIXER_SOURCES
+    jobs = jobs or min(len(sources), os.cpu_count() or 1, 16)
     with cf.ThreadPoolExecutor(jobs) as ex:
-        objs = list(ex.map(_compile, SOURCES))
+        objs = list(ex.map(_compile, sources))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -1,0 +1,478 @@
+// qdr_attend.hip -- attention of new tokens over the paged cache:
+//   o = sum_i p_i v_i / sum_i p_i,  p_i = 2^(s_i - m),  s_i = scale log2(e) q.k_i,
+// one pass over the keys with the running maximum m and sum (online softmax).
+// Everything is transposed: S^T = K Q^T has a query in each column, so a
+// query's statistics are one value a lane, and the accumulators of S^T are the
+// B operand of O^T = V^T P^T (qdr_mfma.h); the cache keeps K and V in the
+// order of the A operands.  So nothing crosses lanes between the two products
+// except the column maximum (two shuffles).
+// 8-bit caches: codes are exact in bfloat16, the key's scale multiplies its
+// scores and the value's scale its weights, both in fp32.
+#include "qdr_mfma.h"
+#include "qdr_mixer.h"
+
+namespace qdr {
+
+namespace {
+
+constexpr int kD = 128;
+constexpr float kNone = -INFINITY;
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Eight codes as bfloat16 (exact).
+__device__ __forceinline__ Frag widen(uint32_t a, uint32_t b) {
+  Frag f;
+  f.u[0] = pack_bf16((float)(int8_t)a, (float)(int8_t)(a >> 8));
+  f.u[1] = pack_bf16((float)(int8_t)(a >> 16), (float)(int8_t)(a >> 24));
+  f.u[2] = pack_bf16((float)(int8_t)b, (float)(int8_t)(b >> 8));
+  f.u[3] = pack_bf16((float)(int8_t)(b >> 16), (float)(int8_t)(b >> 24));
+  return f;
+}
+
+// The rows of a tile: `tokens` tokens from `token` on, times `heads` query
+// heads from `head` on; row r is token r / heads, head r % heads.
+struct Tile {
+  int b, first, len;     // sequence and its rows
+  int token, tokens;     // tokens of the tile, from the sequence's `token`
+  int head, heads;       // query heads, from `head` of the whole call
+  int position;          // of the tile's first token
+  int keys;              // keys that the tile's last token sees
+  bool skipped;          // its rows are 0
+};
+
+template <bool FEW>
+__device__ __forceinline__ bool tile_of(const AttendArgs &A, const AttendPlan &plan, int tile, int part, int kvh, Tile &t) {
+  const KvArgs &P = A.kv;
+  const int per = FEW ? plan.few_tokens : plan.many_tokens;
+  t.b = sequence_of(P.cu, P.n, per, 1, tile);
+  if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len)) return false;
+  t.token = (tile - (t.first / per + t.b)) * per;
+  if (t.token < 0 || t.token >= t.len) return false;
+  // where a call has both kinds of launches, each takes its own sequences
+  if (plan.few && plan.many && (t.len <= plan.few_tokens) != FEW) return false;
+  t.tokens = min(per, t.len - t.token);
+  const int heads = FEW ? plan.few_heads : plan.many_heads;
+  t.head = kvh * plan.group + part * heads;
+  t.heads = min(heads, plan.group - part * heads);
+  const int ctx = P.context[t.b];
+  const long long room = (long long)P.max_pages << P.page_shift;
+  t.skipped = ctx < t.len || ctx > room;
+  t.position = ctx - t.len + t.token;
+  t.keys = t.skipped ? 0 : t.position + t.tokens;
+  return true;
+}
+
+// Blocks of one piece of the keys: pieces are cut so that none is shorter
+// than `least` blocks but the last.
+__device__ __forceinline__ int piece_blocks(int blocks, int splits, int least) {
+  return max((blocks + splits - 1) / splits, least);
+}
+
+__device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int b, int kvh, int block, uint32_t bytes) {
+  const int page = P.pages[(size_t)b * P.max_pages + (block >> (P.page_shift - 5))];
+  if (page < 0 || page >= P.num_pages) return nullptr;
+  const int per = 1 << (P.page_shift - 5);
+  return P.base + (((size_t)page * P.heads + kvh) * per + (block & (per - 1))) * bytes;
+}
+
+// ---- few rows: up to 16 (one token of up to 16 heads, a few tokens of fewer)
+// Four waves take every fourth block of 32 keys, each with its own running
+// maximum, straight from memory into operands; they meet in LDS at the end.
+template <int KIND>
+struct FewIn {
+  u32x4 k[KIND == 8 ? 4 : 8], v[KIND == 8 ? 4 : 8];
+  f32x4 ks[2], vs[2];
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan plan) {
+  const KvArgs &P = A.kv;
+  __shared__ float sm[4][16], sl[4][16];
+  __shared__ f32x4 so[4][8][64];
+  const int split = blockIdx.x % plan.few_splits;
+  const int part = blockIdx.x / plan.few_splits % plan.few_parts;
+  const int kvh = blockIdx.x / (plan.few_splits * plan.few_parts) % P.heads;
+  const int tile = blockIdx.x / (plan.few_splits * plan.few_parts * P.heads);
+  Tile t;
+  if (!tile_of<true>(A, plan, tile, part, kvh, t)) return;
+  const int blocks = (t.keys + kBlock - 1) / kBlock;
+  const int each = piece_blocks(blocks, plan.few_splits, kFewLeast);
+  const int lo = split * each, hi = min(lo + each, blocks);
+  if (lo >= hi && split > 0) return;
+
+  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, i16 = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // column i16 of the products: one (token, head) of the tile
+  const int tok = i16 / t.heads, hd = i16 % t.heads;
+  const bool row = tok < t.tokens;
+  const size_t at = ((size_t)(t.first + t.token + (row ? tok : 0)) * A.q_heads + t.head + (row ? hd : 0)) * kD;
+  const int limit = row ? t.position + tok : -1;   // last key that it sees
+  Frag q[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    q[s].w = *(const u32x4_a4 *)(A.q + at + 64 * (s >> 1) + 16 * g + 8 * (s & 1));
+    if (!row) q[s].w = (u32x4){0, 0, 0, 0};
+  }
+  f32x4 o[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) o[d] = (f32x4){0, 0, 0, 0};
+  float m = kNone, sum = 0.0f;
+
+  auto load = [&](int block, FewIn<KIND> &in) -> bool {
+    const uint8_t *blk = block_at(P, t.b, kvh, block, KIND == 8 ? kKv8Block : kKv16Block);
+    if (!blk) {
+      if (l == 0) atomicOr(P.err, kErrPage);
+      return false;
+    }
+    constexpr int N = KIND == 8 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      in.k[i] = *(const u32x4 *)(blk + (i * 64 + l) * 16);
+      in.v[i] = *(const u32x4 *)(blk + N * 1024 + (i * 64 + l) * 16);
+    }
+    if (KIND == 8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        in.ks[i] = *(const f32x4 *)(blk + kKv8Scale + 64 * i + 16 * g);
+        in.vs[i] = *(const f32x4 *)(blk + kKv8Scale + 4 * kBlock + 64 * i + 16 * g);
+      }
+    }
+    return true;
+  };
+
+  FewIn<KIND> in;
+  bool have = lo + w < hi && load(lo + w, in);
+  for (int block = lo + w; block < hi; block += 4) {
+    const FewIn<KIND> now = in;
+    const bool good = have;
+    have = block + 4 < hi && load(block + 4, in);
+    if (!good) continue;
+    f32x4 s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        Frag k;
+        if (KIND == 8) {
+          const u32x4 z = now.k[2 * i + (x >> 1)];
+          k = (x & 1) ? widen(z[2], z[3]) : widen(z[0], z[1]);
+        } else {
+          k.w = now.k[(4 * i + x) & (KIND == 8 ? 3 : 7)];
+        }
+        s[i] = mma(k, q[x], s[i]);
+      }
+      if (KIND == 8) s[i] *= now.ks[i];
+      s[i] *= A.scale_log2;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (block * kBlock + 16 * i + 4 * g + r > limit) s[i][r] = kNone;
+    }
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m1 = fmaxf(m, top);
+    const float ref = m1 == kNone ? 0.0f : m1;      // no key seen yet: weights 2^(-inf) = 0
+    const float fade = ex2(m - ref);
+    m = m1;
+    f32x4 p[2];
+    float add = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        p[i][r] = ex2(s[i][r] - ref);
+        add += p[i][r];
+        // a masked key's scale is not looked at
+        if (KIND == 8) p[i][r] = s[i][r] == kNone ? 0.0f : p[i][r] * now.vs[i][r];
+      }
+    sum = __builtin_fmaf(sum, fade, add);
+    Frag pf;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pf.u[2 * i] = pack_bf16(p[i][0], p[i][1]);
+      pf.u[2 * i + 1] = pack_bf16(p[i][2], p[i][3]);
+    }
+    // values behind the last key of the tile may be anything: 0 times them is not 0
+    const int left = t.keys - block * kBlock;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      Frag v;
+      if (KIND == 8) {
+        const u32x4 z = now.v[d >> 1];
+        v = (d & 1) ? widen(z[2], z[3]) : widen(z[0], z[1]);
+      } else {
+        v.w = now.v[d & (KIND == 8 ? 3 : 7)];
+        if (left < kBlock) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool out = 4 * g + (e & 3) + 16 * (e >> 2) >= left;
+            if (out) v.u[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+      }
+      o[d] = mma(v, pf, o[d] * fade);
+    }
+  }
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (g == 0) {
+    sm[w][i16] = m;
+    sl[w][i16] = sum;
+  }
+  __syncthreads();
+  const float top = fmaxf(fmaxf(sm[0][i16], sm[1][i16]), fmaxf(sm[2][i16], sm[3][i16]));
+  const float ref = top == kNone ? 0.0f : top;
+  float total = 0.0f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) total = __builtin_fmaf(sl[x][i16], ex2(sm[x][i16] - ref), total);
+  const float fade = ex2(m - ref);
+#pragma unroll
+  for (int d = 0; d < 8; ++d) so[w][d][l] = o[d] * fade;
+  __syncthreads();
+  // lane (g, i16) of wave w: channels 16 d + 4 g .. of column i16, d = 2 w, 2 w + 1
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int d = 2 * w + x;
+    const f32x4 y = (so[0][d][l] + so[1][d][l]) + (so[2][d][l] + so[3][d][l]);
+    if (plan.few_splits == 1) {
+      if (row) {
+        const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+        *(u32x2_a4 *)(A.o + at + 16 * d + 4 * g) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+      }
+    } else {
+      float *to = A.part + (size_t)blockIdx.x * (kFewRows * (kD + 2));
+      *(f32x4 *)(to + (size_t)i16 * kD + 16 * d + 4 * g) = y;
+      if (w == 0 && x == 0 && g == 0) {
+        to[kFewRows * kD + i16] = top;
+        to[kFewRows * kD + kFewRows + i16] = total;
+      }
+    }
+  }
+}
+
+// ---- many rows: up to 128, 32 a wave; blocks of keys go through LDS
+template <int KIND>
+__global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan plan) {
+  const KvArgs &P = A.kv;
+  __shared__ u32x4 sk[8][64], sv[8][64];
+  __shared__ f32x4 ss[2][8];
+  const int tiles = plan.many_tiles;
+  const int tile = tiles - 1 - (int)(blockIdx.x % tiles);   // the last tiles see the most keys
+  const int split = blockIdx.x / tiles % plan.many_splits;
+  const int part = blockIdx.x / (tiles * plan.many_splits) % plan.many_parts;
+  const int kvh = blockIdx.x / (tiles * plan.many_splits * plan.many_parts);
+  Tile t;
+  if (!tile_of<false>(A, plan, tile, part, kvh, t)) return;
+  const int blocks = (t.keys + kBlock - 1) / kBlock;
+  const int each = piece_blocks(blocks, plan.many_splits, kManyLeast);
+  const int lo = split * each, hi = min(lo + each, blocks);
+  if (lo >= hi && split > 0) return;
+
+  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, i16 = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  Frag q[2][4];
+  f32x4 o[2][8];
+  float m[2], sum[2];
+  int limit[2];
+  size_t at[2];
+  bool row[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int r = 32 * w + 16 * c + i16;
+    const int tok = r / t.heads, hd = r % t.heads;
+    row[c] = tok < t.tokens;
+    at[c] = ((size_t)(t.first + t.token + (row[c] ? tok : 0)) * A.q_heads + t.head + (row[c] ? hd : 0)) * kD;
+    limit[c] = row[c] ? t.position + tok : -1;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      q[c][s].w = *(const u32x4_a4 *)(A.q + at[c] + 64 * (s >> 1) + 16 * g + 8 * (s & 1));
+      if (!row[c]) q[c][s].w = (u32x4){0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int d = 0; d < 8; ++d) o[c][d] = (f32x4){0, 0, 0, 0};
+    m[c] = kNone;
+    sum[c] = 0.0f;
+  }
+
+  for (int block = lo; block < hi; ++block) {
+    const uint8_t *blk = block_at(P, t.b, kvh, block, KIND == 8 ? kKv8Block : kKv16Block);
+    if (!blk) {
+      if (tid == 0) atomicOr(P.err, kErrPage);
+      continue;
+    }
+    const int left = t.keys - block * kBlock;
+    __syncthreads();
+    if (KIND == 8) {
+      const u32x4 k = *(const u32x4 *)(blk + tid * 16), v = *(const u32x4 *)(blk + kKv8Half + tid * 16);
+      sk[2 * w][l] = widen(k[0], k[1]).w;
+      sk[2 * w + 1][l] = widen(k[2], k[3]).w;
+      sv[2 * w][l] = widen(v[0], v[1]).w;
+      sv[2 * w + 1][l] = widen(v[2], v[3]).w;
+      if (tid < 16) ss[tid >> 3][tid & 7] = *(const f32x4 *)(blk + kKv8Scale + 16 * tid);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sk[4 * x + w][l] = *(const u32x4 *)(blk + (tid + 256 * x) * 16);
+        Frag v;
+        v.w = *(const u32x4 *)(blk + kKv16Half + (tid + 256 * x) * 16);
+        if (left < kBlock) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool out = 4 * g + (e & 3) + 16 * (e >> 2) >= left;
+            if (out) v.u[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+        sv[4 * x + w][l] = v.w;
+      }
+    }
+    __syncthreads();
+    f32x4 s[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[0][i] = s[1][i] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        Frag k;
+        k.w = sk[4 * i + x][l];
+        s[0][i] = mma(k, q[0][x], s[0][i]);
+        s[1][i] = mma(k, q[1][x], s[1][i]);
+      }
+    }
+    Frag pf[2];
+    float fade[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (KIND == 8) s[c][i] *= ss[0][4 * i + g];
+        s[c][i] *= A.scale_log2;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (block * kBlock + 16 * i + 4 * g + r > limit[c]) s[c][i][r] = kNone;
+      }
+      float top = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
+                        fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m1 = fmaxf(m[c], top);
+      const float ref = m1 == kNone ? 0.0f : m1;
+      fade[c] = ex2(m[c] - ref);
+      m[c] = m1;
+      float add = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f32x4 p;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          p[r] = ex2(s[c][i][r] - ref);
+          add += p[r];
+          if (KIND == 8) p[r] = s[c][i][r] == kNone ? 0.0f : p[r] * ss[1][4 * i + g][r];
+        }
+        pf[c].u[2 * i] = pack_bf16(p[0], p[1]);
+        pf[c].u[2 * i + 1] = pack_bf16(p[2], p[3]);
+      }
+      sum[c] = __builtin_fmaf(sum[c], fade[c], add);
+    }
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      Frag v;
+      v.w = sv[d][l];
+      o[0][d] = mma(v, pf[0], o[0][d] * fade[0]);
+      o[1][d] = mma(v, pf[1], o[1][d] * fade[1]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    sum[c] += __shfl_xor(sum[c], 16);
+    sum[c] += __shfl_xor(sum[c], 32);
+    if (plan.many_splits == 1) {
+      if (!row[c]) continue;
+      const float inv = sum[c] > 0.0f || sum[c] != sum[c] ? 1.0f / sum[c] : 0.0f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const f32x4 y = o[c][d] * inv;
+        *(u32x2_a4 *)(A.o + at[c] + 16 * d + 4 * g) = (u32x2){pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+      }
+    } else {
+      const size_t unit = (((size_t)tile * P.heads + kvh) * plan.many_parts + part) * plan.many_splits + split;
+      float *to = A.part + plan.few_floats + unit * (kManyRows * (kD + 2));
+      const int r = 32 * w + 16 * c + i16;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) *(f32x4 *)(to + (size_t)r * kD + 16 * d + 4 * g) = o[c][d];
+      if (g == 0) {
+        to[kManyRows * kD + r] = m[c];
+        to[kManyRows * kD + kManyRows + r] = sum[c];
+      }
+    }
+  }
+}
+
+// Joins the pieces of the keys: one wave a row, two channels a lane.
+template <bool FEW>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, AttendPlan plan) {
+  constexpr int kRows = FEW ? kFewRows : kManyRows;
+  const KvArgs &P = A.kv;
+  const int parts = FEW ? plan.few_parts : plan.many_parts, splits = FEW ? plan.few_splits : plan.many_splits;
+  const int l = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = (blockIdx.x % (kRows / 4)) * 4 + w, unit = blockIdx.x / (kRows / 4);
+  const int part = unit % parts, kvh = unit / parts % P.heads, tile = unit / (parts * P.heads);
+  Tile t;
+  if (!tile_of<FEW>(A, plan, tile, part, kvh, t)) return;
+  const int tok = r / t.heads, hd = r % t.heads;
+  if (tok >= t.tokens) return;
+  const int blocks = (t.keys + kBlock - 1) / kBlock;
+  const int each = piece_blocks(blocks, splits, FEW ? kFewLeast : kManyLeast);
+  const int live = max((blocks + each - 1) / each, 1);
+  const float *from = A.part + (FEW ? 0 : plan.few_floats) + (size_t)unit * splits * (kRows * (kD + 2));
+  constexpr size_t kStep = kRows * (kD + 2);
+  float m = kNone;
+  for (int s = 0; s < live; ++s) m = fmaxf(m, from[s * kStep + kRows * kD + r]);
+  const float ref = m == kNone ? 0.0f : m;
+  float sum = 0.0f, a = 0.0f, b = 0.0f;
+  for (int s = 0; s < live; ++s) {
+    const float f = ex2(from[s * kStep + kRows * kD + r] - ref);
+    sum = __builtin_fmaf(from[s * kStep + kRows * kD + kRows + r], f, sum);
+    const f32x2 y = *(const f32x2 *)(from + s * kStep + (size_t)r * kD + 2 * l);
+    a = __builtin_fmaf(y[0], f, a);
+    b = __builtin_fmaf(y[1], f, b);
+  }
+  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+  const size_t at = ((size_t)(t.first + t.token + tok) * A.q_heads + t.head + hd) * kD;
+  *(uint32_t *)(A.o + at + 2 * l) = pack_bf16(a * inv, b * inv);
+}
+
+__global__ void __launch_bounds__(256) k_attend_check(KvArgs P) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= P.n) return;
+  const long long room = (long long)P.max_pages << P.page_shift;
+  int first, len;
+  if (!rows_of(P.cu, P.T, b, &first, &len) || (len > 0 && (P.context[b] < len || P.context[b] > room)))
+    atomicOr(P.err, kErrLength);
+}
+
+}  // namespace
+
+template <int KIND>
+static hipError_t attend(const AttendArgs &a, const AttendPlan &p, hipStream_t st) {
+  hipLaunchKernelGGL(k_attend_check, dim3((a.kv.n + 255) / 256), dim3(256), 0, st, a.kv);
+  if (p.few) {
+    const uint32_t units = (uint32_t)p.few_tiles * a.kv.heads * p.few_parts;
+    hipLaunchKernelGGL(k_attend_few<KIND>, dim3(units * p.few_splits), dim3(256), 0, st, a, p);
+    if (p.few_splits > 1) hipLaunchKernelGGL(k_attend_join<true>, dim3(units * (kFewRows / 4)), dim3(256), 0, st, a, p);
+  }
+  if (p.many) {
+    const uint32_t units = (uint32_t)p.many_tiles * a.kv.heads * p.many_parts;
+    hipLaunchKernelGGL(k_attend_many<KIND>, dim3(units * p.many_splits), dim3(256), 0, st, a, p);
+    if (p.many_splits > 1) hipLaunchKernelGGL(k_attend_join<false>, dim3(units * (kManyRows / 4)), dim3(256), 0, st, a, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attend(const AttendArgs &a, const AttendPlan &p, int kind, hipStream_t st) {
+  return kind == 8 ? attend<8>(a, p, st) : attend<16>(a, p, st);
+}
+
+}  // namespace qdr

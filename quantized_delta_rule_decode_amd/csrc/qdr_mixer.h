@@ -1,0 +1,109 @@
+// qdr_mixer.h -- arguments and launches of the token mixers (prompt form,
+// additive step, key/value cache); the public ABI is include/qdr_mixer.h.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+namespace qdr {
+
+constexpr uint32_t kErrSlot = 1u, kErrLength = 2u, kErrPage = 4u;   // QDR_DEVERR_*
+
+// ---- prompt form (qdr_prompt.hip)
+constexpr int kChunk = 64;                       // tokens taken at a time
+// Fragments of a lower triangular 64 x 64 matrix: row tile w (16 rows) has
+// w/2 + 1 of them, each 16 rows x 32 columns, 64 lanes x 8 fp32.
+constexpr int kTriFrags = 6;
+constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
+// Workspace of one (chunk, head): the two triangular matrices, then the
+// decays from the chunk's start and to its end.
+constexpr size_t kChunkFloats = 2 * kTriFloats + 2 * kChunk;
+
+struct PromptArgs {
+  const int32_t *slots, *carry, *cu;
+  int32_t n, T, H, num_slots;
+  int32_t chunks;             // chunk places of a head: T/64 + n
+  const uint16_t *q, *k, *v;
+  const float *beta, *gate;
+  uint16_t *o;
+  float *chunk_ws;            // [chunks][H][kChunkFloats]
+  // where the states are: an uncompressed pool's blocks, or dense fp32
+  uint8_t *pool;              // NULL: dense
+  uint64_t slot_stride;
+  float *S;                   // [n][H][128][128]
+  int32_t *slots_in, *slots_out;   // dense: slots to unpack and to pack (-1: none)
+  uint32_t *err;
+};
+hipError_t launch_prompt_slots(const PromptArgs &, hipStream_t);
+hipError_t launch_prompt_chunks(const PromptArgs &, bool delta, hipStream_t);
+hipError_t launch_prompt_scan(const PromptArgs &, bool delta, hipStream_t);
+
+// ---- additive step (qdr_linear.hip)
+struct LinearArgs {
+  const int32_t *slots;
+  int32_t B, H, num_slots;
+  const void *q, *k, *v;
+  const float *gate;
+  void *o;
+  uint8_t *pool;
+  uint64_t slot_stride;
+  uint32_t *err;
+};
+hipError_t launch_linear_step(const LinearArgs &, bool bf16, hipStream_t);
+
+// ---- key/value cache (qdr_kv.hip, qdr_attend.hip)
+// A page holds, head after head, its tokens in blocks of 32.  A block is laid
+// out in the order in which the attention's matrix instructions take it:
+//   K   [16-token tile][.][lane (g, key)][16 B]: channels 64 h + 16 g ..: with
+//       8-bit codes 16 of them (h = 0, 1), with bfloat16 8 (part 2 h + p holds
+//       channels 64 h + 16 g + 8 p ..)
+//   V   [16-channel tile][lane (g, channel)][8 tokens 4 g + {0..3, 16..19}];
+//       8-bit codes keep the two tiles of a pair in one lane's 16 B
+//   8-bit only: fp32 scales of the 32 keys, then of the 32 values.
+constexpr int kBlock = 32;
+constexpr uint32_t kKv8Half = 4096, kKv8Scale = 2 * kKv8Half, kKv8Block = kKv8Scale + 2 * kBlock * 4;
+constexpr uint32_t kKv16Half = 8192, kKv16Block = 2 * kKv16Half;
+
+struct KvArgs {
+  uint8_t *base;
+  int32_t num_pages, page_shift, heads;   // page_shift: log2(page_tokens)
+  const int32_t *pages;
+  int32_t max_pages;
+  const int32_t *cu, *context;
+  int32_t n, T;
+  uint16_t *k, *v;                // write: read only
+  uint32_t *err;
+};
+hipError_t launch_kv_write(const KvArgs &, int kind, hipStream_t);
+hipError_t launch_kv_read(const KvArgs &, int kind, hipStream_t);
+
+// Rows (tokens x query heads of one key/value head) of the two kinds of
+// tiles, and the fewest blocks of keys that a piece of them has.
+constexpr int kFewRows = 16, kManyRows = 128;
+constexpr int kFewLeast = 4, kManyLeast = 4;
+
+// How an attention call is cut up: rows of a tile, tiles, and pieces of the
+// keys; decided on the host from the call's counts alone.
+struct AttendPlan {
+  int group;          // query heads a key/value head
+  // few-row tiles: rows = tokens x heads <= 16
+  bool few; int few_heads, few_tokens, few_parts, few_tiles, few_splits;
+  // many-row tiles: up to 128 rows
+  bool many; int many_heads, many_tokens, many_parts, many_tiles, many_splits;
+  size_t few_floats, many_floats;   // partial results in the workspace
+};
+AttendPlan plan_attend(int n, int T, int q_heads, int heads, int max_pages, int page_shift);
+
+struct AttendArgs {
+  KvArgs kv;
+  const uint16_t *q;
+  uint16_t *o;
+  int32_t q_heads;
+  float scale_log2;      // scale * log2(e)
+  float *part;           // partial results where the keys are cut
+};
+hipError_t launch_attend(const AttendArgs &, const AttendPlan &, int kind, hipStream_t);
+
+}  // namespace qdr

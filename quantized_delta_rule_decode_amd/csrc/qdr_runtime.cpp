@@ -20,6 +20,7 @@
 #include <string>
 #include <vector>
 
+#include "qdr_host.h"
 #include "qdr_internal.h"
 
 namespace {
@@ -294,6 +295,48 @@ qdr_status dispatch(qdr_pool *p, qdr::LaunchArgs a, int n, int mode, hipStream_t
 }
 
 }  // namespace
+
+// ---- for the entry points in other files (qdr_host.h)
+namespace qdr {
+
+PoolView pool_view(const qdr_pool *p) {
+  PoolView v{};
+  v.base = p->base;
+  v.slot_stride = p->L.slot_stride;
+  v.num_slots = p->desc.num_slots;
+  v.num_heads = p->desc.num_heads;
+  v.gate = p->desc.gate;
+  v.device = p->device;
+  v.all_fp32 = p->desc.unit == QDR_UNIT_HEAD;
+  for (uint8_t k : p->kinds) v.all_fp32 = v.all_fp32 && k == QDR_K_FP32;
+  v.err = p->d_err;
+  return v;
+}
+
+qdr_status set_error(qdr_status st, const char *message) { return fail(st, "%s", message); }
+qdr_status set_ok() { return ok(); }
+
+qdr_status pool_check_slots(const qdr_pool *p, const int32_t *slots, int32_t n, hipStream_t st) {
+  return check_slots_host(p, slots, n, st, true);
+}
+
+hipError_t pool_after_writeback(qdr_pool *p, hipStream_t st) { return after_writeback(p, st); }
+
+qdr_status pool_pack(qdr_pool *p, const int32_t *slots, int32_t n, const float *S, hipStream_t st) {
+  LaunchArgs a = base_args(p);
+  a.slots = slots;
+  a.S_in = S;
+  return dispatch(p, a, n, MODE_PACK, st);
+}
+
+qdr_status pool_unpack(qdr_pool *p, const int32_t *slots, int32_t n, float *S, hipStream_t st) {
+  LaunchArgs a = base_args(p);
+  a.slots = slots;
+  a.S_out = S;
+  return dispatch(p, a, n, MODE_UNPACK, st);
+}
+
+}  // namespace qdr
 
 extern "C" {
 

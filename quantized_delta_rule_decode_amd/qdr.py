@@ -1,4 +1,4 @@
-"""Python binding of libqdr (include/qdr.h): argument marshalling only.
+"""Python binding of libqdr (include/qdr.h, include/qdr_mixer.h): argument marshalling only.
 
 Every function here has the name of the C entry point it calls.  Tensors are
 torch tensors on the current HIP device; the library receives their device
@@ -20,7 +20,9 @@ GATE_SCALAR, GATE_DIAG = 0, 1
 UNIT_HEAD, UNIT_ROW = 0, 1
 SCALE_DUAL, SCALE_ROW_ABSMAX = 0, 1
 K_INT2, K_INT4, K_INT6, K_INT8, K_FP16, K_FP32 = 2, 4, 6, 8, 16, 32
-DEVERR_SLOT = 1
+DEVERR_SLOT, DEVERR_LENGTH, DEVERR_PAGE = 1, 2, 4
+RULE_DELTA, RULE_SUM = 0, 1
+KV_INT8, KV_BF16 = 8, 16
 
 _STATUS = {0: "QDR_OK", -1: "QDR_E_INVAL", -2: "QDR_E_NOMEM", -3: "QDR_E_DEVICE",
            -4: "QDR_E_SLOT", -5: "QDR_E_UNSUPPORTED"}
@@ -50,9 +52,18 @@ class Layout(ctypes.Structure):
                 ("base", ctypes.c_void_p), ("bits_per_value", ctypes.c_double)]
 
 
+class KVDesc(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
 EXPORTS = ["qdr_pool_bytes", "qdr_pool_create", "qdr_pool_destroy", "qdr_slot_reset",
            "qdr_pack", "qdr_unpack", "qdr_decode_step", "qdr_decode_step_split", "qdr_decode_step_bf16", "qdr_get_layout", "qdr_read_raw",
            "qdr_write_raw", "qdr_poll_device_error", "qdr_last_error", "qdr_clock_probe"]
+
+MIXER_EXPORTS = ["qdr_prompt_workspace", "qdr_prompt", "qdr_linear_step", "qdr_linear_step_bf16", "qdr_kv_bytes",
+                 "qdr_kv_create", "qdr_kv_destroy", "qdr_kv_write", "qdr_kv_read", "qdr_kv_attend_workspace",
+                 "qdr_kv_attend", "qdr_kv_poll_device_error"]
 
 _lib = None
 
@@ -85,6 +96,18 @@ def load():
         "qdr_write_raw": [P, I32, P, SZ, P],
         "qdr_poll_device_error": [P, ctypes.POINTER(ctypes.c_uint32)],
         "qdr_clock_probe": [P, I32, P],
+        "qdr_prompt_workspace": [P, I32, I32, ctypes.POINTER(SZ)],
+        "qdr_prompt": [P, I32, P, P, P, I32, I32, P, P, P, P, P, P, P, SZ, P],
+        "qdr_linear_step": [P, P, I32, P, P, P, P, P, P],
+        "qdr_linear_step_bf16": [P, P, I32, P, P, P, P, P, P],
+        "qdr_kv_bytes": [ctypes.POINTER(KVDesc), ctypes.POINTER(SZ)],
+        "qdr_kv_create": [ctypes.POINTER(KVDesc), P, SZ, ctypes.POINTER(P)],
+        "qdr_kv_destroy": [P],
+        "qdr_kv_write": [P, P, I32, P, P, I32, I32, P, P, P],
+        "qdr_kv_read": [P, P, I32, P, P, I32, I32, P, P, P],
+        "qdr_kv_attend_workspace": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "qdr_kv_attend": [P, P, I32, P, P, I32, I32, I32, P, ctypes.c_float, P, P, SZ, P],
+        "qdr_kv_poll_device_error": [P, ctypes.POINTER(ctypes.c_uint32)],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -118,6 +141,34 @@ def _dptr(t, dtype, name, numel=None):
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(cu, **tensors):
+    """n of the cumulative counts and T, the rows that every given tensor has."""
+    import torch
+    _dptr(cu, torch.int32, "cu")
+    if cu.dim() != 1 or cu.numel() < 1:
+        raise ValueError("cu must be one-dimensional with n + 1 elements")
+    rows = {t.shape[0] if t.dim() else -1 for t in tensors.values()}
+    if len(rows) != 1:
+        raise ValueError("rows differ: " + ", ".join(f"{k} {tuple(t.shape)}" for k, t in tensors.items()))
+    return cu.numel() - 1, rows.pop()
+
+
+def _workspace(given, need, stream):
+    """Pointer and bytes of a call's workspace; without one, memory of torch's
+    that is not reused before the call's stream is done with it."""
+    import torch
+    if given is not None:
+        return _dptr(given, given.dtype, "workspace"), given.numel() * given.element_size(), given
+    with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    return ctypes.c_void_p(ws.data_ptr()), need, ws
 
 
 def _desc(num_slots, num_heads, kinds, omega, unit, gate, scale_mode, fit_iters, scale_bits=32):
@@ -245,6 +296,51 @@ class Pool:
             _dptr(gate, f32, "gate", gn), _dptr(o, f32, "o", B * H * DIM),
             _stream(stream_readout), _stream(stream_writeback)))
 
+    # ---- token mixers over the pool's states (include/qdr_mixer.h)
+    def qdr_prompt_workspace(self, n, T) -> int:
+        """Bytes of the workspace of a prompt call over n sequences and T rows."""
+        b = ctypes.c_size_t(0)
+        _check("qdr_prompt_workspace", load().qdr_prompt_workspace(self._h, int(n), int(T), ctypes.byref(b)))
+        return int(b.value)
+
+    def qdr_prompt(self, rule, slots, cu, q, k, v, beta, gate, o, carry=None, workspace=None, stream=None):
+        """Whole prompts into the pool's slots.  q, k, v, o: torch.bfloat16
+        [T][H][128]; beta (None for RULE_SUM) and gate fp32 [T][H]; cu int32
+        [n+1]; slots and carry int32 [n].  workspace: None, or a device tensor
+        of at least qdr_prompt_workspace(n, T) bytes."""
+        import torch
+        H, bf, f32, i32 = self.num_heads, torch.bfloat16, torch.float32, torch.int32
+        n, T = _rows(cu, q=q, k=k, v=v, gate=gate, o=o, **({} if beta is None else {"beta": beta}))
+        for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+            _shape(t, (T, H, DIM), name)
+        for name, t in (("gate", gate), ("beta", beta)):
+            if t is not None:
+                _shape(t, (T, H), name)
+        ws, size, keep = _workspace(workspace, 0 if workspace is not None else self.qdr_prompt_workspace(n, T), stream)
+        _check("qdr_prompt", load().qdr_prompt(
+            self._h, int(rule), _dptr(slots, i32, "slots", n), None if carry is None else _dptr(carry, i32, "carry", n),
+            _dptr(cu, i32, "cu"), n, T, _dptr(q, bf, "q"), _dptr(k, bf, "k"), _dptr(v, bf, "v"),
+            None if beta is None else _dptr(beta, f32, "beta"), _dptr(gate, f32, "gate"), _dptr(o, bf, "o"),
+            ws, size, _stream(stream)))
+
+    def _linear_step(self, fn, dtype, slots, q, k, v, gate, o, stream):
+        import torch
+        B, H = slots.numel(), self.num_heads
+        _check(fn, getattr(load(), fn)(
+            self._h, _dptr(slots, torch.int32, "slots"), B,
+            _dptr(q, dtype, "q", B * H * DIM), _dptr(k, dtype, "k", B * H * DIM), _dptr(v, dtype, "v", B * H * DIM),
+            _dptr(gate, torch.float32, "gate", B * H), _dptr(o, dtype, "o", B * H * DIM), _stream(stream)))
+
+    def qdr_linear_step(self, slots, q, k, v, gate, o, stream=None):
+        """q, k, v, o: fp32 [B][H][128]; gate fp32 [B][H]; an uncompressed pool."""
+        import torch
+        self._linear_step("qdr_linear_step", torch.float32, slots, q, k, v, gate, o, stream)
+
+    def qdr_linear_step_bf16(self, slots, q, k, v, gate, o, stream=None):
+        """The same with torch.bfloat16 q, k, v, o."""
+        import torch
+        self._linear_step("qdr_linear_step_bf16", torch.bfloat16, slots, q, k, v, gate, o, stream)
+
     def qdr_read_raw(self, slot, stream=None) -> np.ndarray:
         out = np.empty(self.slot_stride, np.uint8)
         _check("qdr_read_raw", load().qdr_read_raw(
@@ -265,6 +361,96 @@ class Pool:
     def block(self, raw_slot: np.ndarray, h: int) -> np.ndarray:
         off = int(self.head_off[h])
         return raw_slot[off: off + int(self.head_bytes[h])]
+
+
+def qdr_kv_bytes(num_pages, page_tokens, num_heads, kind=KV_INT8) -> int:
+    d, n = KVDesc(num_pages, page_tokens, num_heads, DIM, kind), ctypes.c_size_t(0)
+    _check("qdr_kv_bytes", load().qdr_kv_bytes(ctypes.byref(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+class KVCache:
+    """A paged key/value cache (qdr_kv_create ... qdr_kv_destroy)."""
+
+    def __init__(self, num_pages, page_tokens, num_heads, kind=KV_INT8, dev_mem=None):
+        self.num_pages, self.page_tokens, self.num_heads, self.kind = int(num_pages), int(page_tokens), int(num_heads), int(kind)
+        d, h = KVDesc(self.num_pages, self.page_tokens, self.num_heads, DIM, self.kind), ctypes.c_void_p(None)
+        mem_ptr, mem_bytes = None, 0
+        if dev_mem is not None:
+            mem_ptr, mem_bytes = _dptr(dev_mem, dev_mem.dtype, "dev_mem"), dev_mem.numel() * dev_mem.element_size()
+        self._dev_mem = dev_mem
+        _check("qdr_kv_create", load().qdr_kv_create(ctypes.byref(d), mem_ptr, mem_bytes, ctypes.byref(h)))
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            _check("qdr_kv_destroy", load().qdr_kv_destroy(self._h))
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    # ---- entry points (same names as the C ABI)
+    def _where(self, pages, cu, context):
+        import torch
+        n = cu.numel() - 1
+        if pages.dim() != 2 or pages.shape[0] != n:
+            raise ValueError(f"pages has shape {tuple(pages.shape)}, expected ({n}, max_pages)")
+        i32 = torch.int32
+        return _dptr(pages, i32, "pages"), pages.shape[1], _dptr(cu, i32, "cu"), _dptr(context, i32, "context", n)
+
+    def _move(self, fn, pages, cu, context, k, v, stream):
+        import torch
+        n, T = _rows(cu, k=k, v=v)
+        for name, t in (("k", k), ("v", v)):
+            _shape(t, (T, self.num_heads, DIM), name)
+        _check(fn, getattr(load(), fn)(self._h, *self._where(pages, cu, context), n, T, _dptr(k, torch.bfloat16, "k"),
+                                       _dptr(v, torch.bfloat16, "v"), _stream(stream)))
+
+    def qdr_kv_write(self, pages, cu, context, k, v, stream=None):
+        """pages int32 [n][max_pages], cu int32 [n+1], context int32 [n]; k, v
+        torch.bfloat16 [T][heads][128]: each sequence's last cached tokens."""
+        self._move("qdr_kv_write", pages, cu, context, k, v, stream)
+
+    def qdr_kv_read(self, pages, cu, context, k, v, stream=None):
+        """The same rows read back into k and v."""
+        self._move("qdr_kv_read", pages, cu, context, k, v, stream)
+
+    def qdr_kv_attend_workspace(self, n, T, q_heads, max_pages) -> int:
+        b = ctypes.c_size_t(0)
+        _check("qdr_kv_attend_workspace", load().qdr_kv_attend_workspace(
+            self._h, int(n), int(T), int(q_heads), int(max_pages), ctypes.byref(b)))
+        return int(b.value)
+
+    def qdr_kv_attend(self, pages, cu, context, q, o, scale=None, workspace=None, stream=None):
+        """q, o: torch.bfloat16 [T][q_heads][128]; scale: 1/sqrt(128) if None;
+        workspace: None, or a device tensor of at least
+        qdr_kv_attend_workspace(n, T, q_heads, max_pages) bytes."""
+        import torch
+        n, T = _rows(cu, q=q, o=o)
+        if q.dim() != 3 or q.shape[2] != DIM:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected ({T}, q_heads, {DIM})")
+        _shape(o, q.shape, "o")
+        where = self._where(pages, cu, context)
+        need = 0 if workspace is not None else self.qdr_kv_attend_workspace(n, T, q.shape[1], where[1])
+        ws, size, keep = _workspace(workspace, need, stream)
+        _check("qdr_kv_attend", load().qdr_kv_attend(
+            self._h, *where, n, T, q.shape[1], _dptr(q, torch.bfloat16, "q"), DIM ** -0.5 if scale is None else float(scale),
+            _dptr(o, torch.bfloat16, "o"), ws, size, _stream(stream)))
+
+    def qdr_kv_poll_device_error(self) -> int:
+        f = ctypes.c_uint32(0)
+        _check("qdr_kv_poll_device_error", load().qdr_kv_poll_device_error(self._h, ctypes.byref(f)))
+        return int(f.value)
 
 
 def qdr_last_error() -> str:
