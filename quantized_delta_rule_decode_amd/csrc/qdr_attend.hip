@@ -45,12 +45,17 @@ template <bool FEW>
 __device__ __forceinline__ bool tile_of(const AttendArgs &A, const AttendPlan &plan, int tile, int part, int kvh, Tile &t) {
   const KvArgs &P = A.kv;
   const int per = FEW ? plan.few_tokens : plan.many_tokens;
-  t.b = sequence_of(P.cu, P.n, per, 1, tile);
-  if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len)) return false;
-  t.token = (tile - (t.first / per + t.b)) * per;
-  if (t.token < 0 || t.token >= t.len) return false;
-  // where a call has both kinds of launches, each takes its own sequences
-  if (plan.few && plan.many && (t.len <= plan.few_tokens) != FEW) return false;
+  if (FEW && plan.many) {
+    // a call with both launches: this one takes the sequences of one tile
+    t.b = tile;
+    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len) || t.len == 0 || t.len > per) return false;
+    t.token = 0;
+  } else {
+    t.b = sequence_of(P.cu, P.n, per, 1, tile);
+    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len)) return false;
+    t.token = (tile - (t.first / per + t.b)) * per;
+    if (t.token < 0 || t.token >= t.len || (!FEW && plan.few && t.len <= plan.few_tokens)) return false;
+  }
   t.tokens = min(per, t.len - t.token);
   const int heads = FEW ? plan.few_heads : plan.many_heads;
   t.head = kvh * plan.group + part * heads;

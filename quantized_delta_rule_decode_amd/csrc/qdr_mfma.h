@@ -60,6 +60,15 @@ __device__ __forceinline__ void split(float a, float b, uint32_t *part) {
   }
 }
 
+// Barrier of a workgroup whose waves exchange data through LDS only: waits for
+// the LDS operations before it, not for loads and stores of global memory, so
+// what was loaded ahead stays in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Index of the sequence that place `id` of a call belongs to, where sequence
 // b has places first(b) = cu[b] / per + extra * b on: first() grows with b, so
 // bisect for the last b with first(b) <= id.

@@ -102,7 +102,7 @@ AttendPlan plan_attend(int n, int T, int q_heads, int heads, int max_pages, int 
   // length is T.  Else the two launches share the sequences out by length.
   p.few = n > 1 || T <= p.few_tokens;
   p.many = T > n && !(n == 1 && T <= p.few_tokens);
-  p.few_tiles = p.few ? T / p.few_tokens + n : 0;
+  p.few_tiles = !p.few ? 0 : p.many ? n : T / p.few_tokens + n;
   p.many_tiles = p.many ? T / p.many_tokens + n : 0;
   const int64_t blocks = (int64_t)max_pages << (page_shift - 5);
   // pieces: enough workgroups for the 256 compute units, a few each

@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
         lo *= *(const f32x4 *)&bt[32 * s + 4 * g];
         hi *= *(const f32x4 *)&bt[32 * s + 16 + 4 * g];
       }
-      float *f = dst + (size_t)(tri_frag(w) + s) * 512 + l * 8;
+      float *f = dst + (size_t)(tri_frag(w) + s) * 512 + l * 4;
       *(f32x4 *)f = lo;
-      *(f32x4 *)(f + 4) = hi;
+      *(f32x4 *)(f + 256) = hi;
     }
   };
   store(ws, false);
@@ -178,15 +178,39 @@ __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
   store(ws + kTriFloats, true);
 }
 
-// What a wave of the scan reads of one chunk, held a chunk ahead.
-template <bool DELTA, int NT>
+// What a thread of the scan reads of one chunk a chunk ahead.
+template <int NT>
 struct ChunkIn {
-  Frag q[4], k[4];            // rows of tile w; channels 32 s + {4 g.., 16 + 4 g..}
-  uint16_t v[NT][4];          // rows 4 g + r of tile w, the wave's columns
-  f32x4 A[2][2], T[2][2];     // [fragment][half]
-  f32x4 from, to;             // decays from the chunk's start, to its end
+  Frag q[4], k[4];            // rows of tile w, channels 32 s + 8 g ..
+  u32x2 v[NT];                // columns 4 (tid & 3) .. of tile n, row tid / 4
+  f32x4 from, to;             // decays from the chunk's start, to its end (rows 4 g .. of tile w)
   float all;                  // over the whole chunk
 };
+// Its rows of A and T, [fragment][half], asked for at the chunk's start.
+struct ChunkTri {
+  f32x4 A[2][2], T[2][2];
+};
+
+// Eight fp32 values as P bfloat16 operands.
+template <int P>
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
+  uint32_t p[4][P];
+  split<P>(a[0], a[1], p[0]);
+  split<P>(a[2], a[3], p[1]);
+  split<P>(b[0], b[1], p[2]);
+  split<P>(b[2], b[3], p[3]);
+#pragma unroll
+  for (int x = 0; x < P; ++x) f[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
+}
+// Four values, each part to its place in a B operand of rows: part x at to + x * stride.
+template <int P>
+__device__ __forceinline__ void put4(f32x4 a, u32x4 *to, int stride, int half) {
+  uint32_t p[2][P];
+  split<P>(a[0], a[1], p[0]);
+  split<P>(a[2], a[3], p[1]);
+#pragma unroll
+  for (int x = 0; x < P; ++x) ((Frag *)(to + x * stride))->h[half] = (u32x2){p[0][x], p[1][x]};
+}
 
 template <bool DELTA, int NT>
 __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
@@ -196,6 +220,7 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
   __shared__ u32x4 sU[DELTA ? 2 : 1][2][NT][64];            // U
   __shared__ u32x4 sD[3][2][NT][64];                        // 2^(g_63 - g) U
   __shared__ __attribute__((aligned(16))) uint16_t sK[kD][72];   // K^T; a row's tokens in operand order
+  __shared__ __attribute__((aligned(16))) uint16_t sV[16 * NT][68];   // V^T
 
   // the slices of one (sequence, head) go to one XCD (workgroups are dealt to
   // the eight in turn): they share its q, k, A and T through one L2
@@ -222,7 +247,9 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
   }
   const bool carried = P.carry != nullptr && P.carry[b] != 0;
 
-  // S: wave w holds rows 32 w + 16 i + 4 g + r
+  // S: wave w holds rows 32 w .. 32 w + 31; row 4 g + r of result i is row
+  // 32 w + 8 g + 4 i + r, so that a lane's two results are eight rows in a
+  // row: the channels that one 16-byte load of q or k has
   f32x4 S[2][NT];
   f32x4 *blk = P.pool ? (f32x4 *)(P.pool + (size_t)slot * P.slot_stride + (size_t)h * (kD * kD * 4)) : nullptr;
   float *dense = P.S + (size_t)bh * kD * kD;
@@ -232,142 +259,130 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
     for (int nt = 0; nt < NT; ++nt) {
       const int col = col0 + 16 * nt + i16;
       if (!carried) S[i][nt] = (f32x4){0, 0, 0, 0};
-      else if (blk) S[i][nt] = blk[(8 * w + 4 * i + g) * kD + col];
+      else if (blk) S[i][nt] = blk[(8 * w + 2 * g + i) * kD + col];
       else
-        for (int r = 0; r < 4; ++r) S[i][nt][r] = dense[(32 * w + 16 * i + 4 * g + r) * kD + col];
+        for (int r = 0; r < 4; ++r) S[i][nt][r] = dense[(32 * w + 8 * g + 4 * i + r) * kD + col];
     }
 
   const int chunks = (len + kChunk - 1) / kChunk;
   const int place0 = first / kChunk + b;
-  auto load = [&](int c, ChunkIn<DELTA, NT> &in) {
+  auto load = [&](int c, ChunkIn<NT> &in) {
     const int nt = min(kChunk, len - c * kChunk);
     const size_t t0 = (size_t)first + (size_t)c * kChunk;
-    const int t = 16 * w + i16;
-    const size_t at = (t0 + (t < nt ? t : 0)) * row + (size_t)h * kD + 4 * g;
+    const int t = 16 * w + i16, tv = tid >> 2;
+    const size_t at = (t0 + (t < nt ? t : 0)) * row + (size_t)h * kD + 8 * g;
+    const size_t av = (t0 + (tv < nt ? tv : 0)) * row + (size_t)h * kD + col0 + 4 * (tid & 3);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      in.q[s].h[0] = *(const u32x2_a4 *)(P.q + at + 32 * s);
-      in.q[s].h[1] = *(const u32x2_a4 *)(P.q + at + 32 * s + 16);
-      in.k[s].h[0] = *(const u32x2_a4 *)(P.k + at + 32 * s);
-      in.k[s].h[1] = *(const u32x2_a4 *)(P.k + at + 32 * s + 16);
+      in.k[s].w = *(const u32x4_a4 *)(P.k + at + 32 * s);
+      in.q[s].w = *(const u32x4_a4 *)(P.q + at + 32 * s);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tv = 16 * w + 4 * g + r;
-      const uint16_t *src = P.v + (t0 + (tv < nt ? tv : 0)) * row + (size_t)h * kD + col0 + i16;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) in.v[n][r] = src[16 * n];
-    }
-    const float *ws = chunk_ws(P, place0 + c, h);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s > w >> 1) continue;
-      const float *f = ws + (size_t)(tri_frag(w) + s) * 512 + l * 8;
-      in.A[s][0] = *(const f32x4 *)f;
-      in.A[s][1] = *(const f32x4 *)(f + 4);
-      if (DELTA) {
-        in.T[s][0] = *(const f32x4 *)(f + kTriFloats);
-        in.T[s][1] = *(const f32x4 *)(f + kTriFloats + 4);
-      }
-    }
-    const float *dec = ws + 2 * kTriFloats;
+    for (int n = 0; n < NT; ++n) in.v[n] = *(const u32x2_a4 *)(P.v + av + 16 * n);
+    const float *dec = chunk_ws(P, place0 + c, h) + 2 * kTriFloats;
     in.from = *(const f32x4 *)(dec + 16 * w + 4 * g);
     in.to = *(const f32x4 *)(dec + kChunk + 16 * w + 4 * g);
     in.all = dec[kChunk - 1];
   };
+  auto load_tri = [&](int c, ChunkTri &tri) {
+    const float *ws = chunk_ws(P, place0 + c, h) + (size_t)tri_frag(w) * 512 + l * 4;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const float *f = ws + (s > w >> 1 ? 0 : s) * 512;   // a tile without a second fragment reads its first again
+      if (DELTA) {
+        tri.T[s][0] = *(const f32x4 *)(f + kTriFloats);
+        tri.T[s][1] = *(const f32x4 *)(f + kTriFloats + 256);
+      }
+      tri.A[s][0] = *(const f32x4 *)f;
+      tri.A[s][1] = *(const f32x4 *)(f + 256);
+    }
+  };
+  const int half = w & 1, step = w >> 1;
 
-  ChunkIn<DELTA, NT> in;
-  if (chunks > 0) load(0, in);
-  for (int c = 0; c < chunks; ++c) {
+  // K^T: lanes of two neighbouring tokens trade halves of each word
+  auto put_k = [&](const Frag *k) {
+    const int odd = l & 1, pos = 32 * step + 8 * (i16 >> 2) + 4 * half + (i16 & 2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t own = k[s].u[x];
+        const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+        const uint32_t word = odd ? __builtin_amdgcn_perm(own, other, 0x07060302u)
+                                  : __builtin_amdgcn_perm(other, own, 0x05040100u);
+        *(uint32_t *)&sK[32 * s + 8 * g + 2 * x + odd][pos] = word;
+      }
+  };
+
+  // one chunk; `next` is filled with the following one meanwhile (the last
+  // chunk with itself: a load that is always there keeps the waits exact)
+  auto chunk = [&](int c, ChunkIn<NT> &in, ChunkIn<NT> &next) {
+    ChunkTri tri;
+    load_tri(c, tri);
+    load(min(c + 1, chunks - 1), next);
     const int nt = min(kChunk, len - c * kChunk);
     const size_t t0 = (size_t)first + (size_t)c * kChunk;
-    {   // nothing of the rows behind the end
-      const bool out = 16 * w + i16 >= nt;
+    if (nt < kChunk) {   // nothing of the rows behind the end
+      if (16 * w + i16 >= nt)
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        if (out) in.q[s].w = in.k[s].w = (u32x4){0, 0, 0, 0};
+        for (int s = 0; s < 4; ++s) in.q[s].w = in.k[s].w = (u32x4){0, 0, 0, 0};
+      if (tid >> 2 >= nt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (16 * w + 4 * g + r >= nt) in.v[n][r] = 0;
+        for (int n = 0; n < NT; ++n) in.v[n] = (u32x2){0, 0};
     }
     // S as the B operand of contraction step w
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      uint32_t p[4][3];
-      split<3>(S[0][n][0], S[0][n][1], p[0]);
-      split<3>(S[0][n][2], S[0][n][3], p[1]);
-      split<3>(S[1][n][0], S[1][n][1], p[2]);
-      split<3>(S[1][n][2], S[1][n][3], p[3]);
+      Frag f[3];
+      split8<3>(S[0][n], S[1][n], f);
 #pragma unroll
-      for (int x = 0; x < 3; ++x) sS[x][w][n][l] = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
+      for (int x = 0; x < 3; ++x) sS[x][w][n][l] = f[x].w;
     }
-    // K^T: lanes of two neighbouring tokens trade halves of each word
-    {
-      const int t = 16 * w + i16, odd = t & 1;
-      const int pos = 32 * (w >> 1) + 8 * ((i16 >> 2)) + 4 * (w & 1) + (t & 2);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t own = in.k[s].u[x];
-          const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-          const uint32_t word = odd ? __builtin_amdgcn_perm(own, other, 0x07060302u)
-                                    : __builtin_amdgcn_perm(other, own, 0x05040100u);
-          const int d = 32 * s + 16 * (x >> 1) + 4 * g + 2 * (x & 1) + odd;
-          *(uint32_t *)&sK[d][pos] = word;
-        }
-    }
-    float v[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[n][r] = __uint_as_float((uint32_t)in.v[n][r] << 16);
-    const int half = w & 1, step = w >> 1;
-    if (!DELTA) {   // U = V is known: exact in one part
+      for (int x = 0; x < 4; ++x)
+        sV[16 * n + 4 * (tid & 3) + x][tid >> 2] = (uint16_t)(in.v[n][x >> 1] >> (16 * (x & 1)));
+    lds_barrier();   // S and V are there; every wave is done with the last chunk's K^T, U and D
+
+    f32x4 v[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        ((Frag *)&sU[0][step][n][l])->h[half] = (u32x2){pack_bf16(v[n][0], v[n][1]), pack_bf16(v[n][2], v[n][3])};
-        uint32_t p[2][3];
-        split<3>(v[n][0] * in.to[0], v[n][1] * in.to[1], p[0]);
-        split<3>(v[n][2] * in.to[2], v[n][3] * in.to[3], p[1]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) ((Frag *)&sD[x][step][n][l])->h[half] = (u32x2){p[0][x], p[1][x]};
+    for (int n = 0; n < NT; ++n) {
+      const u32x2 y = *(const u32x2 *)&sV[16 * n + i16][16 * w + 4 * g];
+      v[n] = (f32x4){lo_f32(y[0]), hi_f32(y[0]), lo_f32(y[1]), hi_f32(y[1])};
+      if (!DELTA) {   // U = V is known: exact in one part
+        ((Frag *)&sU[0][step][n][l])->h[half] = y;
+        put4<3>(v[n] * in.to, &sD[0][step][n][l], 2 * NT * 64, half);
       }
     }
-    __syncthreads();
-
     // rows of tile w: Q S, and K S for DELTA
-    f32x4 o[NT], r0[NT];
+    f32x4 o[NT], r[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n] = r0[n] = (f32x4){0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n) o[n] = r[n] = (f32x4){0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 2; x >= 0; --x) {
+        for (int x = DELTA ? 2 : 1; x >= 0; --x) {
           Frag f;
           f.w = sS[x][s][n][l];
-          if (DELTA) r0[n] = mma(in.k[s], f, r0[n]);
+          if (DELTA) r[n] = mma(in.k[s], f, r[n]);
           if (x < 2) o[n] = mma(in.q[s], f, o[n]);
         }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) o[n] *= in.from;
     if (DELTA) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float r[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) r[x] = __builtin_fmaf(-in.from[x], r0[n][x], v[n][x]);
-        uint32_t p[2][3];
-        split<3>(r[0], r[1], p[0]);
-        split<3>(r[2], r[3], p[1]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) ((Frag *)&sR[x][step][n][l])->h[half] = (u32x2){p[0][x], p[1][x]};
+        for (int x = 0; x < 4; ++x) r[n][x] = __builtin_fmaf(-in.from[x], r[n][x], v[n][x]);
+        put4<3>(r[n], &sR[0][step][n][l], 2 * NT * 64, half);
       }
-      __syncthreads();
+    }
+    put_k(in.k);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n] *= in.from;
+    lds_barrier();
+    if (DELTA) {
       // U = T R
       f32x4 u[NT];
 #pragma unroll
@@ -375,14 +390,8 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s > step) continue;
-        uint32_t p[4][3];
-        split<3>(in.T[s][0][0], in.T[s][0][1], p[0]);
-        split<3>(in.T[s][0][2], in.T[s][0][3], p[1]);
-        split<3>(in.T[s][1][0], in.T[s][1][1], p[2]);
-        split<3>(in.T[s][1][2], in.T[s][1][3], p[3]);
         Frag a[3];
-#pragma unroll
-        for (int x = 0; x < 3; ++x) a[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
+        split8<3>(tri.T[s][0], tri.T[s][1], a);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -395,31 +404,37 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint32_t p[2][3];
-        split<2>(u[n][0], u[n][1], p[0]);
-        split<2>(u[n][2], u[n][3], p[1]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) ((Frag *)&sU[x][step][n][l])->h[half] = (u32x2){p[0][x], p[1][x]};
-        u[n] *= in.to;
-        split<3>(u[n][0], u[n][1], p[0]);
-        split<3>(u[n][2], u[n][3], p[1]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) ((Frag *)&sD[x][step][n][l])->h[half] = (u32x2){p[0][x], p[1][x]};
+        put4<2>(u[n], &sU[0][step][n][l], 2 * NT * 64, half);
+        put4<3>(u[n] * in.to, &sD[0][step][n][l], 2 * NT * 64, half);
       }
-      __syncthreads();
+      lds_barrier();
     }
+    // S = 2^g_63 S + K^T D
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) S[i][n] *= in.all;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        Frag a;
+        a.w = *(const u32x4 *)&sK[32 * w + 8 * (i16 >> 2) + 4 * i + (i16 & 3)][32 * s + 8 * g];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 2; x >= 0; --x) {
+            Frag f;
+            f.w = sD[x][s][n][l];
+            S[i][n] = mma(a, f, S[i][n]);
+          }
+      }
     // O += A U
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (s > step) continue;
-      uint32_t p[4][2];
-      split<2>(in.A[s][0][0], in.A[s][0][1], p[0]);
-      split<2>(in.A[s][0][2], in.A[s][0][3], p[1]);
-      split<2>(in.A[s][1][0], in.A[s][1][1], p[2]);
-      split<2>(in.A[s][1][2], in.A[s][1][3], p[3]);
       Frag a[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) a[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
+      split8<2>(tri.A[s][0], tri.A[s][1], a);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         Frag f;
@@ -432,40 +447,27 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
         o[n] = mma(a[0], f, o[n]);
       }
     }
+    // lanes of two neighbouring columns trade rows: two columns of a row a store
+    const int odd = l & 1;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * w + 4 * g + r;
-      if (t < nt) {
-        uint16_t *dst = P.o + (t0 + t) * row + (size_t)h * kD + col0 + i16;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) dst[16 * n] = (uint16_t)pack_bf16(o[n][r], 0.0f);
-      }
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t lo = pack_bf16(o[n][0], o[n][1]), hi = pack_bf16(o[n][2], o[n][3]);
+      const uint32_t own = odd ? hi : lo, give = odd ? lo : hi;
+      const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+      // rows 4 g + 2 odd, + 1 of columns i16 & ~1, + 1
+      const uint32_t a = odd ? got : own, d = odd ? own : got;
+      const uint32_t r0 = __builtin_amdgcn_perm(d, a, 0x05040100u), r1 = __builtin_amdgcn_perm(d, a, 0x07060302u);
+      const int t = 16 * w + 4 * g + 2 * odd;
+      uint16_t *dst = P.o + (t0 + t) * row + (size_t)h * kD + col0 + 16 * n + (i16 & 14);
+      if (t < nt) *(uint32_t *)dst = r0;
+      if (t + 1 < nt) *(uint32_t *)(dst + row) = r1;
     }
-    const float all = in.all;
-    if (c + 1 < chunks) load(c + 1, in);
-    // S = 2^g_63 S + K^T D
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) S[i][n] *= all;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        Frag a;
-        a.w = *(const u32x4 *)&sK[32 * w + 16 * i + i16][32 * s + 8 * g];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int x = 2; x >= 0; --x) {
-            Frag f;
-            f.w = sD[x][s][n][l];
-            S[i][n] = mma(a, f, S[i][n]);
-          }
-      }
-    // the next chunk writes sS, sK (and sU, sD for SUM) before its first
-    // barrier: every wave has to be done with them
-    __syncthreads();
+  };
+  ChunkIn<NT> even, odd;
+  if (chunks > 0) load(0, even);
+  for (int c = 0; c < chunks; c += 2) {
+    chunk(c, even, odd);
+    if (c + 1 < chunks) chunk(c + 1, odd, even);
   }
 
   if (carried && len == 0) return;   // the slot stays as it is
@@ -474,9 +476,9 @@ __global__ void __launch_bounds__(256, 2) k_prompt_scan(PromptArgs P) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int col = col0 + 16 * n + i16;
-      if (blk) blk[(8 * w + 4 * i + g) * kD + col] = S[i][n];
+      if (blk) blk[(8 * w + 2 * g + i) * kD + col] = S[i][n];
       else
-        for (int r = 0; r < 4; ++r) dense[(32 * w + 16 * i + 4 * g + r) * kD + col] = S[i][n][r];
+        for (int r = 0; r < 4; ++r) dense[(32 * w + 8 * g + 4 * i + r) * kD + col] = S[i][n][r];
     }
 }
 

@@ -66,6 +66,7 @@ MIXER_EXPORTS = ["qdr_prompt_workspace", "qdr_prompt", "qdr_linear_step", "qdr_l
                  "qdr_kv_attend", "qdr_kv_poll_device_error"]
 
 _lib = None
+_raw_stream = None
 
 
 def load():
@@ -78,7 +79,7 @@ def load():
     # torch's HIP runtime must be the process's HIP runtime: importing torch
     # first makes libqdr.so bind to the already loaded libamdhip64.so.7
     # instead of loading a second runtime instance.
-    import torch  # noqa: F401
+    import torch
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     sig = {
@@ -113,6 +114,9 @@ def load():
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    # the current stream's handle without building a Stream object (4 us a call)
+    global _raw_stream
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     L.qdr_last_error.argtypes = []
     L.qdr_last_error.restype = ctypes.c_char_p
     _lib = L
@@ -125,9 +129,12 @@ def _check(fn, status):
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch._C._cuda_getDevice())
 
 
 def _dptr(t, dtype, name, numel=None):
@@ -140,7 +147,7 @@ def _dptr(t, dtype, name, numel=None):
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _shape(t, shape, name):

@@ -240,7 +240,7 @@ static int plans() {
             CHECK(p.few_parts * p.few_heads >= group && (p.few_parts - 1) * p.few_heads < group);
             CHECK(p.many_parts * p.many_heads >= group && (p.many_parts - 1) * p.many_heads < group);
             // one launch only: it takes every sequence; two: they share them out
-            CHECK((p.few ? p.few_tiles >= T / p.few_tokens + n : p.few_tiles == 0));
+            CHECK(p.few_tiles == (!p.few ? 0 : p.many ? n : T / p.few_tokens + n));
             CHECK((p.many ? p.many_tiles >= T / p.many_tokens + n : p.many_tiles == 0));
             CHECK(p.few_splits >= 1 && p.few_splits <= 64 && p.many_splits >= 1 && p.many_splits <= 64);
             const size_t few = (size_t)p.few_tiles * heads * p.few_parts * p.few_splits * 16 * 130;
