@@ -189,332 +189,233 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
 #pragma unroll
   for (int x = 0; x < P; ++x) f[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
 }
-// Four values, each part to its place in a B operand of rows: part x at to + x * stride.
-template <int P>
-__device__ __forceinline__ void put4(f32x4 a, u32x4 *to, int stride, int half) {
-  uint32_t p[2][P];
-  split<P>(a[0], a[1], p[0]);
-  split<P>(a[2], a[3], p[1]);
-#pragma unroll
-  for (int x = 0; x < P; ++x) ((Frag *)(to + x * stride))->h[half] = (u32x2){p[0][x], p[1][x]};
-}
 
-// What the scan's waves share of a chunk (operands, 1 KiB each).
-template <bool DELTA, int NT>
-struct ScanShared {
-  u32x4 S[3][4][NT][64];                                    // S, three parts
-  u32x4 R[DELTA ? 3 : 1][DELTA ? 2 : 1][NT][64];            // V - 2^g K S
-  u32x4 U[DELTA ? 2 : 1][2][NT][64];                        // U
-  u32x4 D[3][2][NT][64];                                    // 2^(g_63 - g) U
-  uint16_t K[kD][72];                                       // K^T; a row's tokens in operand order
-  uint16_t V[DELTA ? 16 * NT : 1][DELTA ? 68 : 8];          // V^T
+// What a chunk shares with every column: its left operands, 1 KiB each
+// ([lane] of 16 bytes), its values and its decays.
+template <bool DELTA>
+struct Stage {
+  u32x4 Q[4][4][64];                          // [token tile][channels 32 s + 8 g ..]
+  u32x4 K[DELTA ? 4 : 1][4][64];
+  u32x4 Kt[8][2][64];                         // K^T: [tile of S][tokens 32 s + {4 g.., 16 + 4 g..}]
+  u32x4 A[kTriFrags][2][64];                  // two parts
+  u32x4 T[DELTA ? kTriFrags : 1][3][64];      // three
+  uint16_t V[kChunk][136];
+  float dec[2 * kChunk];                      // decays from the chunk's start, then to its end
 };
 
-// Where a (sequence, head) is.
+// A thread's share of it, on the way there.
+template <bool DELTA>
+struct StageIn {
+  u32x4 q[2], k[2], v[2];     // row 16 (wave & 3) + i16, channels 64 (wave >> 2) + 32 x + 8 g ..
+  f32x4 tri[DELTA ? 3 : 2];   // four values of A or T
+  float dec;
+};
+
 struct ScanAt {
-  int first, len, chunks, place0, h, col0;
+  int first, len, chunks, place0, h;
   size_t row;
 };
 
-// Rows of a 64-row operand: tile w, channels 32 s + 8 g .. of row 16 w + i16.
-__device__ __forceinline__ void load_rows(const uint16_t *x, const ScanAt &A, int c, int w, int l, Frag *f) {
-  const int nt = min(kChunk, A.len - c * kChunk), t = 16 * w + (l & 15);
-  const uint16_t *src = x + ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 8 * (l >> 4);
+template <bool DELTA>
+__device__ __forceinline__ void fetch(const PromptArgs &P, const ScanAt &A, int c, int wave, int l, StageIn<DELTA> &in) {
+  const int nt = min(kChunk, A.len - c * kChunk), t = 16 * (wave & 3) + (l & 15);
+  const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 64 * (wave >> 2) + 8 * (l >> 4);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) f[s].w = *(const u32x4_a4 *)(src + 32 * s);
-}
-__device__ __forceinline__ void clear_rows(const ScanAt &A, int c, int w, int l, Frag *f) {
-  const int nt = A.len - c * kChunk;
-  if (nt < kChunk && 16 * w + (l & 15) >= nt)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) f[s].w = (u32x4){0, 0, 0, 0};
-}
-// Rows of tile w of a triangular matrix, [fragment][half]; a tile without a
-// second fragment reads its first again.
-__device__ __forceinline__ void load_tri(const float *m, int w, int l, f32x4 (*t)[2]) {
-  const float *f = m + (size_t)tri_frag(w) * 512 + l * 4;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    t[s][0] = *(const f32x4 *)(f + (s > w >> 1 ? 0 : s) * 512);
-    t[s][1] = *(const f32x4 *)(f + (s > w >> 1 ? 0 : s) * 512 + 256);
+  for (int x = 0; x < 2; ++x) {
+    in.k[x] = *(const u32x4_a4 *)(P.k + at + 32 * x);
+    in.q[x] = *(const u32x4_a4 *)(P.q + at + 32 * x);
+    in.v[x] = *(const u32x4_a4 *)(P.v + at + 32 * x);
   }
+  const float *ws = chunk_ws(P, A.place0 + c, A.h);
+  // groups of 256 values: A's 12, then T's
+#pragma unroll
+  for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
+    const int group = wave + 8 * x;
+    in.tri[x] = *(const f32x4 *)(ws + (DELTA || group < 2 * kTriFrags ? group : wave) * 256 + l * 4);
+  }
+  in.dec = ws[2 * kTriFloats + ((wave & 1) * 64 + l)];
 }
 
-// Waves 0 .. 3: the chain from state to state.  What they read of a chunk is
-// asked for a whole chunk ahead.
-template <bool DELTA, int NT>
-struct ChainIn {
-  Frag k[4];
-  u32x2 v[NT];                // columns 4 (tid & 3) .. of tile n, row tid / 4
-  f32x4 T[2][2];
-  f32x4 from, to;             // DELTA: decays from the chunk's start, to its end (rows 4 g .. of tile w)
-  float end;                  // SUM: to its end, of row tid / 4
-  float all;                  // over the whole chunk
-};
-
-template <bool DELTA, int NT>
-__device__ __forceinline__ void load_chain(const PromptArgs &P, const ScanAt &A, int c, int w, int tid, ChainIn<DELTA, NT> &in) {
-  const int l = tid & 63, g = l >> 4, tv = tid >> 2, nt = min(kChunk, A.len - c * kChunk);
-  load_rows(P.k, A, c, w, l, in.k);
-  const uint16_t *v = P.v + ((size_t)A.first + (size_t)c * kChunk + (tv < nt ? tv : 0)) * A.row + (size_t)A.h * kD + A.col0 + 4 * (tid & 3);
+template <bool DELTA>
+__device__ __forceinline__ void put(const ScanAt &A, int c, int wave, int l, StageIn<DELTA> &in, Stage<DELTA> &st) {
+  const int g = l >> 4, i16 = l & 15, odd = l & 1, tile = wave & 3, t = 16 * tile + i16;
+  if (A.len - c * kChunk <= t)   // nothing of the rows behind the end
 #pragma unroll
-  for (int n = 0; n < NT; ++n) in.v[n] = *(const u32x2_a4 *)(v + 16 * n);
-  const float *ws = chunk_ws(P, A.place0 + c, A.h), *dec = ws + 2 * kTriFloats;
+    for (int x = 0; x < 2; ++x) in.q[x] = in.k[x] = in.v[x] = (u32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int s = 2 * (wave >> 2) + x;
+    st.Q[tile][s][l] = in.q[x];
+    if (DELTA) st.K[tile][s][l] = in.k[x];
+    *(u32x4 *)&st.V[t][32 * s + 8 * g] = in.v[x];
+    // K^T: lanes of two neighbouring tokens trade halves of each word.  Channel
+    // 32 s + 8 g + 4 i + r is row 4 g + r of tile 2 s + i; token 4 g' + r' of
+    // tile `tile` is value 4 (tile & 1) + r' of lane group g'
+    uint32_t *to = (uint32_t *)&st.Kt[2 * s][tile >> 1][16 * (i16 >> 2) + 4 * g + odd] + 2 * (tile & 1) + ((i16 & 2) >> 1);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const uint32_t own = in.k[x][y];
+      const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+      to[(y >> 1) * (2 * 64 * 4) + (y & 1) * 8] = odd ? __builtin_amdgcn_perm(own, other, 0x07060302u)
+                                                      : __builtin_amdgcn_perm(other, own, 0x05040100u);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
+    const int group = wave + 8 * x;
+    uint32_t p[2][3];
+    if (group < 2 * kTriFrags) {
+      split<2>(in.tri[x][0], in.tri[x][1], p[0]);
+      split<2>(in.tri[x][2], in.tri[x][3], p[1]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) ((Frag *)&st.A[group >> 1][y][l])->h[group & 1] = (u32x2){p[0][y], p[1][y]};
+    } else if (DELTA) {
+      const int f = group - 2 * kTriFrags;
+      split<3>(in.tri[x][0], in.tri[x][1], p[0]);
+      split<3>(in.tri[x][2], in.tri[x][3], p[1]);
+#pragma unroll
+      for (int y = 0; y < 3; ++y) ((Frag *)&st.T[f >> 1][y][l])->h[f & 1] = (u32x2){p[0][y], p[1][y]};
+    }
+  }
+  if (wave < 2) st.dec[wave * 64 + l] = in.dec;
+}
+
+// One wave, sixteen columns, one chunk.  Products of S, R and U take their
+// right operands from the accumulators of the product before: nothing but the
+// shared left operands is read from LDS, and nothing waits for another wave.
+template <bool DELTA>
+__device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, int c, int col0, int l, const Stage<DELTA> &st, f32x4 *S) {
+  const int g = l >> 4, i16 = l & 15;
+  Frag f[4][3];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) split8<3>(S[2 * s], S[2 * s + 1], f[s]);
+  f32x4 o[4], r[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] = r[t] = (f32x4){0, 0, 0, 0};
+  // (products of one accumulator never follow each other: four at a time)
   if (DELTA) {
-    load_tri(ws + kTriFloats, w, l, in.T);
-    in.from = *(const f32x4 *)(dec + 16 * w + 4 * g);
-    in.to = *(const f32x4 *)(dec + kChunk + 16 * w + 4 * g);
-  } else {
-    in.end = dec[kChunk + tv];
-  }
-  in.all = dec[kChunk - 1];
-}
-
-// K^T: lanes of two neighbouring tokens trade halves of each word.
-__device__ __forceinline__ void put_k(const Frag *k, uint16_t (*K)[72], int w, int l) {
-  const int g = l >> 4, i16 = l & 15, odd = l & 1;
-  const int pos = 32 * (w >> 1) + 8 * (i16 >> 2) + 4 * (w & 1) + (i16 & 2);
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; ++s) {
+      Frag k[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) k[t].w = st.K[DELTA ? t : 0][s][l];
+#pragma unroll
+      for (int x = 2; x >= 0; --x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[s][x], r[t]);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    Frag q[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) q[t].w = st.Q[t][s][l];
+#pragma unroll
+    for (int x = 1; x >= 0; --x)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f[s][x], o[t]);
+  }
+  f32x4 u[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const f32x4 from = *(const f32x4 *)&st.dec[16 * t + 4 * g];
+    o[t] *= from;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const uint32_t own = k[s].u[x];
-      const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-      const uint32_t word = odd ? __builtin_amdgcn_perm(own, other, 0x07060302u)
-                                : __builtin_amdgcn_perm(other, own, 0x05040100u);
-      *(uint32_t *)&K[32 * s + 8 * g + 2 * x + odd][pos] = word;
+      const float v = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][col0 + i16] << 16);
+      if (DELTA) r[t][x] = __builtin_fmaf(-from[x], r[t][x], v);
+      else u[t][x] = v;
     }
-}
-
-// S as the B operand of contraction step w.
-template <bool DELTA, int NT>
-__device__ __forceinline__ void put_state(const f32x4 (*S)[NT], ScanShared<DELTA, NT> &sh, int w, int l) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    Frag f[3];
-    split8<3>(S[0][n], S[1][n], f);
-#pragma unroll
-    for (int x = 0; x < 3; ++x) sh.S[x][w][n][l] = f[x].w;
   }
-}
-
-// S = 2^g_63 S + K^T D.
-template <bool DELTA, int NT>
-__device__ __forceinline__ void update_state(f32x4 (*S)[NT], float all, const ScanShared<DELTA, NT> &sh, int w, int l) {
-  const int g = l >> 4, i16 = l & 15;
+  if (DELTA) {   // U = T R
+    Frag R[2][3];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int s = 0; s < 2; ++s) split8<3>(r[2 * s], r[2 * s + 1], R[s]);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) S[i][n] *= all;
+    for (int t = 0; t < 4; ++t) u[t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int x = 2; x >= 0; --x) {
+        Frag a[4];
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) a[t].w = st.T[DELTA ? tri_frag(t) + s : 0][x][l];
+#pragma unroll
+        for (int y = 2 - x; y >= 0; --y)
+#pragma unroll
+          for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[s][y], u[t]);
+      }
+  }
+  // S = 2^g_63 S + K^T diag(2^(g_63 - g)) U
+  const float all = st.dec[kChunk - 1];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) S[m] *= all;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    Frag a[2];
+    Frag d[3];
+    split8<3>(u[2 * s] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 4 * g], u[2 * s + 1] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 16 + 4 * g], d);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      a[i].w = *(const u32x4 *)&sh.K[32 * w + 8 * (i16 >> 2) + 4 * i + (i16 & 3)][32 * s + 8 * g];
+    for (int half = 0; half < 8; half += 4) {
+      Frag k[4];
 #pragma unroll
-    for (int x = 2; x >= 0; --x)
+      for (int m = 0; m < 4; ++m) k[m].w = st.Kt[half + m][s][l];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        Frag f;
-        f.w = sh.D[x][s][n][l];
+      for (int x = 2; x >= 0; --x)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) S[i][n] = mma(a[i], f, S[i][n]);
-      }
-  }
-}
-
-// DELTA's chain over one chunk; three barriers.
-template <int NT>
-__device__ __forceinline__ void chain_delta(const ScanAt &A, int c, int w, int tid, ChainIn<true, NT> &in, f32x4 (*S)[NT], ScanShared<true, NT> &sh) {
-  const int l = tid & 63, g = l >> 4, i16 = l & 15, half = w & 1, step = w >> 1;
-  clear_rows(A, c, w, l, in.k);
-  if (A.len - c * kChunk <= tid >> 2)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) in.v[n] = (u32x2){0, 0};
-  put_state<true, NT>(S, sh, w, l);
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      sh.V[16 * n + 4 * (tid & 3) + x][tid >> 2] = (uint16_t)(in.v[n][x >> 1] >> (16 * (x & 1)));
-  lds_barrier();
-  f32x4 r[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) r[n] = (f32x4){0, 0, 0, 0};
-#pragma unroll
-  for (int x = 2; x >= 0; --x)
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        Frag f;
-        f.w = sh.S[x][s][n][l];
-        r[n] = mma(in.k[s], f, r[n]);
-      }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const u32x2 y = *(const u32x2 *)&sh.V[16 * n + i16][16 * w + 4 * g];
-    const f32x4 v = {lo_f32(y[0]), hi_f32(y[0]), lo_f32(y[1]), hi_f32(y[1])};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) r[n][x] = __builtin_fmaf(-in.from[x], r[n][x], v[x]);
-    put4<3>(r[n], &sh.R[0][step][n][l], 2 * NT * 64, half);
-  }
-  Frag T[2][3];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) split8<3>(in.T[s][0], in.T[s][1], T[s]);
-  lds_barrier();
-  // U = T R
-  f32x4 u[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) u[n] = (f32x4){0, 0, 0, 0};
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s > step) continue;
-#pragma unroll
-    for (int y = 2; y >= 0; --y)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        Frag f;
-        f.w = sh.R[y][s][n][l];
-#pragma unroll
-        for (int x = 2 - y; x >= 0; --x) u[n] = mma(T[s][x], f, u[n]);
-      }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    put4<3>(u[n] * in.to, &sh.D[0][step][n][l], 2 * NT * 64, half);
-    put4<2>(u[n], &sh.U[0][step][n][l], 2 * NT * 64, half);
-  }
-  put_k(in.k, sh.K, w, l);
-  lds_barrier();
-  update_state<true, NT>(S, in.all, sh, w, l);
-}
-
-// SUM's: U = V is there from the start and exact in one part; one barrier,
-// and the other half of the shared operands for the next chunk.
-template <int NT>
-__device__ __forceinline__ void chain_sum(const ScanAt &A, int c, int w, int tid, ChainIn<false, NT> &in, f32x4 (*S)[NT], ScanShared<false, NT> &sh) {
-  const int l = tid & 63;
-  clear_rows(A, c, w, l, in.k);
-  const int t = tid >> 2, e = 4 * ((t >> 4) & 1) + (t & 3);
-  const bool out = A.len - c * kChunk <= t;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint32_t y = out ? 0 : in.v[n][x];
-      uint32_t p[3];
-      split<3>(lo_f32(y) * in.end, hi_f32(y) * in.end, p);
-      const int lane = 16 * ((t >> 2) & 3) + 4 * (tid & 3) + 2 * x;
-      uint16_t *u = (uint16_t *)&sh.U[0][t >> 5][n][lane] + e;
-      u[0] = (uint16_t)y;
-      u[8] = (uint16_t)(y >> 16);
-#pragma unroll
-      for (int z = 0; z < 3; ++z) {
-        uint16_t *d = (uint16_t *)&sh.D[z][t >> 5][n][lane] + e;
-        d[0] = (uint16_t)p[z];
-        d[8] = (uint16_t)(p[z] >> 16);
-      }
+        for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
     }
-  put_k(in.k, sh.K, w, l);
-  put_state<false, NT>(S, sh, w, l);
-  lds_barrier();
-  update_state<false, NT>(S, in.all, sh, w, l);
-}
-
-// Waves 4 .. 7: the readout, rows of tile w.
-struct ReadIn {
-  Frag q[4];
-  f32x4 A[2][2], from;
-};
-
-__device__ __forceinline__ void load_read(const PromptArgs &P, const ScanAt &A, int c, int w, int l, ReadIn &in) {
-  load_rows(P.q, A, c, w, l, in.q);
-  const float *ws = chunk_ws(P, A.place0 + c, A.h);
-  load_tri(ws, w, l, in.A);
-  in.from = *(const f32x4 *)(ws + 2 * kTriFloats + 16 * w + 4 * (l >> 4));
-}
-
-template <bool DELTA, int NT>
-__device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A, int c, int w, int l, ReadIn &in, const ScanShared<DELTA, NT> &sh) {
-  const int g = l >> 4, i16 = l & 15, step = w >> 1;
-  f32x4 o[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) o[n] = (f32x4){0, 0, 0, 0};
-  clear_rows(A, c, w, l, in.q);
-  lds_barrier();
-#pragma unroll
-  for (int x = 1; x >= 0; --x)
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        Frag f;
-        f.w = sh.S[x][s][n][l];
-        o[n] = mma(in.q[s], f, o[n]);
-      }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) o[n] *= in.from;
-  Frag a[2][2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) split8<2>(in.A[s][0], in.A[s][1], a[s]);
-  if (DELTA) {
-    lds_barrier();
-    lds_barrier();
   }
+  // O += A U
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    if (s > step) continue;
+    Frag U[2];
+    split8<2>(u[2 * s], u[2 * s + 1], U);   // SUM: V, exact in the first
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      Frag f;
-      if (DELTA) {
-        f.w = sh.U[DELTA ? 1 : 0][s][n][l];
-        o[n] = mma(a[s][0], f, o[n]);
-      }
-      f.w = sh.U[0][s][n][l];
-      o[n] = mma(a[s][1], f, o[n]);
-      o[n] = mma(a[s][0], f, o[n]);
+    for (int x = 1; x >= 0; --x) {
+      Frag a[4];
+#pragma unroll
+      for (int t = 2 * s; t < 4; ++t) a[t].w = st.A[tri_frag(t) + s][x][l];
+#pragma unroll
+      for (int y = DELTA ? 1 - x : 0; y >= 0; --y)
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) o[t] = mma(a[t], U[y], o[t]);
     }
   }
   // lanes of two neighbouring columns trade rows: two columns of a row a store
   const int nt = min(kChunk, A.len - c * kChunk), odd = l & 1;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const uint32_t lo = pack_bf16(o[n][0], o[n][1]), hi = pack_bf16(o[n][2], o[n][3]);
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t lo = pack_bf16(o[t][0], o[t][1]), hi = pack_bf16(o[t][2], o[t][3]);
     const uint32_t own = odd ? hi : lo, give = odd ? lo : hi;
     const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
     // rows 4 g + 2 odd, + 1 of columns i16 & 14, + 1
     const uint32_t x = odd ? got : own, y = odd ? own : got;
     const uint32_t r0 = __builtin_amdgcn_perm(y, x, 0x05040100u), r1 = __builtin_amdgcn_perm(y, x, 0x07060302u);
-    const int t = 16 * w + 4 * g + 2 * odd;
-    uint16_t *dst = P.o + ((size_t)A.first + (size_t)c * kChunk + t) * A.row + (size_t)A.h * kD + A.col0 + 16 * n + (i16 & 14);
-    if (t < nt) *(uint32_t *)dst = r0;
-    if (t + 1 < nt) *(uint32_t *)(dst + A.row) = r1;
+    const int at = 16 * t + 4 * g + 2 * odd;
+    uint16_t *dst = P.o + ((size_t)A.first + (size_t)c * kChunk + at) * A.row + (size_t)A.h * kD + col0 + (i16 & 14);
+    if (at < nt) *(uint32_t *)dst = r0;
+    if (at + 1 < nt) *(uint32_t *)(dst + A.row) = r1;
   }
 }
 
-// The chunks in order.  Four waves carry the state from chunk to chunk and
-// four read it out beside them: the chain is what the time of a long prompt
-// is made of, and everything that it does not need is off it.
-template <bool DELTA, int NT>
+// The chunks in order: eight waves stage a chunk (asked for a chunk ahead),
+// the first NW of them take sixteen columns each through it.
+template <bool DELTA, int NW>
 __global__ void __launch_bounds__(512, 2) k_prompt_scan(PromptArgs P) {
-  constexpr int kSlices = 8 / NT;
-  __shared__ __attribute__((aligned(16))) ScanShared<DELTA, NT> shared[DELTA ? 1 : 2];
+  constexpr int kSlices = 8 / NW;
+  __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
 
   // the slices of one (sequence, head) go to one XCD (workgroups are dealt to
   // the eight in turn): they share its q, k, A and T through one L2
   const int bh = (blockIdx.x / (8 * kSlices)) * 8 + blockIdx.x % 8;
   if (bh >= P.n * P.H) return;
   const int b = bh / P.H;
-  const int tid = threadIdx.x & 255, l = tid & 63, g = l >> 4, i16 = l & 15;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool chain = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0;
+  const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slice = (blockIdx.x / 8) % kSlices, col0 = 16 * (slice * NW + wave);
 
   ScanAt A;
   A.h = bh % P.H;
-  A.col0 = (blockIdx.x / 8) % kSlices * 16 * NT;
   A.row = (size_t)P.H * kD;
   if (!rows_of(P.cu, P.T, b, &A.first, &A.len)) {
     if (threadIdx.x == 0) atomicOr(P.err, kErrLength);
@@ -523,72 +424,49 @@ __global__ void __launch_bounds__(512, 2) k_prompt_scan(PromptArgs P) {
   const int slot = P.slots[b];
   if (slot < 0 || slot >= P.num_slots) {
     if (slot != -1 && threadIdx.x == 0) atomicOr(P.err, kErrSlot);
-    for (size_t i = threadIdx.x; i < (size_t)A.len * (16 * NT); i += 512)
-      P.o[((size_t)A.first + i / (16 * NT)) * A.row + (size_t)A.h * kD + A.col0 + i % (16 * NT)] = 0;
+    for (size_t i = threadIdx.x; i < (size_t)A.len * (16 * NW); i += 512)
+      P.o[((size_t)A.first + i / (16 * NW)) * A.row + (size_t)A.h * kD + slice * 16 * NW + i % (16 * NW)] = 0;
     return;
   }
   A.chunks = (A.len + kChunk - 1) / kChunk;
   A.place0 = A.first / kChunk + b;
 
-  // A chunk's loads are always there (the last chunk asks for itself again):
-  // waits count the loads issued behind the ones they need.
-  if (!chain) {
-    if (A.chunks == 0) return;
-    ReadIn even, odd;
-    load_read(P, A, 0, w, l, even);
-    for (int c = 0; c < A.chunks; c += 2) {
-      load_read(P, A, min(c + 1, A.chunks - 1), w, l, odd);
-      read_chunk<DELTA, NT>(P, A, c, w, l, even, shared[0]);
-      if (c + 1 >= A.chunks) break;
-      load_read(P, A, min(c + 2, A.chunks - 1), w, l, even);
-      read_chunk<DELTA, NT>(P, A, c + 1, w, l, odd, shared[DELTA ? 0 : 1]);
-    }
-    return;
-  }
-
-  // S: wave w holds rows 32 w .. 32 w + 31; row 4 g + r of result i is row
-  // 32 w + 8 g + 4 i + r, so that a lane's two results are eight rows in a
-  // row: the channels that one 16-byte load of q or k has
+  // S: row 4 g + r of result 2 s + i is row 32 s + 8 g + 4 i + r, so that the
+  // two results of a contraction step are, in a lane, eight rows in a row: the
+  // channels that one 16-byte load of q or k has
   const bool carried = P.carry != nullptr && P.carry[b] != 0;
-  f32x4 S[2][NT];
   f32x4 *blk = P.pool ? (f32x4 *)(P.pool + (size_t)slot * P.slot_stride + (size_t)A.h * (kD * kD * 4)) : nullptr;
   float *dense = P.S + (size_t)bh * kD * kD;
+  const int col = col0 + i16;
+  f32x4 S[8];
+  if (wave < NW)
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int col = A.col0 + 16 * nt + i16;
-      if (!carried) S[i][nt] = (f32x4){0, 0, 0, 0};
-      else if (blk) S[i][nt] = blk[(8 * w + 2 * g + i) * kD + col];
+    for (int m = 0; m < 8; ++m) {
+      const int row = 32 * (m >> 1) + 8 * g + 4 * (m & 1);
+      if (!carried) S[m] = (f32x4){0, 0, 0, 0};
+      else if (blk) S[m] = blk[(row >> 2) * kD + col];
       else
-        for (int r = 0; r < 4; ++r) S[i][nt][r] = dense[(32 * w + 8 * g + 4 * i + r) * kD + col];
+        for (int r = 0; r < 4; ++r) S[m][r] = dense[(row + r) * kD + col];
     }
-  auto step = [&](int c, ChainIn<DELTA, NT> &in, ScanShared<DELTA, NT> &sh) {
-    if constexpr (DELTA) chain_delta<NT>(A, c, w, tid, in, S, sh);
-    else chain_sum<NT>(A, c, w, tid, in, S, sh);
-  };
-  if (A.chunks > 0) {
-    ChainIn<DELTA, NT> even, odd;
-    load_chain<DELTA, NT>(P, A, 0, w, tid, even);
-    for (int c = 0; c < A.chunks; c += 2) {
-      load_chain<DELTA, NT>(P, A, min(c + 1, A.chunks - 1), w, tid, odd);
-      step(c, even, shared[0]);
-      if (c + 1 >= A.chunks) break;
-      load_chain<DELTA, NT>(P, A, min(c + 2, A.chunks - 1), w, tid, even);
-      step(c + 1, odd, shared[DELTA ? 0 : 1]);
-    }
+
+  StageIn<DELTA> in;
+  if (A.chunks > 0) fetch<DELTA>(P, A, 0, wave, l, in);
+  for (int c = 0; c < A.chunks; ++c) {
+    put<DELTA>(A, c, wave, l, in, st);
+    lds_barrier();
+    fetch<DELTA>(P, A, min(c + 1, A.chunks - 1), wave, l, in);   // always there: the waits stay exact
+    if (wave < NW) columns<DELTA>(P, A, c, col0, l, st, S);
+    lds_barrier();
   }
 
-  if (carried && A.len == 0) return;   // the slot stays as it is
+  if (wave >= NW || (carried && A.len == 0)) return;   // the slot stays as it is
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = A.col0 + 16 * n + i16;
-      if (blk) blk[(8 * w + 2 * g + i) * kD + col] = S[i][n];
-      else
-        for (int r = 0; r < 4; ++r) dense[(32 * w + 8 * g + 4 * i + r) * kD + col] = S[i][n][r];
-    }
+  for (int m = 0; m < 8; ++m) {
+    const int row = 32 * (m >> 1) + 8 * g + 4 * (m & 1);
+    if (blk) blk[(row >> 2) * kD + col] = S[m];
+    else
+      for (int r = 0; r < 4; ++r) dense[(row + r) * kD + col] = S[m][r];
+  }
 }
 
 // Slots whose states are unpacked before and packed after the scan.
@@ -604,11 +482,20 @@ __global__ void __launch_bounds__(256) k_prompt_slots(PromptArgs P) {
   P.slots_out[b] = ok && in_pool && !(carried && len == 0) ? slot : -1;
 }
 
-template <bool DELTA, int NT>
+template <bool DELTA, int NW>
 hipError_t scan(const PromptArgs &a, hipStream_t st) {
-  const int slices = 8 / NT, bh = (a.n * a.H + 7) / 8;
-  hipLaunchKernelGGL((k_prompt_scan<DELTA, NT>), dim3(bh * 8 * slices), dim3(512), 0, st, a);
+  const int slices = 8 / NW, bh = (a.n * a.H + 7) / 8;
+  hipLaunchKernelGGL((k_prompt_scan<DELTA, NW>), dim3(bh * 8 * slices), dim3(512), 0, st, a);
   return hipGetLastError();
+}
+
+template <bool DELTA>
+hipError_t scan(const PromptArgs &a, hipStream_t st) {
+  const int bh = a.n * a.H;
+  if (bh <= 32) return scan<DELTA, 1>(a, st);
+  if (bh <= 64) return scan<DELTA, 2>(a, st);
+  if (bh <= 128) return scan<DELTA, 4>(a, st);
+  return scan<DELTA, 8>(a, st);
 }
 
 }  // namespace
@@ -626,9 +513,7 @@ hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st)
 }
 
 hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
-  const bool narrow = (int64_t)a.n * a.H * 8 <= 256;
-  if (delta) return narrow ? scan<true, 1>(a, st) : scan<true, 2>(a, st);
-  return narrow ? scan<false, 1>(a, st) : scan<false, 2>(a, st);
+  return delta ? scan<true>(a, st) : scan<false>(a, st);
 }
 
 }  // namespace qdr
