@@ -30,6 +30,19 @@ __device__ __forceinline__ Frag widen(uint32_t a, uint32_t b) {
   return f;
 }
 
+// A lane's eight values of one channel (tokens 4 g + {0..3, 16..19} of a
+// block) with those from token `left` on cleared.
+__device__ __forceinline__ u32x4 keep_tokens(u32x4 v, int g, int left) {
+  Frag f;
+  f.w = v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool out = 4 * g + (e & 3) + 16 * (e >> 2) >= left;
+    if (out) f.u[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+  }
+  return f.w;
+}
+
 // The rows of a tile: `tokens` tokens from `token` on, times `heads` query
 // heads from `head` on; row r is token r / heads, head r % heads.
 struct Tile {
@@ -88,6 +101,7 @@ template <int KIND>
 struct FewIn {
   u32x4 k[KIND == 8 ? 4 : 8], v[KIND == 8 ? 4 : 8];
   f32x4 ks[2], vs[2];
+  bool good;
 };
 
 template <int KIND>
@@ -124,18 +138,17 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
   for (int d = 0; d < 8; ++d) o[d] = (f32x4){0, 0, 0, 0};
   float m = kNone, sum = 0.0f;
 
-  auto load = [&](int block, FewIn<KIND> &in) -> bool {
-    const uint8_t *blk = block_at(P, t.b, kvh, block, KIND == 8 ? kKv8Block : kKv16Block);
-    if (!blk) {
-      if (l == 0) atomicOr(P.err, kErrPage);
-      return false;
-    }
+  // A block's loads are always there: one behind the last, or of a bad page,
+  // is some block of the cache, and its keys are not looked at.
+  auto load = [&](int block, FewIn<KIND> &in) {
+    const uint8_t *blk = block_at(P, t.b, kvh, min(block, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+    in.good = blk != nullptr;
+    if (!blk) blk = P.base;
     constexpr int N = KIND == 8 ? 4 : 8;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      in.k[i] = *(const u32x4 *)(blk + (i * 64 + l) * 16);
-      in.v[i] = *(const u32x4 *)(blk + N * 1024 + (i * 64 + l) * 16);
-    }
+    for (int i = 0; i < N; ++i) in.k[i] = *(const u32x4 *)(blk + (i * 64 + l) * 16);
+#pragma unroll
+    for (int i = 0; i < N; ++i) in.v[i] = *(const u32x4 *)(blk + N * 1024 + (i * 64 + l) * 16);
     if (KIND == 8) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -143,32 +156,31 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
         in.vs[i] = *(const f32x4 *)(blk + kKv8Scale + 4 * kBlock + 64 * i + 16 * g);
       }
     }
-    return true;
   };
-
-  FewIn<KIND> in;
-  bool have = lo + w < hi && load(lo + w, in);
-  for (int block = lo + w; block < hi; block += 4) {
-    const FewIn<KIND> now = in;
-    const bool good = have;
-    have = block + 4 < hi && load(block + 4, in);
-    if (!good) continue;
+  auto take = [&](int block, FewIn<KIND> &in) {
+    if (!in.good) {
+      if (l == 0) atomicOr(P.err, kErrPage);
+      return;
+    }
     f32x4 s[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s[i] = (f32x4){0, 0, 0, 0};
+    for (int i = 0; i < 2; ++i) s[i] = (f32x4){0, 0, 0, 0};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         Frag k;
         if (KIND == 8) {
-          const u32x4 z = now.k[2 * i + (x >> 1)];
+          const u32x4 z = in.k[2 * i + (x >> 1)];
           k = (x & 1) ? widen(z[2], z[3]) : widen(z[0], z[1]);
         } else {
-          k.w = now.k[(4 * i + x) & (KIND == 8 ? 3 : 7)];
+          k.w = in.k[(4 * i + x) & (KIND == 8 ? 3 : 7)];
         }
         s[i] = mma(k, q[x], s[i]);
       }
-      if (KIND == 8) s[i] *= now.ks[i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (KIND == 8) s[i] *= in.ks[i];
       s[i] *= A.scale_log2;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -177,22 +189,25 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
     float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float m1 = fmaxf(m, top);
-    const float ref = m1 == kNone ? 0.0f : m1;      // no key seen yet: weights 2^(-inf) = 0
-    const float fade = ex2(m - ref);
-    m = m1;
+    if (__any(top > m)) {
+      const float m1 = fmaxf(m, top);
+      const float fade = ex2(m - (m1 == kNone ? 0.0f : m1));
+      m = m1;
+      sum *= fade;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] *= fade;
+    }
+    const float ref = m == kNone ? 0.0f : m;        // no key seen yet: weights 2^(-inf) = 0
     f32x4 p[2];
-    float add = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         p[i][r] = ex2(s[i][r] - ref);
-        add += p[i][r];
+        sum += p[i][r];
         // a masked key's scale is not looked at
-        if (KIND == 8) p[i][r] = s[i][r] == kNone ? 0.0f : p[i][r] * now.vs[i][r];
+        if (KIND == 8) p[i][r] = s[i][r] == kNone ? 0.0f : p[i][r] * in.vs[i][r];
       }
-    sum = __builtin_fmaf(sum, fade, add);
     Frag pf;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -201,23 +216,32 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
     }
     // values behind the last key of the tile may be anything: 0 times them is not 0
     const int left = t.keys - block * kBlock;
+    if (KIND == 16 && left < kBlock)
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+        in.v[d & (KIND == 8 ? 3 : 7)] = keep_tokens(in.v[d & (KIND == 8 ? 3 : 7)], g, left);
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
       Frag v;
       if (KIND == 8) {
-        const u32x4 z = now.v[d >> 1];
+        const u32x4 z = in.v[d >> 1];
         v = (d & 1) ? widen(z[2], z[3]) : widen(z[0], z[1]);
       } else {
-        v.w = now.v[d & (KIND == 8 ? 3 : 7)];
-        if (left < kBlock) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool out = 4 * g + (e & 3) + 16 * (e >> 2) >= left;
-            if (out) v.u[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-          }
-        }
+        v.w = in.v[d & (KIND == 8 ? 3 : 7)];
       }
-      o[d] = mma(v, pf, o[d] * fade);
+      o[d] = mma(v, pf, o[d]);
+    }
+  };
+
+  if (lo < hi) {
+    FewIn<KIND> even, odd;
+    load(lo + w, even);
+    for (int block = lo + w; block < hi; block += 8) {
+      load(block + 4, odd);
+      take(block, even);
+      if (block + 4 >= hi) break;
+      load(block + 8, even);
+      take(block + 4, odd);
     }
   }
   sum += __shfl_xor(sum, 16);
@@ -257,17 +281,37 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
   }
 }
 
-// ---- many rows: up to 128, 32 a wave; blocks of keys go through LDS
+// ---- many rows: up to 128, 32 a wave; two blocks of keys at a time through
+// LDS, two pairs of them in turn, the next pair on its way in registers.
+// What the vector units do for a score is what counts beside the products:
+// the scale rides on the subtraction of the maximum, masks are only looked at
+// where a wave's rows end, and the maximum that the weights are taken from
+// moves (and with it the accumulators) only when a score exceeds it by 2^8.
+constexpr float kSlack = 8.0f;
+
+template <int KIND>
+struct ManyIn {
+  u32x4 k[KIND == 8 ? 2 : 4], v[KIND == 8 ? 2 : 4];
+  float scale;        // 8-bit: of the keys, then of the values
+  int left[2];        // tokens of the two blocks that count (0: a bad page)
+};
+
+template <int KIND>
+struct ManyShared {
+  u32x4 k[2][8][64], v[2][8][64];    // [block of the pair]
+  f32x4 scale[2][2][8];              // [block][keys, values]
+};
+
 template <int KIND>
 __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan plan) {
   const KvArgs &P = A.kv;
-  __shared__ u32x4 sk[8][64], sv[8][64];
-  __shared__ f32x4 ss[2][8];
-  const int tiles = plan.many_tiles;
-  const int tile = tiles - 1 - (int)(blockIdx.x % tiles);   // the last tiles see the most keys
-  const int split = blockIdx.x / tiles % plan.many_splits;
-  const int part = blockIdx.x / (tiles * plan.many_splits) % plan.many_parts;
-  const int kvh = blockIdx.x / (tiles * plan.many_splits * plan.many_parts);
+  __shared__ ManyShared<KIND> sh[2];
+  // heads change fastest (workgroups are dealt to the eight XCDs in turn, so
+  // the tiles of one head share few L2s), and the tiles with most keys come first
+  const int kvh = blockIdx.x % P.heads;
+  const int part = blockIdx.x / P.heads % plan.many_parts;
+  const int split = blockIdx.x / (P.heads * plan.many_parts) % plan.many_splits;
+  const int tile = plan.many_tiles - 1 - (int)(blockIdx.x / (P.heads * plan.many_parts * plan.many_splits));
   Tile t;
   if (!tile_of<false>(A, plan, tile, part, kvh, t)) return;
   const int blocks = (t.keys + kBlock - 1) / kBlock;
@@ -283,6 +327,9 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   int limit[2];
   size_t at[2];
   bool row[2];
+  // a negative scale: -q and its magnitude; none: q = 0, and 1 (a masked score is -inf)
+  const uint32_t flip = A.scale_log2 < 0.0f ? 0x80008000u : 0u, keep = A.scale_log2 == 0.0f ? 0u : ~0u;
+  const float scale = A.scale_log2 == 0.0f ? 1.0f : fabsf(A.scale_log2);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int r = 32 * w + 16 * c + i16;
@@ -292,7 +339,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
     limit[c] = row[c] ? t.position + tok : -1;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      q[c][s].w = *(const u32x4_a4 *)(A.q + at[c] + 64 * (s >> 1) + 16 * g + 8 * (s & 1));
+      q[c][s].w = (*(const u32x4_a4 *)(A.q + at[c] + 64 * (s >> 1) + 16 * g + 8 * (s & 1)) & keep) ^ flip;
       if (!row[c]) q[c][s].w = (u32x4){0, 0, 0, 0};
     }
 #pragma unroll
@@ -300,93 +347,138 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
     m[c] = kNone;
     sum[c] = 0.0f;
   }
+  // keys that every row of the wave sees, and that any of them does
+  const int first_tok = 32 * w / t.heads, last_tok = min((32 * w + 31) / t.heads, t.tokens - 1);
+  const int all_see = t.position + first_tok + 1;
+  const int some_see = first_tok < t.tokens ? t.position + last_tok + 1 : 0;
 
-  for (int block = lo; block < hi; ++block) {
-    const uint8_t *blk = block_at(P, t.b, kvh, block, KIND == 8 ? kKv8Block : kKv16Block);
-    if (!blk) {
-      if (tid == 0) atomicOr(P.err, kErrPage);
-      continue;
-    }
-    const int left = t.keys - block * kBlock;
-    __syncthreads();
-    if (KIND == 8) {
-      const u32x4 k = *(const u32x4 *)(blk + tid * 16), v = *(const u32x4 *)(blk + kKv8Half + tid * 16);
-      sk[2 * w][l] = widen(k[0], k[1]).w;
-      sk[2 * w + 1][l] = widen(k[2], k[3]).w;
-      sv[2 * w][l] = widen(v[0], v[1]).w;
-      sv[2 * w + 1][l] = widen(v[2], v[3]).w;
-      if (tid < 16) ss[tid >> 3][tid & 7] = *(const f32x4 *)(blk + kKv8Scale + 16 * tid);
-    } else {
+  auto load = [&](int block, ManyIn<KIND> &in) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        sk[4 * x + w][l] = *(const u32x4 *)(blk + (tid + 256 * x) * 16);
-        Frag v;
-        v.w = *(const u32x4 *)(blk + kKv16Half + (tid + 256 * x) * 16);
-        if (left < kBlock) {
+    for (int y = 0; y < 2; ++y) {
+      const uint8_t *blk = block_at(P, t.b, kvh, min(block + y, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+      in.left[y] = block + y < hi && blk ? min(t.keys - (block + y) * kBlock, kBlock) : 0;
+      if (!blk && block + y < hi && tid == 0) atomicOr(P.err, kErrPage);
+      if (!blk) blk = P.base;
+      if (KIND == 8) {
+        in.k[y] = *(const u32x4 *)(blk + tid * 16);
+        in.v[y] = *(const u32x4 *)(blk + kKv8Half + tid * 16);
+        if (w == y) in.scale = *(const float *)(blk + kKv8Scale + 4 * l);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool out = 4 * g + (e & 3) + 16 * (e >> 2) >= left;
-            if (out) v.u[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-          }
+        for (int x = 0; x < 2; ++x) {
+          in.k[2 * y + (KIND == 8 ? 0 : x)] = *(const u32x4 *)(blk + (tid + 256 * x) * 16);
+          in.v[2 * y + (KIND == 8 ? 0 : x)] = *(const u32x4 *)(blk + kKv16Half + (tid + 256 * x) * 16);
         }
-        sv[4 * x + w][l] = v.w;
       }
     }
-    __syncthreads();
-    f32x4 s[2][2];
+  };
+  auto store = [&](const ManyIn<KIND> &in, ManyShared<KIND> &to) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s[0][i] = s[1][i] = (f32x4){0, 0, 0, 0};
+    for (int y = 0; y < 2; ++y) {
+      if (KIND == 8) {
+        to.k[y][2 * w][l] = widen(in.k[y][0], in.k[y][1]).w;
+        to.k[y][2 * w + 1][l] = widen(in.k[y][2], in.k[y][3]).w;
+        to.v[y][2 * w][l] = widen(in.v[y][0], in.v[y][1]).w;
+        to.v[y][2 * w + 1][l] = widen(in.v[y][2], in.v[y][3]).w;
+        if (w == y) ((float *)to.scale[y])[l] = in.scale;
+      } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 2; ++x) {
+          to.k[y][4 * x + w][l] = in.k[2 * y + (KIND == 8 ? 0 : x)];
+          u32x4 v = in.v[2 * y + (KIND == 8 ? 0 : x)];
+          // values behind the last key may be anything: 0 times them is not 0
+          if (in.left[y] < kBlock) v = keep_tokens(v, g, in.left[y]);
+          to.v[y][4 * x + w][l] = v;
+        }
+      }
+    }
+  };
+
+  ManyIn<KIND> in;
+  if (lo < hi) load(lo, in);
+  for (int block = lo; block < hi; block += 2) {
+    ManyShared<KIND> &now = sh[((block - lo) >> 1) & 1];
+    store(in, now);
+    const int left0 = in.left[0], left1 = in.left[1];
+    lds_barrier();
+    load(block + 2, in);        // always there: the waits stay exact
+    if (block * kBlock >= some_see) continue;
+    f32x4 s[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         Frag k;
-        k.w = sk[4 * i + x][l];
+        k.w = now.k[i >> 1][4 * (i & 1) + x][l];
         s[0][i] = mma(k, q[0][x], s[0][i]);
         s[1][i] = mma(k, q[1][x], s[1][i]);
       }
-    }
-    Frag pf[2];
-    float fade[2];
+    if (KIND == 8)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 f = now.scale[i >> 1][0][4 * (i & 1) + g];
+        s[0][i] *= f;
+        s[1][i] *= f;
+      }
+    const bool masked = left0 < kBlock || left1 < kBlock || (block + 2) * kBlock > all_see;
+    if (masked)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = 16 * (i & 1) + 4 * g + r;
+            if (key >= (i < 2 ? left0 : left1) || (block + (i >> 1)) * kBlock + key > limit[c]) s[c][i][r] = kNone;
+          }
+    Frag pf[2][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      float top = kNone;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (KIND == 8) s[c][i] *= ss[0][4 * i + g];
-        s[c][i] *= A.scale_log2;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (block * kBlock + 16 * i + 4 * g + r > limit[c]) s[c][i][r] = kNone;
-      }
-      float top = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
-                        fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
+      for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, fmaxf(s[c][i][0], s[c][i][1])), fmaxf(s[c][i][2], s[c][i][3]));
       top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m1 = fmaxf(m[c], top);
-      const float ref = m1 == kNone ? 0.0f : m1;
-      fade[c] = ex2(m[c] - ref);
-      m[c] = m1;
-      float add = 0.0f;
+      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+      if (__any(top > m[c] + kSlack)) {
+        const float m1 = fmaxf(m[c], top);
+        const float fade = ex2(m[c] - (m1 == kNone ? 0.0f : m1));
+        m[c] = m1;
+        sum[c] *= fade;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+        for (int d = 0; d < 8; ++d) o[c][d] *= fade;
+      }
+      const float ref = m[c] == kNone ? 0.0f : m[c];
+      float add[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         f32x4 p;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          p[r] = ex2(s[c][i][r] - ref);
-          add += p[r];
-          if (KIND == 8) p[r] = s[c][i][r] == kNone ? 0.0f : p[r] * ss[1][4 * i + g][r];
+          p[r] = ex2(__builtin_fmaf(s[c][i][r], scale, -ref));
+          add[r & 1] += p[r];
         }
-        pf[c].u[2 * i] = pack_bf16(p[0], p[1]);
-        pf[c].u[2 * i + 1] = pack_bf16(p[2], p[3]);
+        if (KIND == 8) {
+          const f32x4 f = now.scale[i >> 1][1][4 * (i & 1) + g];
+          // a masked key's scale is not looked at
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[r] = masked && s[c][i][r] == kNone ? 0.0f : p[r] * f[r];
+        }
+        pf[c][i >> 1].u[2 * (i & 1)] = pack_bf16(p[0], p[1]);
+        pf[c][i >> 1].u[2 * (i & 1) + 1] = pack_bf16(p[2], p[3]);
       }
-      sum[c] = __builtin_fmaf(sum[c], fade[c], add);
+      sum[c] += add[0] + add[1];
     }
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-      Frag v;
-      v.w = sv[d][l];
-      o[0][d] = mma(v, pf[0], o[0][d] * fade[0]);
-      o[1][d] = mma(v, pf[1], o[1][d] * fade[1]);
-    }
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        Frag v;
+        v.w = now.v[y][d][l];
+        o[0][d] = mma(v, pf[0][y], o[0][d]);
+        o[1][d] = mma(v, pf[1][y], o[1][d]);
+      }
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
