@@ -10,6 +10,7 @@
 // scores and the value's scale its weights, both in fp32.
 #include "qdr_mfma.h"
 #include "qdr_mixer.h"
+#include "qdr_paged.h"
 
 namespace qdr {
 
@@ -19,6 +20,14 @@ constexpr int kD = 128;
 constexpr float kNone = -INFINITY;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Largest of three as one instruction (fmaxf first quiets each operand with an
+// instruction of its own); a NaN is passed over.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
 
 // Eight codes as bfloat16 (exact).
 __device__ __forceinline__ Frag widen(uint32_t a, uint32_t b) {
@@ -109,6 +118,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
   const KvArgs &P = A.kv;
   __shared__ float sm[4][16], sl[4][16];
   __shared__ f32x4 so[4][8][64];
+  if (blockIdx.x == 0) check_counts(P);
   const int split = blockIdx.x % plan.few_splits;
   const int part = blockIdx.x / plan.few_splits % plan.few_parts;
   const int kvh = blockIdx.x / (plan.few_splits * plan.few_parts) % P.heads;
@@ -186,7 +196,8 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
       for (int r = 0; r < 4; ++r)
         if (block * kBlock + 16 * i + 4 * g + r > limit) s[i][r] = kNone;
     }
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    float top = max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]);
+    top = max3(max3(top, s[1][1], s[1][2]), s[1][3], s[1][3]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     if (__any(top > m)) {
@@ -208,11 +219,15 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
         // a masked key's scale is not looked at
         if (KIND == 8) p[i][r] = s[i][r] == kNone ? 0.0f : p[i][r] * in.vs[i][r];
       }
-    Frag pf;
+    // two parts: the products are not what few rows wait for, and the weights'
+    // rounding would be as large as the result's
+    Frag pf[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      pf.u[2 * i] = pack_bf16(p[i][0], p[i][1]);
-      pf.u[2 * i + 1] = pack_bf16(p[i][2], p[i][3]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t y[2];
+      parts<2>(p[i >> 1][2 * (i & 1)], p[i >> 1][2 * (i & 1) + 1], y);
+      pf[0].u[i] = y[0];
+      pf[1].u[i] = y[1];
     }
     // values behind the last key of the tile may be anything: 0 times them is not 0
     const int left = t.keys - block * kBlock;
@@ -229,7 +244,8 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
       } else {
         v.w = in.v[d & (KIND == 8 ? 3 : 7)];
       }
-      o[d] = mma(v, pf, o[d]);
+      o[d] = mma(v, pf[1], o[d]);
+      o[d] = mma(v, pf[0], o[d]);
     }
   };
 
@@ -306,6 +322,7 @@ template <int KIND>
 __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan plan) {
   const KvArgs &P = A.kv;
   __shared__ ManyShared<KIND> sh[2];
+  if (blockIdx.x == 0) check_counts(P);
   // heads change fastest (workgroups are dealt to the eight XCDs in turn, so
   // the tiles of one head share few L2s), and the tiles with most keys come first
   const int kvh = blockIdx.x % P.heads;
@@ -423,7 +440,8 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
         s[1][i] *= f;
       }
     const bool masked = left0 < kBlock || left1 < kBlock || (block + 2) * kBlock > all_see;
-    if (masked)
+    if (masked) {
+      asm volatile("");   // a branch, not 64 selects in every pass
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -433,12 +451,16 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
             const int key = 16 * (i & 1) + 4 * g + r;
             if (key >= (i < 2 ? left0 : left1) || (block + (i >> 1)) * kBlock + key > limit[c]) s[c][i][r] = kNone;
           }
+    }
     Frag pf[2][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float top = kNone;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, fmaxf(s[c][i][0], s[c][i][1])), fmaxf(s[c][i][2], s[c][i][3]));
+      float top = max3(s[c][0][0], s[c][0][1], s[c][0][2]), top1 = max3(s[c][2][0], s[c][2][1], s[c][2][2]);
+      top = max3(top, s[c][0][3], s[c][1][0]);
+      top1 = max3(top1, s[c][2][3], s[c][3][0]);
+      top = max3(top, s[c][1][1], s[c][1][2]);
+      top1 = max3(top1, s[c][3][1], s[c][3][2]);
+      top = max3(max3(top, s[c][1][3], s[c][3][3]), top1, top1);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32)) * scale;
       if (__any(top > m[c] + kSlack)) {
@@ -541,20 +563,10 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, AttendPlan pl
   *(uint32_t *)(A.o + at + 2 * l) = pack_bf16(a * inv, b * inv);
 }
 
-__global__ void __launch_bounds__(256) k_attend_check(KvArgs P) {
-  const int b = blockIdx.x * 256 + threadIdx.x;
-  if (b >= P.n) return;
-  const long long room = (long long)P.max_pages << P.page_shift;
-  int first, len;
-  if (!rows_of(P.cu, P.T, b, &first, &len) || (len > 0 && (P.context[b] < len || P.context[b] > room)))
-    atomicOr(P.err, kErrLength);
-}
-
 }  // namespace
 
 template <int KIND>
 static hipError_t attend(const AttendArgs &a, const AttendPlan &p, hipStream_t st) {
-  hipLaunchKernelGGL(k_attend_check, dim3((a.kv.n + 255) / 256), dim3(256), 0, st, a.kv);
   if (p.few) {
     const uint32_t units = (uint32_t)p.few_tiles * a.kv.heads * p.few_parts;
     hipLaunchKernelGGL(k_attend_few<KIND>, dim3(units * p.few_splits), dim3(256), 0, st, a, p);

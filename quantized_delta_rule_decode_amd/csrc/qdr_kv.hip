@@ -12,22 +12,13 @@
 // 264 (8-bit) or 512 B out a token and head.
 #include "qdr_mfma.h"
 #include "qdr_mixer.h"
+#include "qdr_paged.h"
 
 namespace qdr {
 
 namespace {
 
 constexpr int kD = 128;
-
-// Counts and contexts out of order or range, found once a call.
-__device__ __forceinline__ void check_counts(const KvArgs &P) {
-  const long long room = (long long)P.max_pages << P.page_shift;
-  for (int b = threadIdx.x; b < P.n; b += 256) {
-    int first, len;
-    if (!rows_of(P.cu, P.T, b, &first, &len) || (len > 0 && (P.context[b] < len || P.context[b] > room)))
-      atomicOr(P.err, kErrLength);
-  }
-}
 
 // The block a workgroup works on; lo .. hi are its positions that the call has.
 struct Where {

@@ -50,7 +50,7 @@ __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w &
 // the next 8 bits of the significand, so three of them hold an fp32 value to
 // its last bit (while the parts do not underflow).
 template <int P>
-__device__ __forceinline__ void split(float a, float b, uint32_t *part) {
+__device__ __forceinline__ void parts(float a, float b, uint32_t *part) {
   part[0] = pack_bf16(a, b);
 #pragma unroll
   for (int p = 1; p < P; ++p) {

@@ -109,6 +109,7 @@ AttendPlan plan_attend(int n, int T, int q_heads, int heads, int max_pages, int 
   auto cut = [&](int64_t units, int least, int target) {
     int64_t want = units > 0 ? (target + units - 1) / units : 1;
     const int64_t most = (blocks + least - 1) / least;
+    if (blocks <= kOnePiece) want = 1;
     if (want > most) want = most;
     if (want > 64) want = 64;
     return (int)(want < 1 ? 1 : want);

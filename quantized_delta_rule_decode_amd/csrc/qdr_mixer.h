@@ -83,6 +83,9 @@ hipError_t launch_kv_read(const KvArgs &, int kind, hipStream_t);
 // tiles, and the fewest blocks of keys that a piece of them has.
 constexpr int kFewRows = 16, kManyRows = 128;
 constexpr int kFewLeast = 4, kManyLeast = 4;
+// Up to so many blocks the keys are not cut: one workgroup takes 32 blocks in
+// about the time that the second launch costs.
+constexpr int kOnePiece = 32;
 
 // How an attention call is cut up: rows of a tile, tiles, and pieces of the
 // keys; decided on the host from the call's counts alone.

@@ -182,10 +182,10 @@ __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
 template <int P>
 __device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
   uint32_t p[4][P];
-  split<P>(a[0], a[1], p[0]);
-  split<P>(a[2], a[3], p[1]);
-  split<P>(b[0], b[1], p[2]);
-  split<P>(b[2], b[3], p[3]);
+  parts<P>(a[0], a[1], p[0]);
+  parts<P>(a[2], a[3], p[1]);
+  parts<P>(b[0], b[1], p[2]);
+  parts<P>(b[2], b[3], p[3]);
 #pragma unroll
   for (int x = 0; x < P; ++x) f[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
 }
@@ -265,14 +265,14 @@ __device__ __forceinline__ void put(const ScanAt &A, int c, int wave, int l, Sta
     const int group = wave + 8 * x;
     uint32_t p[2][3];
     if (group < 2 * kTriFrags) {
-      split<2>(in.tri[x][0], in.tri[x][1], p[0]);
-      split<2>(in.tri[x][2], in.tri[x][3], p[1]);
+      parts<2>(in.tri[x][0], in.tri[x][1], p[0]);
+      parts<2>(in.tri[x][2], in.tri[x][3], p[1]);
 #pragma unroll
       for (int y = 0; y < 2; ++y) ((Frag *)&st.A[group >> 1][y][l])->h[group & 1] = (u32x2){p[0][y], p[1][y]};
     } else if (DELTA) {
       const int f = group - 2 * kTriFrags;
-      split<3>(in.tri[x][0], in.tri[x][1], p[0]);
-      split<3>(in.tri[x][2], in.tri[x][3], p[1]);
+      parts<3>(in.tri[x][0], in.tri[x][1], p[0]);
+      parts<3>(in.tri[x][2], in.tri[x][3], p[1]);
 #pragma unroll
       for (int y = 0; y < 3; ++y) ((Frag *)&st.T[f >> 1][y][l])->h[f & 1] = (u32x2){p[0][y], p[1][y]};
     }
