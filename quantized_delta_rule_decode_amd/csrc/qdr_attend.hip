@@ -96,8 +96,13 @@ __device__ __forceinline__ int piece_blocks(int blocks, int splits, int least) {
   return max((blocks + splits - 1) / splits, least);
 }
 
-__device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int b, int kvh, int block, uint32_t bytes) {
-  const int page = P.pages[(size_t)b * P.max_pages + (block >> (P.page_shift - 5))];
+// Page of a block of sequence b; asked for ahead of the block's own loads,
+// which wait for it.
+__device__ __forceinline__ int page_of(const KvArgs &P, int b, int block) {
+  return P.pages[(size_t)b * P.max_pages + (block >> (P.page_shift - 5))];
+}
+// The block's memory; NULL on a bad page.
+__device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int page, int kvh, int block, uint32_t bytes) {
   if (page < 0 || page >= P.num_pages) return nullptr;
   const int per = 1 << (P.page_shift - 5);
   return P.base + (((size_t)page * P.heads + kvh) * per + (block & (per - 1))) * bytes;
@@ -150,8 +155,10 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
 
   // A block's loads are always there: one behind the last, or of a bad page,
   // is some block of the cache, and its keys are not looked at.
+  int page = lo < hi ? page_of(P, t.b, min(lo + w, blocks - 1)) : 0;
   auto load = [&](int block, FewIn<KIND> &in) {
-    const uint8_t *blk = block_at(P, t.b, kvh, min(block, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+    const uint8_t *blk = block_at(P, page, kvh, min(block, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+    page = page_of(P, t.b, min(block + 4, blocks - 1));
     in.good = blk != nullptr;
     if (!blk) blk = P.base;
     constexpr int N = KIND == 8 ? 4 : 8;
@@ -369,10 +376,14 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   const int all_see = t.position + first_tok + 1;
   const int some_see = first_tok < t.tokens ? t.position + last_tok + 1 : 0;
 
+  int page[2] = {0, 0};
+  if (lo < hi)
+    for (int y = 0; y < 2; ++y) page[y] = page_of(P, t.b, min(lo + y, blocks - 1));
   auto load = [&](int block, ManyIn<KIND> &in) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const uint8_t *blk = block_at(P, t.b, kvh, min(block + y, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+      const uint8_t *blk = block_at(P, page[y], kvh, min(block + y, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
+      page[y] = page_of(P, t.b, min(block + 2 + y, blocks - 1));
       in.left[y] = block + y < hi && blk ? min(t.keys - (block + y) * kBlock, kBlock) : 0;
       if (!blk && block + y < hi && tid == 0) atomicOr(P.err, kErrPage);
       if (!blk) blk = P.base;
