@@ -69,19 +69,34 @@ bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Parts of a prompt's workspace.
+// Parts of a prompt's workspace.  It is the same for both rules.
 struct PromptSpace {
   int64_t places;                // chunk places of one head
-  size_t chunks, slots, states;  // bytes
-  size_t total() const { return chunks + slots + states; }
+  int32_t segment;               // chunks of a segment (0: sequences are not cut)
+  int64_t segments;              // segment places of one head
+  bool ordered;
+  size_t chunks, tables, states, parts;  // bytes
+  size_t total() const { return chunks + tables + states + parts; }
 };
 
 PromptSpace prompt_space(const qdr::PoolView &v, int32_t n, int32_t T) {
-  PromptSpace s;
+  const size_t state = (size_t)v.num_heads * QDR_DIM * QDR_DIM * sizeof(float);
+  PromptSpace s{};
   s.places = T / qdr::kChunk + (int64_t)n;
   s.chunks = up((size_t)s.places * v.num_heads * qdr::kChunkFloats * sizeof(float));
-  s.slots = v.all_fp32 ? 0 : up((size_t)n * 2 * sizeof(int32_t));
-  s.states = v.all_fp32 ? 0 : (size_t)n * v.num_heads * QDR_DIM * QDR_DIM * sizeof(float);
+  s.ordered = n > 1 && n <= qdr::kMostOrdered;
+  s.tables = up((size_t)n * ((v.all_fp32 ? 0 : 2) + (s.ordered ? 1 : 0)) * sizeof(int32_t));
+  s.states = v.all_fp32 ? 0 : (size_t)n * state;
+  // segments for two rounds of workgroups, none below kSegmentLeast chunks: a
+  // segment's state costs four passes over 64 KiB, as much as four chunks' rows
+  const int64_t chunks = (int64_t)T / qdr::kChunk * v.num_heads;
+  int64_t segment = qdr::kSegmentLeast;
+  while (segment * qdr::kSegmentGroups < chunks) segment *= 2;
+  if (segment * qdr::kChunk < T) {
+    s.segment = (int32_t)segment;
+    s.segments = T / (segment * qdr::kChunk) + n;
+    s.parts = up((size_t)s.segments * (state + v.num_heads * sizeof(float)));
+  }
   return s;
 }
 
@@ -215,7 +230,7 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
   QDR_TRY(check_device(view.device));
   const PromptSpace space = prompt_space(view, n, T);
   QDR_TRY(check_groups(space.places * view.num_heads));
-  QDR_TRY(check_groups(((int64_t)n * view.num_heads + 8) * 8));
+  QDR_TRY(check_groups((n + space.segments) * view.num_heads * 16));   // of 512 threads, eight a head
   QDR_TRY(check_workspace(workspace, workspace_bytes, space.total()));
   hipStream_t st = static_cast<hipStream_t>(stream);
   QDR_TRY(qdr::pool_check_slots(pool, slots, n, st));
@@ -238,13 +253,21 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
   a.o = o;
   a.chunk_ws = reinterpret_cast<float *>(ws);
   a.err = view.err;
+  int32_t *table = reinterpret_cast<int32_t *>(ws + space.chunks);
   if (view.all_fp32) {
     a.pool = view.base;
     a.slot_stride = view.slot_stride;
   } else {
-    a.slots_in = reinterpret_cast<int32_t *>(ws + space.chunks);
-    a.slots_out = a.slots_in + n;
-    a.S = reinterpret_cast<float *>(ws + space.chunks + space.slots);
+    a.slots_in = table;
+    a.slots_out = table + n;
+    table += 2 * (size_t)n;
+    a.S = reinterpret_cast<float *>(ws + space.chunks + space.tables);
+  }
+  if (delta && space.ordered) a.order = table;
+  if (!delta && space.segment) {
+    a.segment = space.segment;
+    a.segments = (int32_t)space.segments;
+    a.segment_ws = reinterpret_cast<float *>(ws + space.chunks + space.tables + space.states);
   }
   hipError_t e = qdr::pool_after_writeback(pool, st);
   if (e == hipSuccess && !a.pool) e = qdr::launch_prompt_slots(a, st);

@@ -20,6 +20,11 @@ constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
 // Workspace of one (chunk, head): the two triangular matrices, then the
 // decays from the chunk's start and to its end.
 constexpr size_t kChunkFloats = 2 * kTriFloats + 2 * kChunk;
+// Chunks of a segment at least, and segments that a call is cut into at most
+// about (of all heads).
+constexpr int kSegmentLeast = 8, kSegmentGroups = 1024;
+// Sequences of a call that are put in order of length (n^2 comparisons).
+constexpr int kMostOrdered = 1024;
 
 struct PromptArgs {
   const int32_t *slots, *carry, *cu;
@@ -34,6 +39,11 @@ struct PromptArgs {
   uint64_t slot_stride;
   float *S;                   // [n][H][128][128]
   int32_t *slots_in, *slots_out;   // dense: slots to unpack and to pack (-1: none)
+  int32_t *order;             // DELTA: [n] sequences by falling length; NULL: as they come
+  // SUM: a sequence is cut into segments of so many chunks that are taken side
+  // by side (0: not cut); places of segments of a head, and their states
+  int32_t segment, segments;
+  float *segment_ws;          // [segments][H][128*128], then [segments][H] decays
   uint32_t *err;
 };
 hipError_t launch_prompt_slots(const PromptArgs &, hipStream_t);

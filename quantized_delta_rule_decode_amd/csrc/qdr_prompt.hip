@@ -195,20 +195,11 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
 template <bool DELTA>
 struct Stage {
   u32x4 Q[4][4][64];                          // [token tile][channels 32 s + 8 g ..]
-  u32x4 K[DELTA ? 4 : 1][4][64];
-  u32x4 Kt[8][2][64];                         // K^T: [tile of S][tokens 32 s + {4 g.., 16 + 4 g..}]
+  u32x4 K[4][4][64];
   u32x4 A[kTriFrags][2][64];                  // two parts
   u32x4 T[DELTA ? kTriFrags : 1][3][64];      // three
   uint16_t V[kChunk][136];
   float dec[2 * kChunk];                      // decays from the chunk's start, then to its end
-};
-
-// A thread's share of it, on the way there.
-template <bool DELTA>
-struct StageIn {
-  u32x4 q[2], k[2], v[2];     // row 16 (wave & 3) + i16, channels 64 (wave >> 2) + 32 x + 8 g ..
-  f32x4 tri[DELTA ? 3 : 2];   // four values of A or T
-  float dec;
 };
 
 struct ScanAt {
@@ -216,104 +207,144 @@ struct ScanAt {
   size_t row;
 };
 
-template <bool DELTA>
-__device__ __forceinline__ void fetch(const PromptArgs &P, const ScanAt &A, int c, int wave, int l, StageIn<DELTA> &in) {
-  const int nt = min(kChunk, A.len - c * kChunk), t = 16 * (wave & 3) + (l & 15);
-  const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 64 * (wave >> 2) + 8 * (l >> 4);
+// Eight waves bring a chunk in (READ: also what only the readout needs).
+template <bool DELTA, bool READ>
+__device__ __forceinline__ void stage(const PromptArgs &P, const ScanAt &A, int c, int wave, int l, Stage<DELTA> &st) {
+  const int nt = min(kChunk, A.len - c * kChunk), g = l >> 4, tile = wave & 3, t = 16 * tile + (l & 15);
+  const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 64 * (wave >> 2) + 8 * g;
+  u32x4 q[2], k[2], v[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    in.k[x] = *(const u32x4_a4 *)(P.k + at + 32 * x);
-    in.q[x] = *(const u32x4_a4 *)(P.q + at + 32 * x);
-    in.v[x] = *(const u32x4_a4 *)(P.v + at + 32 * x);
+    k[x] = *(const u32x4_a4 *)(P.k + at + 32 * x);
+    v[x] = *(const u32x4_a4 *)(P.v + at + 32 * x);
+    if (READ) q[x] = *(const u32x4_a4 *)(P.q + at + 32 * x);
   }
   const float *ws = chunk_ws(P, A.place0 + c, A.h);
   // groups of 256 values: A's 12, then T's
+  constexpr int kGroups = (DELTA ? 4 : 2) * kTriFrags;
+  constexpr int kTri = DELTA ? 3 : READ ? 2 : 0;
+  f32x4 tri[3];
 #pragma unroll
-  for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
+  for (int x = 0; x < kTri; ++x) {
     const int group = wave + 8 * x;
-    in.tri[x] = *(const f32x4 *)(ws + (DELTA || group < 2 * kTriFrags ? group : wave) * 256 + l * 4);
+    tri[x] = *(const f32x4 *)(ws + (group < kGroups ? group : wave) * 256 + l * 4);
   }
-  in.dec = ws[2 * kTriFloats + ((wave & 1) * 64 + l)];
-}
-
-template <bool DELTA>
-__device__ __forceinline__ void put(const ScanAt &A, int c, int wave, int l, StageIn<DELTA> &in, Stage<DELTA> &st) {
-  const int g = l >> 4, i16 = l & 15, odd = l & 1, tile = wave & 3, t = 16 * tile + i16;
-  if (A.len - c * kChunk <= t)   // nothing of the rows behind the end
+  const float dec = ws[2 * kTriFloats + ((wave & 1) * 64 + l)];
+  if (t >= nt)   // nothing of the rows behind the end
 #pragma unroll
-    for (int x = 0; x < 2; ++x) in.q[x] = in.k[x] = in.v[x] = (u32x4){0, 0, 0, 0};
+    for (int x = 0; x < 2; ++x) q[x] = k[x] = v[x] = (u32x4){0, 0, 0, 0};
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int s = 2 * (wave >> 2) + x;
-    st.Q[tile][s][l] = in.q[x];
-    if (DELTA) st.K[tile][s][l] = in.k[x];
-    *(u32x4 *)&st.V[t][32 * s + 8 * g] = in.v[x];
-    // K^T: lanes of two neighbouring tokens trade halves of each word.  Channel
-    // 32 s + 8 g + 4 i + r is row 4 g + r of tile 2 s + i; token 4 g' + r' of
-    // tile `tile` is value 4 (tile & 1) + r' of lane group g'
-    uint32_t *to = (uint32_t *)&st.Kt[2 * s][tile >> 1][16 * (i16 >> 2) + 4 * g + odd] + 2 * (tile & 1) + ((i16 & 2) >> 1);
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const uint32_t own = in.k[x][y];
-      const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-      to[(y >> 1) * (2 * 64 * 4) + (y & 1) * 8] = odd ? __builtin_amdgcn_perm(own, other, 0x07060302u)
-                                                      : __builtin_amdgcn_perm(other, own, 0x05040100u);
-    }
+    if (READ) st.Q[tile][s][l] = q[x];
+    st.K[tile][s][l] = k[x];
+    *(u32x4 *)&st.V[t][32 * s + 8 * g] = v[x];
   }
 #pragma unroll
-  for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
+  for (int x = 0; x < kTri; ++x) {
     const int group = wave + 8 * x;
     uint32_t p[2][3];
     if (group < 2 * kTriFrags) {
-      parts<2>(in.tri[x][0], in.tri[x][1], p[0]);
-      parts<2>(in.tri[x][2], in.tri[x][3], p[1]);
+      parts<2>(tri[x][0], tri[x][1], p[0]);
+      parts<2>(tri[x][2], tri[x][3], p[1]);
 #pragma unroll
       for (int y = 0; y < 2; ++y) ((Frag *)&st.A[group >> 1][y][l])->h[group & 1] = (u32x2){p[0][y], p[1][y]};
     } else if (DELTA) {
       const int f = group - 2 * kTriFrags;
-      parts<3>(in.tri[x][0], in.tri[x][1], p[0]);
-      parts<3>(in.tri[x][2], in.tri[x][3], p[1]);
+      parts<3>(tri[x][0], tri[x][1], p[0]);
+      parts<3>(tri[x][2], tri[x][3], p[1]);
 #pragma unroll
-      for (int y = 0; y < 3; ++y) ((Frag *)&st.T[f >> 1][y][l])->h[f & 1] = (u32x2){p[0][y], p[1][y]};
+      for (int y = 0; y < 3; ++y) ((Frag *)&st.T[DELTA ? f >> 1 : 0][y][l])->h[f & 1] = (u32x2){p[0][y], p[1][y]};
     }
   }
-  if (wave < 2) st.dec[wave * 64 + l] = in.dec;
+  if (wave < 2) st.dec[wave * 64 + l] = dec;
+}
+
+// Row 4 g + r of result 2 s + i of the state is channel state_row(...) + r: a
+// lane's two results of a contraction step are the eight channels that one
+// 16-byte piece of a row of q or k has.  Odd lane groups take its halves in
+// the other order, which spreads the transposing reads of K over all banks.
+__device__ __forceinline__ int state_row(int m, int g) { return 32 * (m >> 1) + 8 * g + 4 * ((m & 1) ^ (g & 1)); }
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Operand of K^T: rows (channels) of result m, tokens 32 s + {4 g.., 16 + 4 g..}.
+// A transposing read gives lane i of a group of 16 the i-th of 16 columns of
+// four rows; the group's lane 4 r + j points to columns 4 j .. of row r.
+template <bool DELTA>
+__device__ __forceinline__ Frag transposed(const Stage<DELTA> &st, int m, int s, int l) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const int g = l >> 4, r = (l >> 2) & 3, j = l & 3;
+  Frag f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][m >> 1][16 * j + 4 * g + r] + ((m & 1) ^ (j & 1));
+    f.h[half] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)piece));
+  }
+  return f;
+}
+
+// S = 2^g_63 S + K^T diag(2^(g_63 - g)) U.
+template <bool DELTA>
+__device__ __forceinline__ void update_state(const Stage<DELTA> &st, const f32x4 *u, f32x4 *S, int l) {
+  const int g = l >> 4;
+  const float all = st.dec[kChunk - 1];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) S[m] *= all;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Frag d[3];
+    split8<3>(u[2 * s] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 4 * g], u[2 * s + 1] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 16 + 4 * g], d);
+#pragma unroll
+    for (int half = 0; half < 8; half += 4) {
+      Frag k[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) k[m] = transposed<DELTA>(st, half + m, s, l);
+#pragma unroll
+      for (int x = 2; x >= 0; --x)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
+    }
+  }
 }
 
 // One wave, sixteen columns, one chunk.  Products of S, R and U take their
 // right operands from the accumulators of the product before: nothing but the
 // shared left operands is read from LDS, and nothing waits for another wave.
+// (Products of one accumulator never follow each other: four at a time.)
 template <bool DELTA>
 __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, int c, int col0, int l, const Stage<DELTA> &st, f32x4 *S) {
-  const int g = l >> 4, i16 = l & 15;
-  Frag f[4][3];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) split8<3>(S[2 * s], S[2 * s + 1], f[s]);
+  const int g = l >> 4, i16 = l & 15, swap = g & 1;
   f32x4 o[4], r[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) o[t] = r[t] = (f32x4){0, 0, 0, 0};
-  // (products of one accumulator never follow each other: four at a time)
-  if (DELTA) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < 4; ++s) {
+    Frag f[3];
+    split8<DELTA ? 3 : 2>(S[2 * s], S[2 * s + 1], f);
+    // odd lane groups: the first result has the piece's second half
+#pragma unroll
+    for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
+      const u32x2 a = f[x].h[0], b = f[x].h[1];
+      f[x].h[0] = swap ? b : a;
+      f[x].h[1] = swap ? a : b;
+    }
+    if (DELTA) {
       Frag k[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) k[t].w = st.K[DELTA ? t : 0][s][l];
+      for (int t = 0; t < 4; ++t) k[t].w = st.K[t][s][l];
 #pragma unroll
       for (int x = 2; x >= 0; --x)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[s][x], r[t]);
+        for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[x], r[t]);
     }
-  }
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
     Frag q[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) q[t].w = st.Q[t][s][l];
 #pragma unroll
     for (int x = 1; x >= 0; --x)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f[s][x], o[t]);
+      for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f[x], o[t]);
   }
   f32x4 u[4];
 #pragma unroll
@@ -328,13 +359,12 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
     }
   }
   if (DELTA) {   // U = T R
-    Frag R[2][3];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) split8<3>(r[2 * s], r[2 * s + 1], R[s]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) u[t] = (f32x4){0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
+      Frag R[3];
+      split8<3>(r[2 * s], r[2 * s + 1], R);
 #pragma unroll
       for (int x = 2; x >= 0; --x) {
         Frag a[4];
@@ -343,33 +373,15 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
 #pragma unroll
         for (int y = 2 - x; y >= 0; --y)
 #pragma unroll
-          for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[s][y], u[t]);
+          for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[y], u[t]);
       }
-  }
-  // S = 2^g_63 S + K^T diag(2^(g_63 - g)) U
-  const float all = st.dec[kChunk - 1];
-#pragma unroll
-  for (int m = 0; m < 8; ++m) S[m] *= all;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    Frag d[3];
-    split8<3>(u[2 * s] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 4 * g], u[2 * s + 1] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 16 + 4 * g], d);
-#pragma unroll
-    for (int half = 0; half < 8; half += 4) {
-      Frag k[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) k[m].w = st.Kt[half + m][s][l];
-#pragma unroll
-      for (int x = 2; x >= 0; --x)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
     }
   }
   // O += A U
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     Frag U[2];
-    split8<2>(u[2 * s], u[2 * s + 1], U);   // SUM: V, exact in the first
+    split8<DELTA ? 2 : 1>(u[2 * s], u[2 * s + 1], U);   // SUM: V, exact in one
 #pragma unroll
     for (int x = 1; x >= 0; --x) {
       Frag a[4];
@@ -387,7 +399,7 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
   for (int t = 0; t < 4; ++t) {
     const uint32_t lo = pack_bf16(o[t][0], o[t][1]), hi = pack_bf16(o[t][2], o[t][3]);
     const uint32_t own = odd ? hi : lo, give = odd ? lo : hi;
-    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);   // lane ^ 1
     // rows 4 g + 2 odd, + 1 of columns i16 & 14, + 1
     const uint32_t x = odd ? got : own, y = odd ? own : got;
     const uint32_t r0 = __builtin_amdgcn_perm(y, x, 0x05040100u), r1 = __builtin_amdgcn_perm(y, x, 0x07060302u);
@@ -396,77 +408,160 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
     if (at < nt) *(uint32_t *)dst = r0;
     if (at + 1 < nt) *(uint32_t *)(dst + A.row) = r1;
   }
+  update_state<DELTA>(st, u, S, l);
 }
 
-// The chunks in order: eight waves stage a chunk (asked for a chunk ahead),
-// the first NW of them take sixteen columns each through it.
-template <bool DELTA, int NW>
-__global__ void __launch_bounds__(512, 2) k_prompt_scan(PromptArgs P) {
-  constexpr int kSlices = 8 / NW;
-  __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
-
-  // the slices of one (sequence, head) go to one XCD (workgroups are dealt to
-  // the eight in turn): they share its q, k, A and T through one L2
-  const int bh = (blockIdx.x / (8 * kSlices)) * 8 + blockIdx.x % 8;
-  if (bh >= P.n * P.H) return;
-  const int b = bh / P.H;
-  const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slice = (blockIdx.x / 8) % kSlices, col0 = 16 * (slice * NW + wave);
-
-  ScanAt A;
-  A.h = bh % P.H;
-  A.row = (size_t)P.H * kD;
-  if (!rows_of(P.cu, P.T, b, &A.first, &A.len)) {
+// Which chunks of which sequence a workgroup takes: a whole sequence, or with
+// SUM a segment of P.segment chunks of one.
+__device__ __forceinline__ bool scan_at(const PromptArgs &P, int place, int *b, int *from, int *to, int *segments, ScanAt &A) {
+  const int per = P.segment * kChunk;
+  *b = P.segment ? sequence_of(P.cu, P.n, per, 1, place) : P.order ? P.order[place] : place;
+  if (!rows_of(P.cu, P.T, *b, &A.first, &A.len)) {
     if (threadIdx.x == 0) atomicOr(P.err, kErrLength);
-    return;
+    return false;
   }
+  A.row = (size_t)P.H * kD;
+  A.chunks = (A.len + kChunk - 1) / kChunk;
+  A.place0 = A.first / kChunk + *b;
+  *segments = P.segment ? max((A.chunks + P.segment - 1) / P.segment, 1) : 1;
+  const int at = P.segment ? place - (A.first / per + *b) : 0;
+  *from = at * P.segment;
+  *to = P.segment ? min(*from + P.segment, A.chunks) : A.chunks;
+  return at >= 0 && at < *segments;
+}
+
+// A segment's state in the workspace: a thread's eight results side by side
+// with its neighbours'; before k_prompt_join what the segment adds to a state,
+// and the decay over it, then the state that it starts from.
+__device__ __forceinline__ f32x4 *segment_ws(const PromptArgs &P, int place, int h) {
+  return (f32x4 *)P.segment_ws + ((size_t)place * P.H + h) * (kD * kD / 4) + threadIdx.x;
+}
+__device__ __forceinline__ float *segment_decay(const PromptArgs &P, int place, int h) {
+  return (float *)((f32x4 *)P.segment_ws + (size_t)P.segments * P.H * (kD * kD / 4)) + (size_t)place * P.H + h;
+}
+
+// The state of a (sequence, head) where it lives.
+struct StateAt {
+  f32x4 *blk;       // an uncompressed pool's block (four rows of a column together), or
+  float *dense;
+  __device__ __forceinline__ StateAt(const PromptArgs &P, int b, int slot, int h)
+      : blk(P.pool ? (f32x4 *)(P.pool + (size_t)slot * P.slot_stride + (size_t)h * (kD * kD * 4)) : nullptr),
+        dense(P.S + ((size_t)b * P.H + h) * kD * kD) {}
+  __device__ __forceinline__ f32x4 get(int row, int col) const {
+    if (blk) return blk[(row >> 2) * kD + col];
+    const float *s = dense + row * kD + col;
+    return (f32x4){s[0], s[kD], s[2 * kD], s[3 * kD]};
+  }
+  __device__ __forceinline__ void set(int row, int col, f32x4 x) const {
+    if (blk) blk[(row >> 2) * kD + col] = x;
+    else
+      for (int r = 0; r < 4; ++r) dense[(row + r) * kD + col] = x[r];
+  }
+};
+
+// The chunks in order, a wave to sixteen columns.  Two workgroups a compute
+// unit: one stages while the other computes.
+template <bool DELTA>
+__global__ void __launch_bounds__(512, 4) k_prompt_scan(PromptArgs P) {
+  __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
+  const int l = threadIdx.x & 63, g = l >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int place = blockIdx.x / P.H, col = 16 * wave + (l & 15);
+  int b, from, to, segments;
+  ScanAt A;
+  A.h = blockIdx.x % P.H;
+  if (!scan_at(P, place, &b, &from, &to, &segments, A)) return;
   const int slot = P.slots[b];
   if (slot < 0 || slot >= P.num_slots) {
     if (slot != -1 && threadIdx.x == 0) atomicOr(P.err, kErrSlot);
-    for (size_t i = threadIdx.x; i < (size_t)A.len * (16 * NW); i += 512)
-      P.o[((size_t)A.first + i / (16 * NW)) * A.row + (size_t)A.h * kD + slice * 16 * NW + i % (16 * NW)] = 0;
+    const size_t first = (size_t)A.first + (size_t)from * kChunk, rows = min((to - from) * kChunk, A.len - from * kChunk);
+    for (size_t i = threadIdx.x; i < rows * kD; i += 512) P.o[(first + i / kD) * A.row + (size_t)A.h * kD + i % kD] = 0;
     return;
   }
-  A.chunks = (A.len + kChunk - 1) / kChunk;
-  A.place0 = A.first / kChunk + b;
-
-  // S: row 4 g + r of result 2 s + i is row 32 s + 8 g + 4 i + r, so that the
-  // two results of a contraction step are, in a lane, eight rows in a row: the
-  // channels that one 16-byte load of q or k has
   const bool carried = P.carry != nullptr && P.carry[b] != 0;
-  f32x4 *blk = P.pool ? (f32x4 *)(P.pool + (size_t)slot * P.slot_stride + (size_t)A.h * (kD * kD * 4)) : nullptr;
-  float *dense = P.S + (size_t)bh * kD * kD;
-  const int col = col0 + i16;
+  const StateAt state(P, b, slot, A.h);
   f32x4 S[8];
-  if (wave < NW)
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int row = 32 * (m >> 1) + 8 * g + 4 * (m & 1);
-      if (!carried) S[m] = (f32x4){0, 0, 0, 0};
-      else if (blk) S[m] = blk[(row >> 2) * kD + col];
-      else
-        for (int r = 0; r < 4; ++r) S[m][r] = dense[(row + r) * kD + col];
-    }
-
-  StageIn<DELTA> in;
-  if (A.chunks > 0) fetch<DELTA>(P, A, 0, wave, l, in);
-  for (int c = 0; c < A.chunks; ++c) {
-    put<DELTA>(A, c, wave, l, in, st);
-    lds_barrier();
-    fetch<DELTA>(P, A, min(c + 1, A.chunks - 1), wave, l, in);   // always there: the waits stay exact
-    if (wave < NW) columns<DELTA>(P, A, c, col0, l, st, S);
-    lds_barrier();
-  }
-
-  if (wave >= NW || (carried && A.len == 0)) return;   // the slot stays as it is
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    const int row = 32 * (m >> 1) + 8 * g + 4 * (m & 1);
-    if (blk) blk[(row >> 2) * kD + col] = S[m];
-    else
-      for (int r = 0; r < 4; ++r) dense[(row + r) * kD + col] = S[m][r];
+    if (segments > 1) S[m] = segment_ws(P, place, A.h)[m * 512];
+    else if (carried) S[m] = state.get(state_row(m, g), col);
+    else S[m] = (f32x4){0, 0, 0, 0};
   }
+  for (int c = from; c < to; ++c) {
+    stage<DELTA, true>(P, A, c, wave, l, st);
+    lds_barrier();
+    columns<DELTA>(P, A, c, 16 * wave, l, st, S);
+    lds_barrier();
+  }
+  // the last segment has the sequence's state; a slot without rows stays as it is
+  if (to < A.chunks || (carried && A.len == 0)) return;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) state.set(state_row(m, g), col, S[m]);
+}
+
+// SUM: what a segment adds to the state it starts from, and the decay over it.
+__global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
+  __shared__ __attribute__((aligned(16))) Stage<false> st;
+  const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int place = blockIdx.x / P.H;
+  int b, from, to, segments;
+  ScanAt A;
+  A.h = blockIdx.x % P.H;
+  if (!scan_at(P, place, &b, &from, &to, &segments, A) || to >= A.chunks) return;
+  f32x4 S[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) S[m] = (f32x4){0, 0, 0, 0};
+  float decay = 1.0f;
+  for (int c = from; c < to; ++c) {
+    stage<false, false>(P, A, c, wave, l, st);
+    lds_barrier();
+    f32x4 u[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        u[t][x] = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][16 * wave + i16] << 16);
+    update_state<false>(st, u, S, l);
+    decay *= st.dec[kChunk - 1];
+    lds_barrier();
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m) segment_ws(P, place, A.h)[m * 512] = S[m];
+  if (threadIdx.x == 0) *segment_decay(P, place, A.h) = decay;
+}
+
+// SUM: the states that the segments start from, a thread to one of its eight
+// results: S_0, then S = decay S + what the segment adds.
+__global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
+  const int m = blockIdx.x % 8, h = blockIdx.x / 8 % P.H, b = blockIdx.x / (8 * P.H);
+  const int l = threadIdx.x & 63, per = P.segment * kChunk;
+  int first, len;
+  const int slot = P.slots[b];
+  if (!rows_of(P.cu, P.T, b, &first, &len) || slot < 0 || slot >= P.num_slots) return;
+  const int segments = (len + per - 1) / per, place = first / per + b;
+  if (segments < 2) return;
+  f32x4 S = {0, 0, 0, 0};
+  if (P.carry != nullptr && P.carry[b] != 0) S = StateAt(P, b, slot, h).get(state_row(m, l >> 4), (threadIdx.x >> 6) * 16 + (l & 15));
+  f32x4 next = segment_ws(P, place, h)[m * 512];
+  for (int i = 0; i < segments; ++i) {
+    const f32x4 add = next;
+    const float decay = *segment_decay(P, place + i, h);   // (the last one's is not used)
+    if (i + 1 < segments) next = segment_ws(P, place + i + 1, h)[m * 512];
+    segment_ws(P, place + i, h)[m * 512] = S;
+    S = S * decay + add;
+  }
+}
+
+// Sequences by falling length: the longest ones start first.
+__global__ void __launch_bounds__(256) k_prompt_order(PromptArgs P) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= P.n) return;
+  auto length = [&](int i) { return (long long)P.cu[i + 1] - P.cu[i]; };
+  const long long mine = length(b);
+  int rank = 0;
+  for (int i = 0; i < P.n; ++i) rank += length(i) > mine || (length(i) == mine && i < b);
+  P.order[rank] = b;
 }
 
 // Slots whose states are unpacked before and packed after the scan.
@@ -480,22 +575,6 @@ __global__ void __launch_bounds__(256) k_prompt_slots(PromptArgs P) {
   const bool in_pool = slot >= 0 && slot < P.num_slots;
   P.slots_in[b] = ok && carried && in_pool && len > 0 ? slot : -1;
   P.slots_out[b] = ok && in_pool && !(carried && len == 0) ? slot : -1;
-}
-
-template <bool DELTA, int NW>
-hipError_t scan(const PromptArgs &a, hipStream_t st) {
-  const int slices = 8 / NW, bh = (a.n * a.H + 7) / 8;
-  hipLaunchKernelGGL((k_prompt_scan<DELTA, NW>), dim3(bh * 8 * slices), dim3(512), 0, st, a);
-  return hipGetLastError();
-}
-
-template <bool DELTA>
-hipError_t scan(const PromptArgs &a, hipStream_t st) {
-  const int bh = a.n * a.H;
-  if (bh <= 32) return scan<DELTA, 1>(a, st);
-  if (bh <= 64) return scan<DELTA, 2>(a, st);
-  if (bh <= 128) return scan<DELTA, 4>(a, st);
-  return scan<DELTA, 8>(a, st);
 }
 
 }  // namespace
@@ -513,7 +592,17 @@ hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st)
 }
 
 hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
-  return delta ? scan<true>(a, st) : scan<false>(a, st);
+  if (delta) {
+    if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
+    return hipGetLastError();
+  }
+  if (a.segment) {
+    hipLaunchKernelGGL(k_prompt_segment, dim3(a.segments * a.H), dim3(512), 0, st, a);
+    hipLaunchKernelGGL(k_prompt_join, dim3(a.n * a.H * 8), dim3(512), 0, st, a);
+  }
+  hipLaunchKernelGGL(k_prompt_scan<false>, dim3((a.segment ? a.segments : a.n) * a.H), dim3(512), 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace qdr
