@@ -248,7 +248,7 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
   a.q = q;
   a.k = k;
   a.v = v;
-  a.beta = beta;
+  a.beta = delta ? beta : nullptr;
   a.gate = gate;
   a.o = o;
   a.chunk_ws = reinterpret_cast<float *>(ws);

@@ -17,9 +17,10 @@ constexpr int kChunk = 64;                       // tokens taken at a time
 // w/2 + 1 of them, each 16 rows x 32 columns, 64 lanes x 8 fp32.
 constexpr int kTriFrags = 6;
 constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
-// Workspace of one (chunk, head): the two triangular matrices, then the
-// decays from the chunk's start and to its end.
-constexpr size_t kChunkFloats = 2 * kTriFloats + 2 * kChunk;
+// Workspace of one (chunk, head): sums of the gates' logarithms (64 fp64), the
+// decays from the chunk's start and to its end (64 fp32 each), and for DELTA
+// one triangular matrix.
+constexpr size_t kDecayFloats = 4 * kChunk, kChunkFloats = kDecayFloats + kTriFloats;
 // Chunks of a segment at least, and segments that a call is cut into at most
 // about (of all heads).
 constexpr int kSegmentLeast = 8, kSegmentGroups = 1024;
@@ -31,9 +32,9 @@ struct PromptArgs {
   int32_t n, T, H, num_slots;
   int32_t chunks;             // chunk places of a head: T/64 + n
   const uint16_t *q, *k, *v;
-  const float *beta, *gate;
+  const float *beta, *gate;   // beta: NULL for SUM
   uint16_t *o;
-  float *chunk_ws;            // [chunks][H][kChunkFloats]
+  float *chunk_ws;            // [chunks][H][kChunkFloats], SUM: [kDecayFloats]
   // where the states are: an uncompressed pool's blocks, or dense fp32
   uint8_t *pool;              // NULL: dense
   uint64_t slot_stride;

@@ -8,12 +8,12 @@
 //   SUM    U = V
 //   O  = diag(2^g) Q S + A U,   A_ts = G_ts q_t.k_s (t >= s)
 //   S' = 2^g_63 S + K^T diag(2^(g_63 - g)) U
-// so all of it is matrix products.  Two launches:
-//   k_prompt_chunks  everything that does not depend on the state, every
-//                    chunk at once: A, and for DELTA T = (I + L)^-1 diag(beta);
-//   k_prompt_scan    the chunks in order; the columns of S, U and O do not
-//                    mix, so a workgroup takes 16 NT columns of one (sequence,
-//                    head) and keeps its part of S in registers throughout.
+// so all of it is matrix products.  Launches:
+//   k_prompt_chunks   DELTA, every chunk at once: T = (I + L)^-1 diag(beta) and
+//                     the decays;  SUM: k_prompt_decays, the decays alone;
+//   k_prompt_segment, k_prompt_join   SUM, long sequences: cut into segments;
+//                     what each adds to a state, then the states they start from;
+//   k_prompt_scan     the chunks of a sequence (segment) in order.
 // Precision: q, k and v are bfloat16 and enter exactly.  Whatever is computed
 // (S, U, T, A) enters a product as a sum of bfloat16 parts: three parts (24
 // bits, an fp32 value) on the way to the state, two (16 bits) where only the
@@ -26,6 +26,10 @@ namespace qdr {
 
 namespace {
 
+// Keeps the reads of later steps from being moved up across it: they would not
+// fit the registers that four waves a SIMD leave.
+#define QDR_PLACE() __builtin_amdgcn_sched_barrier(0)
+
 constexpr int kD = 128;
 constexpr int kLd = 68;        // row stride of a 64 x 64 fp32 matrix in LDS
 constexpr double kLogZero = -2000.0;   // for log2(0): 2^-2000 is 0, and sums of 64 of it stay finite
@@ -33,8 +37,44 @@ constexpr double kLogZero = -2000.0;   // for log2(0): 2^-2000 is 0, and sums of
 // First fragment of row tile w of a triangular matrix.
 __device__ __forceinline__ int tri_frag(int w) { return w < 2 ? w : 2 * w - 2; }
 
-__device__ __forceinline__ float *chunk_ws(const PromptArgs &P, int place, int h) {
-  return P.chunk_ws + ((size_t)place * P.H + h) * kChunkFloats;
+// Workspace of one (chunk, head).
+struct ChunkSpace {
+  double *lg;      // [64] sums of log2 a over the chunk up to each token
+  float *dec;      // [64] 2^lg, [64] 2^(lg_63 - lg)
+  float *T;        // DELTA: fragments of T, [fragment][half][lane][4]
+};
+__device__ __forceinline__ ChunkSpace chunk_space(const PromptArgs &P, int place, int h) {
+  float *ws = P.chunk_ws + ((size_t)place * P.H + h) * (P.beta ? kChunkFloats : kDecayFloats);
+  return {(double *)ws, ws + 2 * kChunk, ws + kDecayFloats};
+}
+
+// One wave: the decays of a chunk, a token to a lane.
+__device__ __forceinline__ double put_decays(const PromptArgs &P, size_t t0, int nt, int h, int l, const ChunkSpace &ws) {
+  const float a = l < nt ? P.gate[(t0 + l) * P.H + h] : 1.0f;
+  double x = a == 0.0f ? kLogZero : log2((double)a);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(x, d);
+    if (l >= d) x += y;
+  }
+  const double end = __shfl(x, 63);
+  ws.lg[l] = x;
+  ws.dec[l] = exp2f((float)x);
+  ws.dec[kChunk + l] = exp2f((float)(end - x));
+  return x;
+}
+
+// The chunk that place `place` of a head stands for; false: none, or one of a
+// sequence that is skipped.
+__device__ __forceinline__ bool chunk_at(const PromptArgs &P, int place, size_t *t0, int *nt) {
+  const int b = sequence_of(P.cu, P.n, kChunk, 1, place);
+  int first, len;
+  if (!rows_of(P.cu, P.T, b, &first, &len)) return false;
+  const int c = place - (first / kChunk + b), slot = P.slots[b];
+  if (c < 0 || c >= (len + kChunk - 1) / kChunk || slot < 0 || slot >= P.num_slots) return false;
+  *t0 = (size_t)first + (size_t)c * kChunk;
+  *nt = min(kChunk, len - c * kChunk);
+  return true;
 }
 
 __device__ __forceinline__ f32x4 mma4(const f32x4 a, const f32x4 b, f32x4 c) {   // 16x16x16 in fp32
@@ -64,118 +104,93 @@ __device__ __forceinline__ void inverse_column(const float (*L)[kLd], float (*X)
     for (int r = 0; r < 4; ++r) X[16 * i + 4 * g + r][16 * J + i16] = x[i][r];
 }
 
-// One workgroup per (chunk, head); wave w makes rows 16 w .. 16 w + 15.
-template <bool DELTA>
+// SUM: a wave to a (chunk, head).
+__global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
+  const int l = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int place = (int)(unit / P.H), h = (int)(unit % P.H);
+  size_t t0;
+  int nt;
+  if (place >= P.chunks || !chunk_at(P, place, &t0, &nt)) return;
+  put_decays(P, t0, nt, h, l, chunk_space(P, place, h));
+}
+
+// DELTA: T and the decays.  One workgroup per (chunk, head); wave w makes
+// rows 16 w .. 16 w + 15 of L, inverts the diagonal block w by substitution,
+// then block column w of the inverse.  Everything fp32 but the exact products
+// of k.
 __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
-  __shared__ __attribute__((aligned(16))) float mat[2][kChunk][kLd];   // L; A, then X
+  __shared__ __attribute__((aligned(16))) float L[kChunk][kLd], X[kChunk][kLd];
   __shared__ double lg[kChunk];
   __shared__ __attribute__((aligned(16))) float bt[kChunk];
 
   const int place = blockIdx.x / P.H, h = blockIdx.x % P.H;
-  const int b = sequence_of(P.cu, P.n, kChunk, 1, place);
-  int first, len;
-  if (!rows_of(P.cu, P.T, b, &first, &len)) return;
-  const int c = place - (first / kChunk + b);
-  const int slot = P.slots[b];
-  if (c < 0 || c * kChunk >= len || slot < 0 || slot >= P.num_slots) return;
-  const int nt = min(kChunk, len - c * kChunk);
-  const size_t t0 = (size_t)first + (size_t)c * kChunk;
-
+  size_t t0;
+  int nt;
+  if (!chunk_at(P, place, &t0, &nt)) return;
   const int tid = threadIdx.x, l = tid & 63, g = l >> 4, i16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  float *ws = chunk_ws(P, place, h);
+  const ChunkSpace ws = chunk_space(P, place, h);
   const size_t row = (size_t)P.H * kD;
 
-  // rows of q and k as operands: lane (g, i) holds channels 32 s + 8 g .. of
-  // token 16 j + i, zero behind the sequence's end
-  auto load = [&](const uint16_t *x, int tile, Frag *f) {
+  // rows of k as operands: lane (g, i) holds channels 32 s + 8 g .. of token
+  // 16 j + i, zero behind the sequence's end
+  auto load = [&](int tile, Frag *f) {
     const int t = 16 * tile + i16;
-    const uint16_t *src = x + (t0 + (t < nt ? t : 0)) * row + (size_t)h * kD + 8 * g;
+    const uint16_t *src = P.k + (t0 + (t < nt ? t : 0)) * row + (size_t)h * kD + 8 * g;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       f[s].w = *(const u32x4_a4 *)(src + 32 * s);
       if (t >= nt) f[s].w = (u32x4){0, 0, 0, 0};
     }
   };
-  Frag q[4], k[4];
-  load(P.q, w, q);
-  load(P.k, w, k);
-
+  Frag k[4];
+  load(w, k);
   if (w == 0) {
-    const float a = l < nt ? P.gate[(t0 + l) * P.H + h] : 1.0f;
-    double x = a == 0.0f ? kLogZero : log2((double)a);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double y = __shfl_up(x, d);
-      if (l >= d) x += y;
-    }
-    lg[l] = x;
-    bt[l] = DELTA && l < nt ? P.beta[(t0 + l) * P.H + h] : 0.0f;
-    const double end = __shfl(x, 63);
-    ws[2 * kTriFloats + l] = exp2f((float)x);
-    ws[2 * kTriFloats + kChunk + l] = exp2f((float)(end - x));
+    lg[l] = put_decays(P, t0, nt, h, l, ws);
+    bt[l] = l < nt ? P.beta[(t0 + l) * P.H + h] : 0.0f;
   }
   __syncthreads();
-
   for (int j = 0; j <= w; ++j) {
     Frag kj[4];
-    load(P.k, j, kj);
-    f32x4 qk = {0, 0, 0, 0}, kk = {0, 0, 0, 0};
+    load(j, kj);
+    f32x4 kk = {0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      qk = mma(q[s], kj[s], qk);
-      if (DELTA) kk = mma(k[s], kj[s], kk);
-    }
+    for (int s = 0; s < 4; ++s) kk = mma(k[s], kj[s], kk);
     const int col = 16 * j + i16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w + 4 * g + r;
-      const float e = exp2f((float)(lg[t] - lg[col]));
-      mat[1][t][col] = t >= col ? qk[r] * e : 0.0f;
-      if (DELTA) mat[0][t][col] = t > col ? bt[t] * (kk[r] * e) : 0.0f;
+      L[t][col] = t > col ? bt[t] * (kk[r] * exp2f((float)(lg[t] - lg[col]))) : 0.0f;
     }
   }
   if ((w & 1) == 0) {   // the block above the diagonal that shares a fragment with it
 #pragma unroll
-    for (int r = 0; r < 4; ++r) mat[1][16 * w + 4 * g + r][16 * (w + 1) + i16] = 0.0f;
+    for (int r = 0; r < 4; ++r) X[16 * w + 4 * g + r][16 * (w + 1) + i16] = 0.0f;
   }
-  __syncthreads();
-
-  auto store = [&](float *dst, bool scale) {
-    for (int s = 0; s <= w >> 1; ++s) {
-      f32x4 lo = *(const f32x4 *)&mat[1][16 * w + i16][32 * s + 4 * g];
-      f32x4 hi = *(const f32x4 *)&mat[1][16 * w + i16][32 * s + 16 + 4 * g];
-      if (scale) {
-        lo *= *(const f32x4 *)&bt[32 * s + 4 * g];
-        hi *= *(const f32x4 *)&bt[32 * s + 16 + 4 * g];
-      }
-      float *f = dst + (size_t)(tri_frag(w) + s) * 512 + l * 4;
-      *(f32x4 *)f = lo;
-      *(f32x4 *)(f + 256) = hi;
-    }
-  };
-  store(ws, false);
-  if (!DELTA) return;
-
-  // diagonal block w: column j by forward substitution in lane j
+  // column j of the diagonal block in lane j
   if (l < 16) {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = l == i ? 1.0f : 0.0f;
 #pragma unroll
-      for (int m = 0; m < i; ++m) s = __builtin_fmaf(-mat[0][16 * w + i][16 * w + m], x[m], s);
+      for (int m = 0; m < i; ++m) s = __builtin_fmaf(-L[16 * w + i][16 * w + m], x[m], s);
       x[i] = s;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mat[1][16 * w + i][16 * w + l] = x[i];
+    for (int i = 0; i < 16; ++i) X[16 * w + i][16 * w + l] = x[i];
   }
   __syncthreads();
-  if (w == 0) inverse_column<0>(mat[0], mat[1], g, i16);
-  else if (w == 1) inverse_column<1>(mat[0], mat[1], g, i16);
-  else if (w == 2) inverse_column<2>(mat[0], mat[1], g, i16);
+  if (w == 0) inverse_column<0>(L, X, g, i16);
+  else if (w == 1) inverse_column<1>(L, X, g, i16);
+  else if (w == 2) inverse_column<2>(L, X, g, i16);
   __syncthreads();
-  store(ws + kTriFloats, true);
+  for (int s = 0; s <= w >> 1; ++s) {
+    float *f = ws.T + (size_t)(tri_frag(w) + s) * 512 + l * 4;
+    *(f32x4 *)f = *(const f32x4 *)&X[16 * w + i16][32 * s + 4 * g] * *(const f32x4 *)&bt[32 * s + 4 * g];
+    *(f32x4 *)(f + 256) = *(const f32x4 *)&X[16 * w + i16][32 * s + 16 + 4 * g] * *(const f32x4 *)&bt[32 * s + 16 + 4 * g];
+  }
 }
 
 // Eight fp32 values as P bfloat16 operands.
@@ -190,74 +205,132 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
   for (int x = 0; x < P; ++x) f[x].w = (u32x4){p[0][x], p[1][x], p[2][x], p[3][x]};
 }
 
-// What a chunk shares with every column: its left operands, 1 KiB each
-// ([lane] of 16 bytes), its values and its decays.
+// What a chunk shares with every column: left operands, 1 KiB each, values
+// and decays.  Rows of q and k lie in pieces of 8 channels; piece c of row i
+// of a tile is at 16 c + (i ^ c): whole rows come in without bank conflicts,
+// and operands and transposing reads go out so.
 template <bool DELTA>
 struct Stage {
-  u32x4 Q[4][4][64];                          // [token tile][channels 32 s + 8 g ..]
-  u32x4 K[4][4][64];
+  u32x4 Q[4][256], K[4][256];                 // [token tile]
   u32x4 A[kTriFrags][2][64];                  // two parts
   u32x4 T[DELTA ? kTriFrags : 1][3][64];      // three
-  uint16_t V[kChunk][136];
+  uint16_t V[kChunk][136];                    // then the readout
+  double lg[kChunk];
   float dec[2 * kChunk];                      // decays from the chunk's start, then to its end
 };
+static_assert(sizeof(Stage<true>) <= 80 * 1024, "two workgroups share a compute unit's 160 KiB");
+
+__device__ __forceinline__ int piece_at(int piece, int i) { return 16 * piece + (i ^ piece); }
+// Operand of rows: lane (g, i) has channels 32 s + 8 g .. of row i of a tile.
+__device__ __forceinline__ Frag rows_operand(const u32x4 *tile, int s, int l) {
+  Frag f;
+  f.w = tile[piece_at(4 * s + (l >> 4), l & 15)];
+  return f;
+}
 
 struct ScanAt {
   int first, len, chunks, place0, h;
   size_t row;
 };
 
-// Eight waves bring a chunk in (READ: also what only the readout needs).
+// A thread's share of a chunk on its way in (READ: also what only the readout
+// needs): pieces of 16 bytes of two rows, and of T.
 template <bool DELTA, bool READ>
-__device__ __forceinline__ void stage(const PromptArgs &P, const ScanAt &A, int c, int wave, int l, Stage<DELTA> &st) {
-  const int nt = min(kChunk, A.len - c * kChunk), g = l >> 4, tile = wave & 3, t = 16 * tile + (l & 15);
-  const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 64 * (wave >> 2) + 8 * g;
-  u32x4 q[2], k[2], v[2];
+struct StageIn {
+  u32x4 q[READ ? 2 : 1], k[2], v[2];
+  f32x4 T[2];
+  double lg;
+  float dec;
+};
+
+template <bool DELTA, bool READ>
+__device__ __forceinline__ void fetch(const PromptArgs &P, const ScanAt &A, int c, int tid, StageIn<DELTA, READ> &in) {
+  const int nt = min(kChunk, A.len - c * kChunk);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    k[x] = *(const u32x4_a4 *)(P.k + at + 32 * x);
-    v[x] = *(const u32x4_a4 *)(P.v + at + 32 * x);
-    if (READ) q[x] = *(const u32x4_a4 *)(P.q + at + 32 * x);
+    const int t = (tid >> 4) + 32 * x;
+    const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 8 * (tid & 15);
+    in.k[x] = *(const u32x4_a4 *)(P.k + at);
+    in.v[x] = *(const u32x4_a4 *)(P.v + at);
+    if (READ) in.q[READ ? x : 0] = *(const u32x4_a4 *)(P.q + at);
   }
-  const float *ws = chunk_ws(P, A.place0 + c, A.h);
-  // groups of 256 values: A's 12, then T's
-  constexpr int kGroups = (DELTA ? 4 : 2) * kTriFrags;
-  constexpr int kTri = DELTA ? 3 : READ ? 2 : 0;
-  f32x4 tri[3];
-#pragma unroll
-  for (int x = 0; x < kTri; ++x) {
-    const int group = wave + 8 * x;
-    tri[x] = *(const f32x4 *)(ws + (group < kGroups ? group : wave) * 256 + l * 4);
+  const ChunkSpace ws = chunk_space(P, A.place0 + c, A.h);
+  if (DELTA) {   // 12 groups of 256 values
+    in.T[0] = *(const f32x4 *)(ws.T + 4 * tid);
+    in.T[1] = *(const f32x4 *)(ws.T + 4 * (tid < 256 ? tid + 512 : tid));
   }
-  const float dec = ws[2 * kTriFloats + ((wave & 1) * 64 + l)];
-  if (t >= nt)   // nothing of the rows behind the end
-#pragma unroll
-    for (int x = 0; x < 2; ++x) q[x] = k[x] = v[x] = (u32x4){0, 0, 0, 0};
+  in.dec = ws.dec[tid & 127];
+  if (READ) in.lg = ws.lg[tid & 63];
+}
+
+template <bool DELTA, bool READ>
+__device__ __forceinline__ void put(const ScanAt &A, int c, int tid, const StageIn<DELTA, READ> &in, Stage<DELTA> &st) {
+  const int nt = A.len - c * kChunk, piece = tid & 15;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int s = 2 * (wave >> 2) + x;
-    if (READ) st.Q[tile][s][l] = q[x];
-    st.K[tile][s][l] = k[x];
-    *(u32x4 *)&st.V[t][32 * s + 8 * g] = v[x];
+    const int t = (tid >> 4) + 32 * x, at = piece_at(piece, t & 15);
+    const bool out = t >= nt;   // nothing of the rows behind the end
+    const u32x4 none = {0, 0, 0, 0};
+    if (READ) st.Q[t >> 4][at] = out ? none : in.q[READ ? x : 0];
+    st.K[t >> 4][at] = out ? none : in.k[x];
+    *(u32x4 *)&st.V[t][8 * piece] = out ? none : in.v[x];
   }
+  if (DELTA)
 #pragma unroll
-  for (int x = 0; x < kTri; ++x) {
-    const int group = wave + 8 * x;
-    uint32_t p[2][3];
-    if (group < 2 * kTriFrags) {
-      parts<2>(tri[x][0], tri[x][1], p[0]);
-      parts<2>(tri[x][2], tri[x][3], p[1]);
+    for (int x = 0; x < 2; ++x) {
+      const int group = (tid >> 6) + 8 * x, l = tid & 63;
+      if (group >= 2 * kTriFrags) continue;
+      uint32_t p[2][3];
+      parts<3>(in.T[x][0], in.T[x][1], p[0]);
+      parts<3>(in.T[x][2], in.T[x][3], p[1]);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) ((Frag *)&st.A[group >> 1][y][l])->h[group & 1] = (u32x2){p[0][y], p[1][y]};
-    } else if (DELTA) {
-      const int f = group - 2 * kTriFrags;
-      parts<3>(tri[x][0], tri[x][1], p[0]);
-      parts<3>(tri[x][2], tri[x][3], p[1]);
-#pragma unroll
-      for (int y = 0; y < 3; ++y) ((Frag *)&st.T[DELTA ? f >> 1 : 0][y][l])->h[f & 1] = (u32x2){p[0][y], p[1][y]};
+      for (int y = 0; y < 3; ++y) ((Frag *)&st.T[DELTA ? group >> 1 : 0][y][l])->h[group & 1] = (u32x2){p[0][y], p[1][y]};
     }
+  if (tid < 128) st.dec[tid] = in.dec;
+  if (READ && tid >= 448) st.lg[tid - 448] = in.lg;
+}
+
+// Tile (t, j) of A, as the left operand that it becomes: computed transposed
+// (rows are keys), its accumulators are half j & 1 of the operand's lanes.
+template <bool DELTA>
+__device__ __forceinline__ void put_tile(Stage<DELTA> &st, int t, int j, int l) {
+  const int g = l >> 4, i16 = l & 15;
+  f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) x = mma(rows_operand(st.K[j], s, l), rows_operand(st.Q[t], s, l), x);
+  const int query = 16 * t + i16, key = 16 * j + 4 * g;
+  const double to = st.lg[query];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = query >= key + r ? x[r] * exp2f((float)(to - st.lg[key + r])) : 0.0f;
+  uint32_t p[2][2];
+  parts<2>(x[0], x[1], p[0]);
+  parts<2>(x[2], x[3], p[1]);
+#pragma unroll
+  for (int y = 0; y < 2; ++y) ((Frag *)&st.A[tri_frag(t) + (j >> 1)][y][l])->h[j & 1] = (u32x2){p[0][y], p[1][y]};
+}
+// The ten tiles over eight waves; the halves above the diagonal are cleared
+// once, before the first chunk.
+template <bool DELTA>
+__device__ __forceinline__ void put_A(Stage<DELTA> &st, int wave, int l) {
+  const int t = wave < 4 ? 3 : wave < 7 ? 2 : 1, j = wave < 4 ? wave : wave < 7 ? wave - 4 : 0;
+#pragma unroll 1
+  for (int x = 0; x < (wave < 2 ? 2 : 1); ++x) put_tile<DELTA>(st, x ? wave : t, x ? wave : j, l);
+}
+template <bool DELTA>
+__device__ __forceinline__ void clear_A(Stage<DELTA> &st, int tid) {
+  if (tid < 256) ((Frag *)&st.A[tri_frag(tid < 128 ? 0 : 2) + (tid < 128 ? 0 : 1)][(tid >> 6) & 1][tid & 63])->h[1] = (u32x2){0, 0};
+}
+
+// The readout of a chunk, whole rows.
+template <bool DELTA>
+__device__ __forceinline__ void put_rows(const PromptArgs &P, const ScanAt &A, int c, int tid, const Stage<DELTA> &st) {
+  const int nt = A.len - c * kChunk;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t = (tid >> 4) + 32 * x;
+    if (t >= nt) continue;
+    *(u32x4_a4 *)(P.o + ((size_t)A.first + (size_t)c * kChunk + t) * A.row + (size_t)A.h * kD + 8 * (tid & 15)) = *(const u32x4 *)&st.V[t][8 * (tid & 15)];
   }
-  if (wave < 2) st.dec[wave * 64 + l] = dec;
 }
 
 // Row 4 g + r of result 2 s + i of the state is channel state_row(...) + r: a
@@ -278,7 +351,7 @@ __device__ __forceinline__ Frag transposed(const Stage<DELTA> &st, int m, int s,
   Frag f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][m >> 1][16 * j + 4 * g + r] + ((m & 1) ^ (j & 1));
+    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][piece_at(4 * (m >> 1) + j, 4 * g + r)] + ((m & 1) ^ (j & 1));
     f.h[half] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)piece));
   }
   return f;
@@ -304,6 +377,7 @@ __device__ __forceinline__ void update_state(const Stage<DELTA> &st, const f32x4
       for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
+      QDR_PLACE();
     }
   }
 }
@@ -313,8 +387,9 @@ __device__ __forceinline__ void update_state(const Stage<DELTA> &st, const f32x4
 // shared left operands is read from LDS, and nothing waits for another wave.
 // (Products of one accumulator never follow each other: four at a time.)
 template <bool DELTA>
-__device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, int c, int col0, int l, const Stage<DELTA> &st, f32x4 *S) {
-  const int g = l >> 4, i16 = l & 15, swap = g & 1;
+__device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4 *S) {
+  const int g = l >> 4, col = 16 * wave + (l & 15), swap = g & 1;
+  put_A<DELTA>(st, wave, l);
   f32x4 o[4], r[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) o[t] = r[t] = (f32x4){0, 0, 0, 0};
@@ -332,7 +407,7 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
     if (DELTA) {
       Frag k[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) k[t].w = st.K[t][s][l];
+      for (int t = 0; t < 4; ++t) k[t] = rows_operand(st.K[t], s, l);
 #pragma unroll
       for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -340,11 +415,12 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
     }
     Frag q[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) q[t].w = st.Q[t][s][l];
+    for (int t = 0; t < 4; ++t) q[t] = rows_operand(st.Q[t], s, l);
 #pragma unroll
     for (int x = 1; x >= 0; --x)
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f[x], o[t]);
+    QDR_PLACE();
   }
   f32x4 u[4];
 #pragma unroll
@@ -353,7 +429,7 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
     o[t] *= from;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float v = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][col0 + i16] << 16);
+      const float v = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][col] << 16);
       if (DELTA) r[t][x] = __builtin_fmaf(-from[x], r[t][x], v);
       else u[t][x] = v;
     }
@@ -374,9 +450,11 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
         for (int y = 2 - x; y >= 0; --y)
 #pragma unroll
           for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[y], u[t]);
+        QDR_PLACE();
       }
     }
   }
+  lds_barrier();   // A is there, and every wave has its values
   // O += A U
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -391,23 +469,17 @@ __device__ __forceinline__ void columns(const PromptArgs &P, const ScanAt &A, in
       for (int y = DELTA ? 1 - x : 0; y >= 0; --y)
 #pragma unroll
         for (int t = 2 * s; t < 4; ++t) o[t] = mma(a[t], U[y], o[t]);
+      QDR_PLACE();
     }
   }
-  // lanes of two neighbouring columns trade rows: two columns of a row a store
-  const int nt = min(kChunk, A.len - c * kChunk), odd = l & 1;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const uint32_t lo = pack_bf16(o[t][0], o[t][1]), hi = pack_bf16(o[t][2], o[t][3]);
-    const uint32_t own = odd ? hi : lo, give = odd ? lo : hi;
-    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);   // lane ^ 1
-    // rows 4 g + 2 odd, + 1 of columns i16 & 14, + 1
-    const uint32_t x = odd ? got : own, y = odd ? own : got;
-    const uint32_t r0 = __builtin_amdgcn_perm(y, x, 0x05040100u), r1 = __builtin_amdgcn_perm(y, x, 0x07060302u);
-    const int at = 16 * t + 4 * g + 2 * odd;
-    uint16_t *dst = P.o + ((size_t)A.first + (size_t)c * kChunk + at) * A.row + (size_t)A.h * kD + col0 + (i16 & 14);
-    if (at < nt) *(uint32_t *)dst = r0;
-    if (at + 1 < nt) *(uint32_t *)(dst + A.row) = r1;
-  }
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t y = pack_bf16(o[t][2 * x], o[t][2 * x + 1]);
+      st.V[16 * t + 4 * g + 2 * x][col] = (uint16_t)y;
+      st.V[16 * t + 4 * g + 2 * x + 1][col] = (uint16_t)(y >> 16);
+    }
   update_state<DELTA>(st, u, S, l);
 }
 
@@ -487,12 +559,20 @@ __global__ void __launch_bounds__(512, 4) k_prompt_scan(PromptArgs P) {
     else if (carried) S[m] = state.get(state_row(m, g), col);
     else S[m] = (f32x4){0, 0, 0, 0};
   }
+  clear_A<DELTA>(st, threadIdx.x);
   for (int c = from; c < to; ++c) {
-    stage<DELTA, true>(P, A, c, wave, l, st);
+    StageIn<DELTA, true> in;
+    fetch<DELTA, true>(P, A, c, threadIdx.x, in);
+    if (c > from) {
+      put_rows<DELTA>(P, A, c - 1, threadIdx.x, st);
+      lds_barrier();
+    }
+    put<DELTA, true>(A, c, threadIdx.x, in, st);
     lds_barrier();
-    columns<DELTA>(P, A, c, 16 * wave, l, st, S);
+    columns<DELTA>(wave, l, st, S);
     lds_barrier();
   }
+  if (to > from) put_rows<DELTA>(P, A, to - 1, threadIdx.x, st);
   // the last segment has the sequence's state; a slot without rows stays as it is
   if (to < A.chunks || (carried && A.len == 0)) return;
 #pragma unroll
@@ -514,7 +594,9 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
   for (int m = 0; m < 8; ++m) S[m] = (f32x4){0, 0, 0, 0};
   float decay = 1.0f;
   for (int c = from; c < to; ++c) {
-    stage<false, false>(P, A, c, wave, l, st);
+    StageIn<false, false> in;
+    fetch<false, false>(P, A, c, threadIdx.x, in);
+    put<false, false>(A, c, threadIdx.x, in, st);
     lds_barrier();
     f32x4 u[4];
 #pragma unroll
@@ -585,9 +667,8 @@ hipError_t launch_prompt_slots(const PromptArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st) {
-  const dim3 grid(a.chunks * a.H);
-  if (delta) hipLaunchKernelGGL(k_prompt_chunks<true>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_prompt_chunks<false>, grid, dim3(256), 0, st, a);
+  if (delta) hipLaunchKernelGGL(k_prompt_chunks, dim3(a.chunks * a.H), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_prompt_decays, dim3((uint32_t)(((int64_t)a.chunks * a.H + 3) / 4)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

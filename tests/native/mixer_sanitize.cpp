@@ -87,7 +87,7 @@ static int prompts() {
   view.num_heads = 2;
   view.all_fp32 = true;
   size_t need = 1;
-  CHECK(qdr_prompt_workspace(&pool, 1, 64, &need) == QDR_OK && need == 2 * 2 * (2 * 6 * 512 + 128) * 4);
+  CHECK(qdr_prompt_workspace(&pool, 1, 64, &need) == QDR_OK && need == 2 * 2 * (6 * 512 + 256) * 4);
   CHECK(qdr_prompt_workspace(&pool, 0, 64, &need) == QDR_OK && need == 0);
   REFUSED(qdr_prompt_workspace(nullptr, 1, 1, &need), QDR_E_INVAL);
   REFUSED(qdr_prompt_workspace(&pool, 1, 1, nullptr), QDR_E_INVAL);
