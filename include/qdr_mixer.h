@@ -63,7 +63,7 @@ qdr_status qdr_prompt_workspace(const qdr_pool *pool, int32_t n, int32_t T, size
  * qdr_decode_step (-1: the sequence is skipped and its o rows are 0).
  * Non-finite inputs reach only rows of their own (sequence, head), from the
  * first token of their 64-token chunk on.  A gate below 0 gives NaN there.
- * QDR_E_UNSUPPORTED for a pool with QDR_GATE_DIAG. */
+ * QDR_E_UNSUPPORTED for a pool with QDR_GATE_DIAG or more than 2^17 heads. */
 qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const int32_t *carry,
                       const int32_t *cu, int32_t n, int32_t T, const uint16_t *q, const uint16_t *k,
                       const uint16_t *v, const float *beta, const float *gate, uint16_t *o,

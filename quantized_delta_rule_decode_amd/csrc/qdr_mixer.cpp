@@ -31,6 +31,7 @@ qdr_status launched(hipError_t e) {
 // Counts of sequences and rows are kept where sums of them fit 32 bits, and
 // launches under 2^32 threads.
 constexpr int32_t kMostRows = 1 << 30;
+constexpr int32_t kMostHeads = 1 << 17;             // 64 rows of a token array under 2^32 bytes
 constexpr int64_t kMostGroups = (int64_t)1 << 24;   // of 256 threads
 
 qdr_status check_counts(int32_t n, int32_t T) {
@@ -227,6 +228,7 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
   if (!aligned4(q) || !aligned4(k) || !aligned4(v) || !aligned4(o)) return fail(QDR_E_INVAL, "tensors must be 4-byte aligned");
   const qdr::PoolView view = qdr::pool_view(pool);
   if (view.gate != QDR_GATE_SCALAR) return fail(QDR_E_UNSUPPORTED, "the prompt form takes one gate a head (QDR_GATE_SCALAR)");
+  if (view.num_heads > kMostHeads) return fail(QDR_E_UNSUPPORTED, "the prompt form takes at most %d heads (got %d)", kMostHeads, view.num_heads);
   QDR_TRY(check_device(view.device));
   const PromptSpace space = prompt_space(view, n, T);
   QDR_TRY(check_groups(space.places * view.num_heads));

@@ -243,16 +243,22 @@ struct StageIn {
   float dec;
 };
 
+// A uniform address and a 32-bit offset (the host keeps 64 rows under 2^32 bytes).
+__device__ __forceinline__ const u32x4_a4 *piece_of(const uint16_t *base, uint32_t offset) {
+  return (const u32x4_a4 *)((const uint8_t *)base + offset);
+}
+
 template <bool DELTA, bool READ>
 __device__ __forceinline__ void fetch(const PromptArgs &P, const ScanAt &A, int c, int tid, StageIn<DELTA, READ> &in) {
   const int nt = min(kChunk, A.len - c * kChunk);
+  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int t = (tid >> 4) + 32 * x;
-    const size_t at = ((size_t)A.first + (size_t)c * kChunk + (t < nt ? t : 0)) * A.row + (size_t)A.h * kD + 8 * (tid & 15);
-    in.k[x] = *(const u32x4_a4 *)(P.k + at);
-    in.v[x] = *(const u32x4_a4 *)(P.v + at);
-    if (READ) in.q[READ ? x : 0] = *(const u32x4_a4 *)(P.q + at);
+    const uint32_t at = (uint32_t)(t < nt ? t : 0) * (uint32_t)(2 * A.row) + 16 * (tid & 15);
+    in.k[x] = *piece_of(P.k + base, at);
+    in.v[x] = *piece_of(P.v + base, at);
+    if (READ) in.q[READ ? x : 0] = *piece_of(P.q + base, at);
   }
   const ChunkSpace ws = chunk_space(P, A.place0 + c, A.h);
   if (DELTA) {   // 12 groups of 256 values
@@ -301,7 +307,7 @@ __device__ __forceinline__ void put_tile(Stage<DELTA> &st, int t, int j, int l) 
   const int query = 16 * t + i16, key = 16 * j + 4 * g;
   const double to = st.lg[query];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = query >= key + r ? x[r] * exp2f((float)(to - st.lg[key + r])) : 0.0f;
+  for (int r = 0; r < 4; ++r) x[r] = query >= key + r ? x[r] * __builtin_amdgcn_exp2f((float)(to - st.lg[key + r])) : 0.0f;
   uint32_t p[2][2];
   parts<2>(x[0], x[1], p[0]);
   parts<2>(x[2], x[3], p[1]);
@@ -325,19 +331,19 @@ __device__ __forceinline__ void clear_A(Stage<DELTA> &st, int tid) {
 template <bool DELTA>
 __device__ __forceinline__ void put_rows(const PromptArgs &P, const ScanAt &A, int c, int tid, const Stage<DELTA> &st) {
   const int nt = A.len - c * kChunk;
+  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int t = (tid >> 4) + 32 * x;
     if (t >= nt) continue;
-    *(u32x4_a4 *)(P.o + ((size_t)A.first + (size_t)c * kChunk + t) * A.row + (size_t)A.h * kD + 8 * (tid & 15)) = *(const u32x4 *)&st.V[t][8 * (tid & 15)];
+    *(u32x4_a4 *)((uint8_t *)(P.o + base) + (uint32_t)t * (uint32_t)(2 * A.row) + 16 * (tid & 15)) = *(const u32x4 *)&st.V[t][8 * (tid & 15)];
   }
 }
 
-// Row 4 g + r of result 2 s + i of the state is channel state_row(...) + r: a
-// lane's two results of a contraction step are the eight channels that one
-// 16-byte piece of a row of q or k has.  Odd lane groups take its halves in
-// the other order, which spreads the transposing reads of K over all banks.
-__device__ __forceinline__ int state_row(int m, int g) { return 32 * (m >> 1) + 8 * g + 4 * ((m & 1) ^ (g & 1)); }
+// Row 4 g + r of result 2 s + i of the state is channel state_row(2 s + i) + r:
+// a lane's two results of a contraction step are the eight channels that one
+// 16-byte piece of a row of q or k has.
+__device__ __forceinline__ int state_row(int m, int g) { return 32 * (m >> 1) + 8 * g + 4 * (m & 1); }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -351,7 +357,7 @@ __device__ __forceinline__ Frag transposed(const Stage<DELTA> &st, int m, int s,
   Frag f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][piece_at(4 * (m >> 1) + j, 4 * g + r)] + ((m & 1) ^ (j & 1));
+    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][piece_at(4 * (m >> 1) + j, 4 * g + r)] + (m & 1);
     f.h[half] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)piece));
   }
   return f;
@@ -388,7 +394,7 @@ __device__ __forceinline__ void update_state(const Stage<DELTA> &st, const f32x4
 // (Products of one accumulator never follow each other: four at a time.)
 template <bool DELTA>
 __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4 *S) {
-  const int g = l >> 4, col = 16 * wave + (l & 15), swap = g & 1;
+  const int g = l >> 4, col = 16 * wave + (l & 15);
   put_A<DELTA>(st, wave, l);
   f32x4 o[4], r[4];
 #pragma unroll
@@ -397,13 +403,6 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
   for (int s = 0; s < 4; ++s) {
     Frag f[3];
     split8<DELTA ? 3 : 2>(S[2 * s], S[2 * s + 1], f);
-    // odd lane groups: the first result has the piece's second half
-#pragma unroll
-    for (int x = 0; x < (DELTA ? 3 : 2); ++x) {
-      const u32x2 a = f[x].h[0], b = f[x].h[1];
-      f[x].h[0] = swap ? b : a;
-      f[x].h[1] = swap ? a : b;
-    }
     if (DELTA) {
       Frag k[4];
 #pragma unroll
@@ -593,11 +592,12 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
 #pragma unroll
   for (int m = 0; m < 8; ++m) S[m] = (f32x4){0, 0, 0, 0};
   float decay = 1.0f;
+  StageIn<false, false> in;
+  fetch<false, false>(P, A, from, threadIdx.x, in);
   for (int c = from; c < to; ++c) {
-    StageIn<false, false> in;
-    fetch<false, false>(P, A, c, threadIdx.x, in);
     put<false, false>(A, c, threadIdx.x, in, st);
     lds_barrier();
+    fetch<false, false>(P, A, min(c + 1, to - 1), threadIdx.x, in);
     f32x4 u[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
