@@ -533,7 +533,7 @@ struct StateAt {
 // The chunks in order, a wave to sixteen columns.  Two workgroups a compute
 // unit: one stages while the other computes.
 template <bool DELTA>
-__global__ void __launch_bounds__(512, 4) k_prompt_scan(PromptArgs P) {
+__global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
   const int l = threadIdx.x & 63, g = l >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -559,15 +559,17 @@ __global__ void __launch_bounds__(512, 4) k_prompt_scan(PromptArgs P) {
     else S[m] = (f32x4){0, 0, 0, 0};
   }
   clear_A<DELTA>(st, threadIdx.x);
+  StageIn<DELTA, true> in;
+  if (DELTA && from < to) fetch<DELTA, true>(P, A, from, threadIdx.x, in);
   for (int c = from; c < to; ++c) {
-    StageIn<DELTA, true> in;
-    fetch<DELTA, true>(P, A, c, threadIdx.x, in);
+    if (!DELTA) fetch<DELTA, true>(P, A, c, threadIdx.x, in);
     if (c > from) {
       put_rows<DELTA>(P, A, c - 1, threadIdx.x, st);
       lds_barrier();
     }
     put<DELTA, true>(A, c, threadIdx.x, in, st);
     lds_barrier();
+    if (DELTA) fetch<DELTA, true>(P, A, min(c + 1, to - 1), threadIdx.x, in);
     columns<DELTA>(wave, l, st, S);
     lds_barrier();
   }
