@@ -298,33 +298,36 @@ __device__ __forceinline__ void put(const ScanAt &A, int c, int tid, const Stage
 
 // Tile (t, j) of A, as the left operand that it becomes: computed transposed
 // (rows are keys), its accumulators are half j & 1 of the operand's lanes.
-template <bool DELTA>
-__device__ __forceinline__ void put_tile(Stage<DELTA> &st, int t, int j, int l) {
+__device__ __forceinline__ void put_tile(const u32x4 *K, const Frag *q, const double *lg, u32x4 (*A)[2][64], int t, int j, int l) {
   const int g = l >> 4, i16 = l & 15;
   f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-  for (int s = 0; s < 4; ++s) x = mma(rows_operand(st.K[j], s, l), rows_operand(st.Q[t], s, l), x);
+  for (int s = 0; s < 4; ++s) x = mma(rows_operand(K, s, l), q[s], x);
   const int query = 16 * t + i16, key = 16 * j + 4 * g;
-  const double to = st.lg[query];
+  const double to = lg[query];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = query >= key + r ? x[r] * __builtin_amdgcn_exp2f((float)(to - st.lg[key + r])) : 0.0f;
+  for (int r = 0; r < 4; ++r) x[r] = query >= key + r ? x[r] * __builtin_amdgcn_exp2f((float)(to - lg[key + r])) : 0.0f;
   uint32_t p[2][2];
   parts<2>(x[0], x[1], p[0]);
   parts<2>(x[2], x[3], p[1]);
 #pragma unroll
-  for (int y = 0; y < 2; ++y) ((Frag *)&st.A[tri_frag(t) + (j >> 1)][y][l])->h[j & 1] = (u32x2){p[0][y], p[1][y]};
+  for (int y = 0; y < 2; ++y) ((Frag *)&A[tri_frag(t) + (j >> 1)][y][l])->h[j & 1] = (u32x2){p[0][y], p[1][y]};
 }
 // The ten tiles over eight waves; the halves above the diagonal are cleared
 // once, before the first chunk.
 template <bool DELTA>
 __device__ __forceinline__ void put_A(Stage<DELTA> &st, int wave, int l) {
-  const int t = wave < 4 ? 3 : wave < 7 ? 2 : 1, j = wave < 4 ? wave : wave < 7 ? wave - 4 : 0;
 #pragma unroll 1
-  for (int x = 0; x < (wave < 2 ? 2 : 1); ++x) put_tile<DELTA>(st, x ? wave : t, x ? wave : j, l);
+  for (int x = 0; x < (wave < 2 ? 2 : 1); ++x) {
+    const int t = x ? wave : wave < 4 ? 3 : wave < 7 ? 2 : 1, j = x ? wave : wave < 4 ? wave : wave < 7 ? wave - 4 : 0;
+    Frag q[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) q[s] = rows_operand(st.Q[t], s, l);
+    put_tile(st.K[j], q, st.lg, st.A, t, j, l);
+  }
 }
-template <bool DELTA>
-__device__ __forceinline__ void clear_A(Stage<DELTA> &st, int tid) {
-  if (tid < 256) ((Frag *)&st.A[tri_frag(tid < 128 ? 0 : 2) + (tid < 128 ? 0 : 1)][(tid >> 6) & 1][tid & 63])->h[1] = (u32x2){0, 0};
+__device__ __forceinline__ void clear_A(u32x4 (*A)[2][64], int tid) {
+  if (tid < 256) ((Frag *)&A[tri_frag(tid < 128 ? 0 : 2) + (tid < 128 ? 0 : 1)][(tid >> 6) & 1][tid & 63])->h[1] = (u32x2){0, 0};
 }
 
 // The readout of a chunk, whole rows.
@@ -350,39 +353,59 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // Operand of K^T: rows (channels) of result m, tokens 32 s + {4 g.., 16 + 4 g..}.
 // A transposing read gives lane i of a group of 16 the i-th of 16 columns of
 // four rows; the group's lane 4 r + j points to columns 4 j .. of row r.
-template <bool DELTA>
-__device__ __forceinline__ Frag transposed(const Stage<DELTA> &st, int m, int s, int l) {
+__device__ __forceinline__ Frag transposed(const u32x4 (*K)[256], int m, int s, int l) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const int g = l >> 4, r = (l >> 2) & 3, j = l & 3;
   Frag f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const u32x2 *piece = (const u32x2 *)&st.K[2 * s + half][piece_at(4 * (m >> 1) + j, 4 * g + r)] + (m & 1);
+    const u32x2 *piece = (const u32x2 *)&K[2 * s + half][piece_at(4 * (m >> 1) + j, 4 * g + r)] + (m & 1);
     f.h[half] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)piece));
   }
   return f;
 }
 
 // S = 2^g_63 S + K^T diag(2^(g_63 - g)) U.
-template <bool DELTA>
-__device__ __forceinline__ void update_state(const Stage<DELTA> &st, const f32x4 *u, f32x4 *S, int l) {
+__device__ __forceinline__ void update_state(const u32x4 (*K)[256], const float *dec, const f32x4 *u, f32x4 *S, int l) {
   const int g = l >> 4;
-  const float all = st.dec[kChunk - 1];
+  const float all = dec[kChunk - 1];
 #pragma unroll
   for (int m = 0; m < 8; ++m) S[m] *= all;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     Frag d[3];
-    split8<3>(u[2 * s] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 4 * g], u[2 * s + 1] * *(const f32x4 *)&st.dec[kChunk + 32 * s + 16 + 4 * g], d);
+    split8<3>(u[2 * s] * *(const f32x4 *)&dec[kChunk + 32 * s + 4 * g], u[2 * s + 1] * *(const f32x4 *)&dec[kChunk + 32 * s + 16 + 4 * g], d);
 #pragma unroll
     for (int half = 0; half < 8; half += 4) {
       Frag k[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) k[m] = transposed<DELTA>(st, half + m, s, l);
+      for (int m = 0; m < 4; ++m) k[m] = transposed(K, half + m, s, l);
 #pragma unroll
       for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
+      QDR_PLACE();
+    }
+  }
+}
+
+// U = T R.
+__device__ __forceinline__ void solve(const u32x4 (*T)[3][64], const f32x4 *r, f32x4 *u, int l) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) u[t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Frag R[3];
+    split8<3>(r[2 * s], r[2 * s + 1], R);
+#pragma unroll
+    for (int x = 2; x >= 0; --x) {
+      Frag a[4];
+#pragma unroll
+      for (int t = 2 * s; t < 4; ++t) a[t].w = T[tri_frag(t) + s][x][l];
+#pragma unroll
+      for (int y = 2 - x; y >= 0; --y)
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[y], u[t]);
       QDR_PLACE();
     }
   }
@@ -433,26 +456,7 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
       else u[t][x] = v;
     }
   }
-  if (DELTA) {   // U = T R
-#pragma unroll
-    for (int t = 0; t < 4; ++t) u[t] = (f32x4){0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Frag R[3];
-      split8<3>(r[2 * s], r[2 * s + 1], R);
-#pragma unroll
-      for (int x = 2; x >= 0; --x) {
-        Frag a[4];
-#pragma unroll
-        for (int t = 2 * s; t < 4; ++t) a[t].w = st.T[DELTA ? tri_frag(t) + s : 0][x][l];
-#pragma unroll
-        for (int y = 2 - x; y >= 0; --y)
-#pragma unroll
-          for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[y], u[t]);
-        QDR_PLACE();
-      }
-    }
-  }
+  if (DELTA) solve(st.T, r, u, l);
   lds_barrier();   // A is there, and every wave has its values
   // O += A U
 #pragma unroll
@@ -479,7 +483,7 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
       st.V[16 * t + 4 * g + 2 * x][col] = (uint16_t)y;
       st.V[16 * t + 4 * g + 2 * x + 1][col] = (uint16_t)(y >> 16);
     }
-  update_state<DELTA>(st, u, S, l);
+  update_state(st.K, st.dec, u, S, l);
 }
 
 // Which chunks of which sequence a workgroup takes: a whole sequence, or with
@@ -558,7 +562,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
     else if (carried) S[m] = state.get(state_row(m, g), col);
     else S[m] = (f32x4){0, 0, 0, 0};
   }
-  clear_A<DELTA>(st, threadIdx.x);
+  clear_A(st.A, threadIdx.x);
   StageIn<DELTA, true> in;
   if (DELTA && from < to) fetch<DELTA, true>(P, A, from, threadIdx.x, in);
   for (int c = from; c < to; ++c) {
@@ -576,6 +580,271 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
   if (to > from) put_rows<DELTA>(P, A, to - 1, threadIdx.x, st);
   // the last segment has the sequence's state; a slot without rows stays as it is
   if (to < A.chunks || (carried && A.len == 0)) return;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) state.set(state_row(m, g), col, S[m]);
+}
+
+// DELTA with few heads: what counts is how long one chunk takes, for they
+// follow each other.  A workgroup takes 32 columns of one (sequence, head),
+// and its waves work on three chunks at once, one barrier a chunk:
+//   0, 1   the chain from state to state, sixteen columns each (chunk c);
+//   2, 3   the readout of their columns: Q S of chunk c, A U of chunk c - 1;
+//   4 .. 7 A of chunk c, and chunk c + 1 on its way into LDS.
+struct ChainShared {
+  struct Part {                       // chunk c in part c & 1
+    u32x4 K[4][256], T[kTriFrags][3][64];
+    uint16_t V[kChunk][40];
+    float dec[2 * kChunk];
+    double lg[kChunk];
+  } part[2];
+  u32x4 A[2][kTriFrags][2][64];
+  u32x4 S[2][2][4][2][64];            // [c & 1][columns][contraction step][part]: state before chunk c
+  u32x4 U[2][2][2][2][64];
+};
+static_assert(sizeof(ChainShared) <= 160 * 1024, "one workgroup has a compute unit's LDS");
+
+__device__ __forceinline__ void split_state(const f32x4 *S, Frag (*f)[3], u32x4 (*to)[2][64], int l) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    split8<3>(S[2 * s], S[2 * s + 1], f[s]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) to[s][x][l] = f[s][x].w;
+  }
+}
+
+// Waves 0, 1.
+__device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &sh, int group, Frag (*f)[3], f32x4 *S) {
+  const int g = l >> 4;
+  const ChainShared::Part &p = sh.part[c & 1];
+  f32x4 r[4], u[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) r[t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    Frag k[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) k[t] = rows_operand(p.K[t], s, l);
+#pragma unroll
+    for (int x = 2; x >= 0; --x)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[s][x], r[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const f32x4 from = *(const f32x4 *)&p.dec[16 * t + 4 * g];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      r[t][x] = __builtin_fmaf(-from[x], r[t][x], __uint_as_float((uint32_t)p.V[16 * t + 4 * g + x][col] << 16));
+  }
+  solve(p.T, r, u, l);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Frag U[2];
+    split8<2>(u[2 * s], u[2 * s + 1], U);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) sh.U[c & 1][group][s][x][l] = U[x].w;
+  }
+  update_state(p.K, p.dec, u, S, l);
+  split_state(S, f, sh.S[(c + 1) & 1][group], l);
+}
+
+// Waves 4 .. 7: a thread's share of a chunk on its way in, and the rows of q
+// that its wave needs for A.
+struct HelpIn {
+  u32x4 k[4], v;
+  f32x4 T[3];
+  Frag q[4];
+  double lg;
+  float dec;
+};
+
+__device__ __forceinline__ void load_q(const PromptArgs &P, const ScanAt &A, int c, int tile, int l, Frag *q) {
+  const int nt = min(kChunk, A.len - c * kChunk), t = 16 * tile + (l & 15);
+  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    q[s].w = *piece_of(P.q + base, (uint32_t)(t < nt ? t : 0) * (uint32_t)(2 * A.row) + 64 * s + 16 * (l >> 4));
+}
+__device__ __forceinline__ void clear_q(const ScanAt &A, int c, int tile, int l, Frag *q) {
+  if (A.len - c * kChunk <= 16 * tile + (l & 15))
+#pragma unroll
+    for (int s = 0; s < 4; ++s) q[s].w = (u32x4){0, 0, 0, 0};
+}
+
+__device__ __forceinline__ void help_fetch(const PromptArgs &P, const ScanAt &A, int c, int col0, int tid, HelpIn &in) {
+  const int nt = min(kChunk, A.len - c * kChunk);
+  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
+  auto offset = [&](int t) { return (uint32_t)(t < nt ? t : 0) * (uint32_t)(2 * A.row); };
+#pragma unroll
+  for (int x = 0; x < 4; ++x) in.k[x] = *piece_of(P.k + base, offset((tid >> 4) + 16 * x) + 16 * (tid & 15));
+  in.v = *piece_of(P.v + base + col0, offset(tid >> 2) + 16 * (tid & 3));
+  const ChunkSpace ws = chunk_space(P, A.place0 + c, A.h);
+#pragma unroll
+  for (int x = 0; x < 3; ++x) in.T[x] = *(const f32x4 *)(ws.T + 4 * (tid + 256 * x));
+  in.lg = ws.lg[tid & 63];
+  in.dec = ws.dec[tid & 127];
+}
+
+__device__ __forceinline__ void help_put(const ScanAt &A, int c, int tid, const HelpIn &in, ChainShared::Part &p) {
+  const int nt = A.len - c * kChunk, piece = tid & 15, l = tid & 63;
+  const u32x4 none = {0, 0, 0, 0};   // nothing of the rows behind the end
+#pragma unroll
+  for (int x = 0; x < 4; ++x) p.K[x][piece_at(piece, tid >> 4)] = (tid >> 4) + 16 * x >= nt ? none : in.k[x];
+  *(u32x4 *)&p.V[tid >> 2][8 * (tid & 3)] = tid >> 2 >= nt ? none : in.v;
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int group = (tid >> 6) + 4 * x;
+    uint32_t y[2][3];
+    parts<3>(in.T[x][0], in.T[x][1], y[0]);
+    parts<3>(in.T[x][2], in.T[x][3], y[1]);
+#pragma unroll
+    for (int z = 0; z < 3; ++z) ((Frag *)&p.T[group >> 1][z][l])->h[group & 1] = (u32x2){y[0][z], y[1][z]};
+  }
+  if (tid < 64) p.lg[tid] = in.lg;
+  else if (tid >= 128) p.dec[tid - 128] = in.dec;
+}
+
+// Waves 2, 3.
+__device__ __forceinline__ void read_state(const ScanAt &A, int c, int l, Frag (*q)[4], const ChainShared &sh, int group, f32x4 *o) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    clear_q(A, c, t, l, q[t]);
+    o[t] = (f32x4){0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int x = 1; x >= 0; --x) {
+      Frag f;
+      f.w = sh.S[c & 1][group][s][x][l];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] = mma(q[t][s], f, o[t]);
+    }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] *= *(const f32x4 *)&sh.part[c & 1].dec[16 * t + 4 * (l >> 4)];
+}
+
+__device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A, int c, int col0, int l, const ChainShared &sh, int group, f32x4 *o) {
+  const int g = l >> 4, i16 = l & 15, odd = l & 1, nt = A.len - c * kChunk;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Frag U[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) U[x].w = sh.U[c & 1][group][s][x][l];
+#pragma unroll
+    for (int x = 1; x >= 0; --x)
+#pragma unroll
+      for (int y = 1 - x; y >= 0; --y)
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) {
+          Frag a;
+          a.w = sh.A[c & 1][tri_frag(t) + s][x][l];
+          o[t] = mma(a, U[y], o[t]);
+        }
+  }
+  // lanes of two neighbouring columns trade rows: two columns of a row a store
+  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD + col0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t lo = pack_bf16(o[t][0], o[t][1]), hi = pack_bf16(o[t][2], o[t][3]);
+    const uint32_t own = odd ? hi : lo, give = odd ? lo : hi;
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+    // rows 4 g + 2 odd, + 1 of columns i16 & 14, + 1
+    const uint32_t x = odd ? got : own, y = odd ? own : got;
+    const int at = 16 * t + 4 * g + 2 * odd;
+    uint8_t *dst = (uint8_t *)(P.o + base) + (uint32_t)at * (uint32_t)(2 * A.row) + 2 * (i16 & 14);
+    if (at < nt) *(uint32_t *)dst = __builtin_amdgcn_perm(y, x, 0x05040100u);
+    if (at + 1 < nt) *(uint32_t *)(dst + 2 * A.row) = __builtin_amdgcn_perm(y, x, 0x07060302u);
+  }
+}
+
+__global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
+  __shared__ __attribute__((aligned(16))) ChainShared sh;
+  // the four slices of a (sequence, head) go to one XCD (workgroups are dealt
+  // to the eight in turn) and share its rows through one L2
+  const int bh = blockIdx.x / 32 * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % 4;
+  if (bh >= P.n * P.H) return;
+  const int l = threadIdx.x & 63, g = l >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int b, from, to, segments;
+  ScanAt A;
+  A.h = bh % P.H;
+  if (!scan_at(P, bh / P.H, &b, &from, &to, &segments, A)) return;
+  const int slot = P.slots[b];
+  if (slot < 0 || slot >= P.num_slots) {
+    if (slot != -1 && threadIdx.x == 0) atomicOr(P.err, kErrSlot);
+    for (size_t i = threadIdx.x; i < (size_t)A.len * 32; i += 512)
+      P.o[((size_t)A.first + i / 32) * A.row + (size_t)A.h * kD + 32 * slice + i % 32] = 0;
+    return;
+  }
+  const int chunks = A.chunks, group = wave & 1, col0 = 32 * slice + 16 * group;
+  // Every wave passes chunks + 1 barriers; behind barrier c chunk c is in its
+  // part and the state before it in S.  Loads are always there (the last chunk
+  // asks for itself again): the waits count those behind the ones they need.
+  if (wave >= 4) {
+    if (chunks == 0) return;
+    const int tid = threadIdx.x - 256, tile = wave - 4;
+    HelpIn in;
+    help_fetch(P, A, 0, 32 * slice, tid, in);
+    clear_A(sh.A[0], tid);
+    clear_A(sh.A[1], tid);
+    help_put(A, 0, tid, in, sh.part[0]);
+    load_q(P, A, 0, tile, l, in.q);
+    help_fetch(P, A, min(1, chunks - 1), 32 * slice, tid, in);
+    lds_barrier();
+    for (int c = 0; c < chunks; ++c) {
+      Frag q[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) q[s] = in.q[s];
+      clear_q(A, c, tile, l, q);
+      if (c + 1 < chunks) help_put(A, c + 1, tid, in, sh.part[(c + 1) & 1]);
+      load_q(P, A, min(c + 1, chunks - 1), tile, l, in.q);
+      help_fetch(P, A, min(c + 2, chunks - 1), 32 * slice, tid, in);
+      for (int j = 0; j <= tile; ++j) put_tile(sh.part[c & 1].K[j], q, sh.part[c & 1].lg, sh.A[c & 1], tile, j, l);
+      lds_barrier();
+    }
+    return;
+  }
+  if (wave >= 2) {
+    if (chunks == 0) return;
+    Frag even[4][4], odd[4][4];
+    f32x4 o[4];
+    auto load = [&](int c, Frag (*q)[4]) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) load_q(P, A, min(c, chunks - 1), t, l, q[t]);
+    };
+    load(0, even);
+    lds_barrier();
+    for (int c = 0; c < chunks; c += 2) {
+      load(c + 1, odd);
+      if (c > 0) read_chunk(P, A, c - 1, col0, l, sh, group, o);
+      read_state(A, c, l, even, sh, group, o);
+      lds_barrier();
+      if (c + 1 >= chunks) break;
+      load(c + 2, even);
+      read_chunk(P, A, c, col0, l, sh, group, o);
+      read_state(A, c + 1, l, odd, sh, group, o);
+      lds_barrier();
+    }
+    read_chunk(P, A, chunks - 1, col0, l, sh, group, o);
+    return;
+  }
+  const bool carried = P.carry != nullptr && P.carry[b] != 0;
+  const StateAt state(P, b, slot, A.h);
+  const int col = col0 + (l & 15);
+  f32x4 S[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) S[m] = carried ? state.get(state_row(m, g), col) : (f32x4){0, 0, 0, 0};
+  if (chunks > 0) {
+    Frag f[4][3];
+    split_state(S, f, sh.S[0][group], l);
+    lds_barrier();
+    for (int c = 0; c < chunks; ++c) {
+      chain_chunk(c, 16 * group + (l & 15), l, sh, group, f, S);
+      lds_barrier();
+    }
+  }
+  if (carried && A.len == 0) return;   // the slot stays as it is
 #pragma unroll
   for (int m = 0; m < 8; ++m) state.set(state_row(m, g), col, S[m]);
 }
@@ -606,7 +875,7 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         u[t][x] = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][16 * wave + i16] << 16);
-    update_state<false>(st, u, S, l);
+    update_state(st.K, st.dec, u, S, l);
     decay *= st.dec[kChunk - 1];
     lds_barrier();
   }
@@ -677,7 +946,10 @@ hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st)
 hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
   if (delta) {
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
+    // few heads: their chains side by side, four workgroups to each, as long as
+    // all of them are resident at once (256 compute units)
+    if ((int64_t)a.n * a.H <= 64) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
+    else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
   }
   if (a.segment) {
