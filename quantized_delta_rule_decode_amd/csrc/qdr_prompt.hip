@@ -586,20 +586,22 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
 
 // DELTA with few heads: what counts is how long one chunk takes, for they
 // follow each other.  A workgroup takes 32 columns of one (sequence, head),
-// and its waves work on three chunks at once, one barrier a chunk:
-//   0, 1   the chain from state to state, sixteen columns each (chunk c);
-//   2, 3   the readout of their columns: Q S of chunk c, A U of chunk c - 1;
-//   4 .. 7 A of chunk c, and chunk c + 1 on its way into LDS.
+// and its waves work on three chunks at once.  Between two barriers at a
+// chunk's ends there is one in its middle:
+//   waves      before it                          after it
+//   0, 1       K S, U (sixteen columns each)      U out, the state, S out
+//   2, 3       A U of the chunk before, Q S       A
+//   4 .. 7     the next chunk into LDS            A
 struct ChainShared {
   struct Part {                       // chunk c in part c & 1
-    u32x4 K[4][256], T[kTriFrags][3][64];
+    u32x4 Q[4][256], K[4][256], T[kTriFrags][3][64];
     uint16_t V[kChunk][40];
     float dec[2 * kChunk];
     double lg[kChunk];
   } part[2];
-  u32x4 A[2][kTriFrags][2][64];
-  u32x4 S[2][2][4][2][64];            // [c & 1][columns][contraction step][part]: state before chunk c
-  u32x4 U[2][2][2][2][64];
+  u32x4 A[kTriFrags][2][64];
+  u32x4 S[2][4][2][64];               // [columns][contraction step][part]: the state before the chunk
+  u32x4 U[2][2][2][64];
 };
 static_assert(sizeof(ChainShared) <= 160 * 1024, "one workgroup has a compute unit's LDS");
 
@@ -637,46 +639,36 @@ __device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &
       r[t][x] = __builtin_fmaf(-from[x], r[t][x], __uint_as_float((uint32_t)p.V[16 * t + 4 * g + x][col] << 16));
   }
   solve(p.T, r, u, l);
+  lds_barrier();
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     Frag U[2];
     split8<2>(u[2 * s], u[2 * s + 1], U);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) sh.U[c & 1][group][s][x][l] = U[x].w;
+    for (int x = 0; x < 2; ++x) sh.U[group][s][x][l] = U[x].w;
   }
   update_state(p.K, p.dec, u, S, l);
-  split_state(S, f, sh.S[(c + 1) & 1][group], l);
+  split_state(S, f, sh.S[group], l);
 }
 
-// Waves 4 .. 7: a thread's share of a chunk on its way in, and the rows of q
-// that its wave needs for A.
+// Waves 4 .. 7: a thread's share of a chunk on its way in.
 struct HelpIn {
-  u32x4 k[4], v;
+  u32x4 q[4], k[4], v;
   f32x4 T[3];
-  Frag q[4];
   double lg;
   float dec;
 };
-
-__device__ __forceinline__ void load_q(const PromptArgs &P, const ScanAt &A, int c, int tile, int l, Frag *q) {
-  const int nt = min(kChunk, A.len - c * kChunk), t = 16 * tile + (l & 15);
-  const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-    q[s].w = *piece_of(P.q + base, (uint32_t)(t < nt ? t : 0) * (uint32_t)(2 * A.row) + 64 * s + 16 * (l >> 4));
-}
-__device__ __forceinline__ void clear_q(const ScanAt &A, int c, int tile, int l, Frag *q) {
-  if (A.len - c * kChunk <= 16 * tile + (l & 15))
-#pragma unroll
-    for (int s = 0; s < 4; ++s) q[s].w = (u32x4){0, 0, 0, 0};
-}
 
 __device__ __forceinline__ void help_fetch(const PromptArgs &P, const ScanAt &A, int c, int col0, int tid, HelpIn &in) {
   const int nt = min(kChunk, A.len - c * kChunk);
   const size_t base = ((size_t)A.first + (size_t)c * kChunk) * A.row + (size_t)A.h * kD;
   auto offset = [&](int t) { return (uint32_t)(t < nt ? t : 0) * (uint32_t)(2 * A.row); };
 #pragma unroll
-  for (int x = 0; x < 4; ++x) in.k[x] = *piece_of(P.k + base, offset((tid >> 4) + 16 * x) + 16 * (tid & 15));
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t at = offset((tid >> 4) + 16 * x) + 16 * (tid & 15);
+    in.k[x] = *piece_of(P.k + base, at);
+    in.q[x] = *piece_of(P.q + base, at);
+  }
   in.v = *piece_of(P.v + base + col0, offset(tid >> 2) + 16 * (tid & 3));
   const ChunkSpace ws = chunk_space(P, A.place0 + c, A.h);
 #pragma unroll
@@ -686,10 +678,14 @@ __device__ __forceinline__ void help_fetch(const PromptArgs &P, const ScanAt &A,
 }
 
 __device__ __forceinline__ void help_put(const ScanAt &A, int c, int tid, const HelpIn &in, ChainShared::Part &p) {
-  const int nt = A.len - c * kChunk, piece = tid & 15, l = tid & 63;
+  const int nt = A.len - c * kChunk, piece = tid & 15, l = tid & 63, at = piece_at(piece, tid >> 4);
   const u32x4 none = {0, 0, 0, 0};   // nothing of the rows behind the end
 #pragma unroll
-  for (int x = 0; x < 4; ++x) p.K[x][piece_at(piece, tid >> 4)] = (tid >> 4) + 16 * x >= nt ? none : in.k[x];
+  for (int x = 0; x < 4; ++x) {
+    const bool out = (tid >> 4) + 16 * x >= nt;
+    p.K[x][at] = out ? none : in.k[x];
+    p.Q[x][at] = out ? none : in.q[x];
+  }
   *(u32x4 *)&p.V[tid >> 2][8 * (tid & 3)] = tid >> 2 >= nt ? none : in.v;
 #pragma unroll
   for (int x = 0; x < 3; ++x) {
@@ -704,24 +700,38 @@ __device__ __forceinline__ void help_put(const ScanAt &A, int c, int tid, const 
   else if (tid >= 128) p.dec[tid - 128] = in.dec;
 }
 
-// Waves 2, 3.
-__device__ __forceinline__ void read_state(const ScanAt &A, int c, int l, Frag (*q)[4], const ChainShared &sh, int group, f32x4 *o) {
+// A's ten tiles over waves 2 .. 7.
+__device__ __forceinline__ void help_A(const ChainShared::Part &p, u32x4 (*A)[2][64], int wave, int l) {
+#pragma unroll 1
+  for (int i = wave - 2; i < 10; i += 6) {
+    const int t = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, j = i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0;
+    Frag q[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    clear_q(A, c, t, l, q[t]);
-    o[t] = (f32x4){0, 0, 0, 0};
+    for (int s = 0; s < 4; ++s) q[s] = rows_operand(p.Q[t], s, l);
+    put_tile(p.K[j], q, p.lg, A, t, j, l);
   }
+}
+
+// Waves 2, 3.
+__device__ __forceinline__ void read_state(int c, int l, const ChainShared &sh, int group, f32x4 *o) {
+  const ChainShared::Part &p = sh.part[c & 1];
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int t = 0; t < 4; ++t) o[t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    Frag q[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) q[t] = rows_operand(p.Q[t], s, l);
 #pragma unroll
     for (int x = 1; x >= 0; --x) {
       Frag f;
-      f.w = sh.S[c & 1][group][s][x][l];
+      f.w = sh.S[group][s][x][l];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] = mma(q[t][s], f, o[t]);
+      for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f, o[t]);
     }
+  }
 #pragma unroll
-  for (int t = 0; t < 4; ++t) o[t] *= *(const f32x4 *)&sh.part[c & 1].dec[16 * t + 4 * (l >> 4)];
+  for (int t = 0; t < 4; ++t) o[t] *= *(const f32x4 *)&p.dec[16 * t + 4 * (l >> 4)];
 }
 
 __device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A, int c, int col0, int l, const ChainShared &sh, int group, f32x4 *o) {
@@ -730,7 +740,7 @@ __device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A,
   for (int s = 0; s < 2; ++s) {
     Frag U[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) U[x].w = sh.U[c & 1][group][s][x][l];
+    for (int x = 0; x < 2; ++x) U[x].w = sh.U[group][s][x][l];
 #pragma unroll
     for (int x = 1; x >= 0; --x)
 #pragma unroll
@@ -738,7 +748,7 @@ __device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A,
 #pragma unroll
         for (int t = 2 * s; t < 4; ++t) {
           Frag a;
-          a.w = sh.A[c & 1][tri_frag(t) + s][x][l];
+          a.w = sh.A[tri_frag(t) + s][x][l];
           o[t] = mma(a, U[y], o[t]);
         }
   }
@@ -778,52 +788,35 @@ __global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
     return;
   }
   const int chunks = A.chunks, group = wave & 1, col0 = 32 * slice + 16 * group;
-  // Every wave passes chunks + 1 barriers; behind barrier c chunk c is in its
-  // part and the state before it in S.  Loads are always there (the last chunk
-  // asks for itself again): the waits count those behind the ones they need.
+  // Every wave passes 2 chunks + 1 barriers.  Loads are always there (the last
+  // chunk asks for itself again): the waits count those behind the ones they need.
   if (wave >= 4) {
     if (chunks == 0) return;
-    const int tid = threadIdx.x - 256, tile = wave - 4;
+    const int tid = threadIdx.x - 256;
     HelpIn in;
     help_fetch(P, A, 0, 32 * slice, tid, in);
-    clear_A(sh.A[0], tid);
-    clear_A(sh.A[1], tid);
+    clear_A(sh.A, tid);
     help_put(A, 0, tid, in, sh.part[0]);
-    load_q(P, A, 0, tile, l, in.q);
     help_fetch(P, A, min(1, chunks - 1), 32 * slice, tid, in);
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
-      Frag q[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) q[s] = in.q[s];
-      clear_q(A, c, tile, l, q);
       if (c + 1 < chunks) help_put(A, c + 1, tid, in, sh.part[(c + 1) & 1]);
-      load_q(P, A, min(c + 1, chunks - 1), tile, l, in.q);
       help_fetch(P, A, min(c + 2, chunks - 1), 32 * slice, tid, in);
-      for (int j = 0; j <= tile; ++j) put_tile(sh.part[c & 1].K[j], q, sh.part[c & 1].lg, sh.A[c & 1], tile, j, l);
+      lds_barrier();
+      help_A(sh.part[c & 1], sh.A, wave, l);
       lds_barrier();
     }
     return;
   }
   if (wave >= 2) {
     if (chunks == 0) return;
-    Frag even[4][4], odd[4][4];
     f32x4 o[4];
-    auto load = [&](int c, Frag (*q)[4]) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) load_q(P, A, min(c, chunks - 1), t, l, q[t]);
-    };
-    load(0, even);
     lds_barrier();
-    for (int c = 0; c < chunks; c += 2) {
-      load(c + 1, odd);
+    for (int c = 0; c < chunks; ++c) {
       if (c > 0) read_chunk(P, A, c - 1, col0, l, sh, group, o);
-      read_state(A, c, l, even, sh, group, o);
+      read_state(c, l, sh, group, o);
       lds_barrier();
-      if (c + 1 >= chunks) break;
-      load(c + 2, even);
-      read_chunk(P, A, c, col0, l, sh, group, o);
-      read_state(A, c + 1, l, odd, sh, group, o);
+      help_A(sh.part[c & 1], sh.A, wave, l);
       lds_barrier();
     }
     read_chunk(P, A, chunks - 1, col0, l, sh, group, o);
@@ -837,7 +830,7 @@ __global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
   for (int m = 0; m < 8; ++m) S[m] = carried ? state.get(state_row(m, g), col) : (f32x4){0, 0, 0, 0};
   if (chunks > 0) {
     Frag f[4][3];
-    split_state(S, f, sh.S[0][group], l);
+    split_state(S, f, sh.S[group], l);
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
       chain_chunk(c, 16 * group + (l & 15), l, sh, group, f, S);
