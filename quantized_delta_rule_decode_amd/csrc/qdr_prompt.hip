@@ -26,9 +26,13 @@ namespace qdr {
 
 namespace {
 
-// Keeps the reads of later steps from being moved up across it: they would not
-// fit the registers that four waves a SIMD leave.
-#define QDR_PLACE() __builtin_amdgcn_sched_barrier(0)
+// Where TIGHT: keeps the reads of later steps from being moved up across it.
+// They would not fit the registers that four waves a SIMD leave (SUM); with
+// two (DELTA) they hide the LDS behind the products.
+template <bool TIGHT>
+__device__ __forceinline__ void place() {
+  if (TIGHT) __builtin_amdgcn_sched_barrier(0);
+}
 
 constexpr int kD = 128;
 constexpr int kLd = 68;        // row stride of a 64 x 64 fp32 matrix in LDS
@@ -366,6 +370,7 @@ __device__ __forceinline__ Frag transposed(const u32x4 (*K)[256], int m, int s, 
 }
 
 // S = 2^g_63 S + K^T diag(2^(g_63 - g)) U.
+template <bool TIGHT>
 __device__ __forceinline__ void update_state(const u32x4 (*K)[256], const float *dec, const f32x4 *u, f32x4 *S, int l) {
   const int g = l >> 4;
   const float all = dec[kChunk - 1];
@@ -384,7 +389,7 @@ __device__ __forceinline__ void update_state(const u32x4 (*K)[256], const float 
       for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int m = 0; m < 4; ++m) S[half + m] = mma(k[m], d[x], S[half + m]);
-      QDR_PLACE();
+      place<TIGHT>();
     }
   }
 }
@@ -406,7 +411,6 @@ __device__ __forceinline__ void solve(const u32x4 (*T)[3][64], const f32x4 *r, f
       for (int y = 2 - x; y >= 0; --y)
 #pragma unroll
         for (int t = 2 * s; t < 4; ++t) u[t] = mma(a[t], R[y], u[t]);
-      QDR_PLACE();
     }
   }
 }
@@ -442,7 +446,7 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
     for (int x = 1; x >= 0; --x)
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] = mma(q[t], f[x], o[t]);
-    QDR_PLACE();
+    place<!DELTA>();
   }
   f32x4 u[4];
 #pragma unroll
@@ -472,7 +476,7 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
       for (int y = DELTA ? 1 - x : 0; y >= 0; --y)
 #pragma unroll
         for (int t = 2 * s; t < 4; ++t) o[t] = mma(a[t], U[y], o[t]);
-      QDR_PLACE();
+      place<!DELTA>();
     }
   }
 #pragma unroll
@@ -483,7 +487,7 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
       st.V[16 * t + 4 * g + 2 * x][col] = (uint16_t)y;
       st.V[16 * t + 4 * g + 2 * x + 1][col] = (uint16_t)(y >> 16);
     }
-  update_state(st.K, st.dec, u, S, l);
+  update_state<!DELTA>(st.K, st.dec, u, S, l);
 }
 
 // Which chunks of which sequence a workgroup takes: a whole sequence, or with
@@ -647,7 +651,7 @@ __device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &
 #pragma unroll
     for (int x = 0; x < 2; ++x) sh.U[group][s][x][l] = U[x].w;
   }
-  update_state(p.K, p.dec, u, S, l);
+  update_state<false>(p.K, p.dec, u, S, l);
   split_state(S, f, sh.S[group], l);
 }
 
@@ -700,15 +704,22 @@ __device__ __forceinline__ void help_put(const ScanAt &A, int c, int tid, const 
   else if (tid >= 128) p.dec[tid - 128] = in.dec;
 }
 
-// A's ten tiles over waves 2 .. 7.
+// A's ten tiles over waves 2 .. 7: two in step to those beside no chain wave
+// (they share their vector units with 2, 3, 6, 7), one to 4 and 5.
 __device__ __forceinline__ void help_A(const ChainShared::Part &p, u32x4 (*A)[2][64], int wave, int l) {
-#pragma unroll 1
-  for (int i = wave - 2; i < 10; i += 6) {
+  auto tile = [&](int i) {
     const int t = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, j = i < 4 ? i : i < 7 ? i - 4 : i < 9 ? i - 7 : 0;
     Frag q[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) q[s] = rows_operand(p.Q[t], s, l);
     put_tile(p.K[j], q, p.lg, A, t, j, l);
+  };
+  if (wave == 4 || wave == 5) {
+    tile(wave + 4);
+  } else {
+    const int i = 2 * ((wave & 1) + (wave >> 2 << 1));
+    tile(i);
+    tile(i + 1);
   }
 }
 
@@ -868,7 +879,7 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         u[t][x] = __uint_as_float((uint32_t)st.V[16 * t + 4 * g + x][16 * wave + i16] << 16);
-    update_state(st.K, st.dec, u, S, l);
+    update_state<true>(st.K, st.dec, u, S, l);
     decay *= st.dec[kChunk - 1];
     lds_barrier();
   }
