@@ -3,8 +3,9 @@
 // 8-bit: r = max |x| over the head's 128 channels (1 below 2^-126), z =
 // nearest-even(127 x / r), scale r / 127.  x and r are bfloat16, so 127 x is
 // exact in fp32 and the quotient is no nearer to a half-integer than 2^-9
-// unless it is one: one correctly rounded division gives the definition's code
-// in every case.
+// unless it is one.  Times 1/r it is right to a few units of 2^-23, and one
+// step q + (127 x - q r) / r, whose difference is exact, returns a quotient
+// that fp32 holds (a half-integer) exactly: the definition's code in every case.
 // A workgroup takes one block (32 consecutive positions) of one (sequence,
 // head), so that the values, which the cache keeps transposed, leave in whole
 // 16-byte units wherever all their eight tokens are in the call; at a ragged
@@ -63,6 +64,13 @@ __device__ __forceinline__ bool locate(const KvArgs &P, Where &at) {
 __device__ __forceinline__ int slot_of(int r) { return 4 * (r >> 4) + (r & 3); }
 __device__ __forceinline__ int group_of(int r) { return (r >> 2) & 3; }
 
+// Where a channel's tokens are in LDS: eight bytes more every 16 channels put
+// the eight threads of a token (16 channels each) on banks of their own.
+template <int E>
+__device__ __forceinline__ int channel_at(int ch) { return ch * (kBlock * E + 8) + 8 * (ch >> 4); }
+template <int E>
+constexpr int kChannels = kD * (kBlock * E + 8) + 8 * (kD / 16);
+
 __device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Codes of 16 channels and the vector's scale.  |x| as integers order like
@@ -82,8 +90,10 @@ __device__ __forceinline__ u32x4 quantise(const u32x4 *x, float *scale) {
   float r = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(m << 16);
   if (m < 0x0080u) r = 1.0f;
   *scale = __fdiv_rn(r, 127.0f);
-  const float down = r > 0x1p100f ? 0x1p-10f : 1.0f;   // 127 x has to stay finite
-  r *= down;
+  // 127 x has to stay finite, and what is left of it after q r exact
+  const float by = r > 0x1p100f ? 0x1p-10f : r < 0x1p-60f ? 0x1p64f : 1.0f;
+  r *= by;
+  const float inv = __builtin_amdgcn_rcpf(r);
   u32x4 z;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -92,7 +102,8 @@ __device__ __forceinline__ u32x4 quantise(const u32x4 *x, float *scale) {
     for (int j = 0; j < 4; ++j) {
       const uint32_t w = x[(4 * i + j) >> 3][((4 * i + j) >> 1) & 3];
       const float y = (j & 1) ? hi_f32(w) : lo_f32(w);
-      const float t = rintf(__fdiv_rn(127.0f * (y * down), r));
+      const float x127 = 127.0f * (y * by), q = x127 * inv;
+      const float t = rintf(__builtin_fmaf(__builtin_fmaf(-q, r, x127), inv, q));
       word |= ((uint32_t)(int)(t == t ? t : 0.0f) & 0xFFu) << (8 * j);
     }
     z[i] = word;
@@ -103,8 +114,7 @@ __device__ __forceinline__ u32x4 quantise(const u32x4 *x, float *scale) {
 template <int KIND>
 __global__ void __launch_bounds__(256) k_kv_write(KvArgs P) {
   constexpr int E = KIND / 8;                       // bytes of an element
-  __shared__ __attribute__((aligned(16))) uint8_t sv[kD * (kBlock * E + 8)];   // V, channel by channel
-  constexpr int kRow = kBlock * E + 8;
+  __shared__ __attribute__((aligned(16))) uint8_t sv[kChannels<E>];   // V, channel by channel
   Where at;
   if (!locate<KIND>(P, at) || !at.blk) return;
   const int h = blockIdx.x % P.heads;
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(256) k_kv_write(KvArgs P) {
         *(float *)(at.blk + kKv8Scale + 4 * kBlock + 4 * r) = vs;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sv[(16 * seg + i) * kRow + pos] = (uint8_t)(vz[i >> 2] >> (8 * (i & 3)));
+      for (int i = 0; i < 16; ++i) sv[channel_at<E>(16 * seg + i) + pos] = (uint8_t)(vz[i >> 2] >> (8 * (i & 3)));
     }
   } else if (in) {
 #pragma unroll
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(256) k_kv_write(KvArgs P) {
       *(u32x4 *)(at.blk + ((tile * 4 + half * 2 + p) * 64 + g * 16 + key) * 16) = k[p];
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      *(uint16_t *)&sv[(16 * seg + i) * kRow + 2 * pos] = (uint16_t)(v[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
+      *(uint16_t *)&sv[channel_at<E>(16 * seg + i) + 2 * pos] = (uint16_t)(v[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
   }
   __syncthreads();
   uint8_t *dst = at.blk + (KIND == 8 ? kKv8Half : kKv16Half);
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(256) k_kv_write(KvArgs P) {
 #pragma unroll
     for (int part = 0; part < (KIND == 8 ? 2 : 1); ++part) {
       const int ch = KIND == 8 ? 32 * (unit >> 6) + 16 * part + m : 16 * (unit >> 6) + m;
-      const uint8_t *src = &sv[ch * kRow + 8 * E * gg];
+      const uint8_t *src = &sv[channel_at<E>(ch) + 8 * E * gg];
       uint8_t *to = dst + unit * 16 + 8 * part;
       if (whole) {
         *(u32x2 *)to = *(const u32x2 *)src;
@@ -175,8 +185,7 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w, int byte, float s) {
 template <int KIND>
 __global__ void __launch_bounds__(256) k_kv_read(KvArgs P) {
   constexpr int E = KIND / 8;
-  constexpr int kRow = kBlock * E + 8;
-  __shared__ __attribute__((aligned(16))) uint8_t sv[kD * kRow];
+  __shared__ __attribute__((aligned(16))) uint8_t sv[kChannels<E>];
   Where at;
   if (!locate<KIND>(P, at)) return;
   const int h = blockIdx.x % P.heads;
@@ -190,11 +199,11 @@ __global__ void __launch_bounds__(256) k_kv_read(KvArgs P) {
       const int unit = tid + 256 * x, lane = unit & 63, gg = lane >> 4, m = lane & 15;
       const u32x4 y = *(const u32x4 *)(src + unit * 16);
       if (KIND == 8) {
-        *(u32x2 *)&sv[(32 * (unit >> 6) + m) * kRow + 8 * gg] = (u32x2){y[0], y[1]};
-        *(u32x2 *)&sv[(32 * (unit >> 6) + 16 + m) * kRow + 8 * gg] = (u32x2){y[2], y[3]};
+        *(u32x2 *)&sv[channel_at<E>(32 * (unit >> 6) + m) + 8 * gg] = (u32x2){y[0], y[1]};
+        *(u32x2 *)&sv[channel_at<E>(32 * (unit >> 6) + 16 + m) + 8 * gg] = (u32x2){y[2], y[3]};
       } else {
-        *(u32x2 *)&sv[(16 * (unit >> 6) + m) * kRow + 16 * gg] = (u32x2){y[0], y[1]};
-        *(u32x2 *)&sv[(16 * (unit >> 6) + m) * kRow + 16 * gg + 8] = (u32x2){y[2], y[3]};
+        *(u32x2 *)&sv[channel_at<E>(16 * (unit >> 6) + m) + 16 * gg] = (u32x2){y[0], y[1]};
+        *(u32x2 *)&sv[channel_at<E>(16 * (unit >> 6) + m) + 16 * gg + 8] = (u32x2){y[2], y[3]};
       }
     }
     const int tile = r >> 4, key = r & 15, half = seg >> 2, g = seg & 3;
@@ -207,8 +216,8 @@ __global__ void __launch_bounds__(256) k_kv_read(KvArgs P) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         k[i >> 2][i & 3] = two_codes(z[i >> 1], 2 * (i & 1), ks);
-        const float a = (float)(int8_t)sv[(16 * seg + 2 * i) * kRow + pos] * vs;
-        const float b = (float)(int8_t)sv[(16 * seg + 2 * i + 1) * kRow + pos] * vs;
+        const float a = (float)(int8_t)sv[channel_at<E>(16 * seg + 2 * i) + pos] * vs;
+        const float b = (float)(int8_t)sv[channel_at<E>(16 * seg + 2 * i + 1) + pos] * vs;
         v[i >> 2][i & 3] = pack_bf16(a, b);
       }
     } else {
@@ -218,8 +227,8 @@ __global__ void __launch_bounds__(256) k_kv_read(KvArgs P) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i >> 2][i & 3] = (uint32_t)*(const uint16_t *)&sv[(16 * seg + 2 * i) * kRow + 2 * pos] |
-                           (uint32_t)*(const uint16_t *)&sv[(16 * seg + 2 * i + 1) * kRow + 2 * pos] << 16;
+        v[i >> 2][i & 3] = (uint32_t)*(const uint16_t *)&sv[channel_at<E>(16 * seg + 2 * i) + 2 * pos] |
+                           (uint32_t)*(const uint16_t *)&sv[channel_at<E>(16 * seg + 2 * i + 1) + 2 * pos] << 16;
     }
   }
   if (!in) return;

@@ -70,16 +70,29 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // Index of the sequence that place `id` of a call belongs to, where sequence
-// b has places first(b) = cu[b] / per + extra * b on: first() grows with b, so
-// bisect for the last b with first(b) <= id.
+// b has places first(b) = cu[b] / per + extra * b on: first() grows with b, and
+// the last b with first(b) <= id is found 64 candidates at a time (a load for
+// up to 64 sequences, two for up to 4096).  The whole wave calls it.
 __device__ __forceinline__ int sequence_of(const int32_t *cu, int n, int per, int extra, int id) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    const int c = cu[mid];
-    if ((c >= 0 ? c / per : 0) + extra * mid <= id) lo = mid; else hi = mid - 1;
+  const int lane = (int)(threadIdx.x & 63);
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 63) >> 6, at = lane * step;
+    bool not_behind = false;
+    if (at < len) {
+      const int c = cu[lo + at];
+      not_behind = (c >= 0 ? c / per : 0) + extra * (lo + at) <= id;
+    }
+    const int count = __popcll(__ballot(not_behind));
+    if (count > 1) {
+      lo += (count - 1) * step;
+      len = min(step, len - (count - 1) * step);
+    } else {
+      len = min(step, len);
+    }
+    if (step == 1) break;
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Rows [first, first + len) of sequence b; false where the counts are out of

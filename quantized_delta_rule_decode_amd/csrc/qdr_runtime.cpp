@@ -189,6 +189,7 @@ struct qdr_pool {
   // caller's stream by two events, so they overlap the integer launch
   hipStream_t float_stream = nullptr;
   hipEvent_t fork_ev = nullptr, join_ev = nullptr;
+  bool all_fp32 = false;              // whole heads, none quantised
 };
 
 namespace {
@@ -307,8 +308,7 @@ PoolView pool_view(const qdr_pool *p) {
   v.num_heads = p->desc.num_heads;
   v.gate = p->desc.gate;
   v.device = p->device;
-  v.all_fp32 = p->desc.unit == QDR_UNIT_HEAD;
-  for (uint8_t k : p->kinds) v.all_fp32 = v.all_fp32 && k == QDR_K_FP32;
+  v.all_fp32 = p->all_fp32;
   v.err = p->d_err;
   return v;
 }
@@ -362,6 +362,8 @@ qdr_status qdr_pool_create(const qdr_pool_desc *desc, void *dev_mem, size_t dev_
   p->kinds.assign(desc->kinds, desc->kinds + nk);
   p->omega.assign((size_t)desc->num_heads * QDR_DIM, 1.0f);
   if (desc->omega) std::memcpy(p->omega.data(), desc->omega, sizeof(float) * p->omega.size());
+  p->all_fp32 = desc->unit == QDR_UNIT_HEAD &&
+                std::all_of(p->kinds.begin(), p->kinds.end(), [](uint8_t k) { return k == QDR_K_FP32; });
   p->desc.kinds = p->kinds.data();
   p->desc.omega = p->omega.data();
   build_layout(&p->desc, p->L);
