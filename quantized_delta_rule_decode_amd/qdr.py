@@ -150,32 +150,34 @@ def _dptr(t, dtype, name, numel=None):
     return t.data_ptr()
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _ptr(t, dtype, name, shape):
+    """Address of a contiguous device tensor of this type and shape; one test
+    where all is well (a call of small tensors takes as long as its launch)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dptr(t, dtype, name)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _rows(cu, **tensors):
-    """n of the cumulative counts and T, the rows that every given tensor has."""
-    import torch
-    _dptr(cu, torch.int32, "cu")
-    if cu.dim() != 1 or cu.numel() < 1:
+def _sequences(cu):
+    """n of the cumulative counts."""
+    if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu must be one-dimensional with n + 1 elements")
-    rows = {t.shape[0] if t.dim() else -1 for t in tensors.values()}
-    if len(rows) != 1:
-        raise ValueError("rows differ: " + ", ".join(f"{k} {tuple(t.shape)}" for k, t in tensors.items()))
-    return cu.numel() - 1, rows.pop()
+    return cu.shape[0] - 1
 
 
 def _workspace(given, need, stream):
     """Pointer and bytes of a call's workspace; without one, memory of torch's
     that is not reused before the call's stream is done with it."""
-    import torch
     if given is not None:
-        return _dptr(given, given.dtype, "workspace"), given.numel() * given.element_size(), given
+        return _ptr(given, given.dtype, "workspace", given.shape), given.nbytes, given
+    import torch
     with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
         ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    return ctypes.c_void_p(ws.data_ptr()), need, ws
+    return ws.data_ptr(), need, ws
 
 
 def _desc(num_slots, num_heads, kinds, omega, unit, gate, scale_mode, fit_iters, scale_bits=32):
@@ -316,27 +318,23 @@ class Pool:
         [n+1]; slots and carry int32 [n].  workspace: None, or a device tensor
         of at least qdr_prompt_workspace(n, T) bytes."""
         import torch
-        H, bf, f32, i32 = self.num_heads, torch.bfloat16, torch.float32, torch.int32
-        n, T = _rows(cu, q=q, k=k, v=v, gate=gate, o=o, **({} if beta is None else {"beta": beta}))
-        for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-            _shape(t, (T, H, DIM), name)
-        for name, t in (("gate", gate), ("beta", beta)):
-            if t is not None:
-                _shape(t, (T, H), name)
+        bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        n, T, H = _sequences(cu), q.shape[0], self.num_heads
+        rows, gates = (T, H, DIM), (T, H)
         ws, size, keep = _workspace(workspace, 0 if workspace is not None else self.qdr_prompt_workspace(n, T), stream)
-        _check("qdr_prompt", load().qdr_prompt(
-            self._h, int(rule), _dptr(slots, i32, "slots", n), None if carry is None else _dptr(carry, i32, "carry", n),
-            _dptr(cu, i32, "cu"), n, T, _dptr(q, bf, "q"), _dptr(k, bf, "k"), _dptr(v, bf, "v"),
-            None if beta is None else _dptr(beta, f32, "beta"), _dptr(gate, f32, "gate"), _dptr(o, bf, "o"),
-            ws, size, _stream(stream)))
+        _check("qdr_prompt", _lib.qdr_prompt(
+            self._h, rule, _ptr(slots, i32, "slots", (n,)), None if carry is None else _ptr(carry, i32, "carry", (n,)),
+            _ptr(cu, i32, "cu", (n + 1,)), n, T, _ptr(q, bf, "q", rows), _ptr(k, bf, "k", rows), _ptr(v, bf, "v", rows),
+            None if beta is None else _ptr(beta, f32, "beta", gates), _ptr(gate, f32, "gate", gates),
+            _ptr(o, bf, "o", rows), ws, size, _stream(stream)))
 
     def _linear_step(self, fn, dtype, slots, q, k, v, gate, o, stream):
         import torch
         B, H = slots.numel(), self.num_heads
-        _check(fn, getattr(load(), fn)(
-            self._h, _dptr(slots, torch.int32, "slots"), B,
-            _dptr(q, dtype, "q", B * H * DIM), _dptr(k, dtype, "k", B * H * DIM), _dptr(v, dtype, "v", B * H * DIM),
-            _dptr(gate, torch.float32, "gate", B * H), _dptr(o, dtype, "o", B * H * DIM), _stream(stream)))
+        rows = (B, H, DIM)
+        _check(fn, getattr(_lib, fn)(
+            self._h, _ptr(slots, torch.int32, "slots", (B,)), B, _ptr(q, dtype, "q", rows), _ptr(k, dtype, "k", rows),
+            _ptr(v, dtype, "v", rows), _ptr(gate, torch.float32, "gate", (B, H)), _ptr(o, dtype, "o", rows), _stream(stream)))
 
     def qdr_linear_step(self, slots, q, k, v, gate, o, stream=None):
         """q, k, v, o: fp32 [B][H][128]; gate fp32 [B][H]; an uncompressed pool."""
@@ -407,21 +405,17 @@ class KVCache:
         self.close()
 
     # ---- entry points (same names as the C ABI)
-    def _where(self, pages, cu, context):
+    def _where(self, n, pages, cu, context):
         import torch
-        n = cu.numel() - 1
-        if pages.dim() != 2 or pages.shape[0] != n:
-            raise ValueError(f"pages has shape {tuple(pages.shape)}, expected ({n}, max_pages)")
         i32 = torch.int32
-        return _dptr(pages, i32, "pages"), pages.shape[1], _dptr(cu, i32, "cu"), _dptr(context, i32, "context", n)
+        most = pages.shape[1] if pages.dim() == 2 else 0
+        return _ptr(pages, i32, "pages", (n, most)), most, _ptr(cu, i32, "cu", (n + 1,)), _ptr(context, i32, "context", (n,)), n
 
     def _move(self, fn, pages, cu, context, k, v, stream):
         import torch
-        n, T = _rows(cu, k=k, v=v)
-        for name, t in (("k", k), ("v", v)):
-            _shape(t, (T, self.num_heads, DIM), name)
-        _check(fn, getattr(load(), fn)(self._h, *self._where(pages, cu, context), n, T, _dptr(k, torch.bfloat16, "k"),
-                                       _dptr(v, torch.bfloat16, "v"), _stream(stream)))
+        n, rows = _sequences(cu), (k.shape[0], self.num_heads, DIM)
+        _check(fn, getattr(_lib, fn)(self._h, *self._where(n, pages, cu, context), rows[0], _ptr(k, torch.bfloat16, "k", rows),
+                                     _ptr(v, torch.bfloat16, "v", rows), _stream(stream)))
 
     def qdr_kv_write(self, pages, cu, context, k, v, stream=None):
         """pages int32 [n][max_pages], cu int32 [n+1], context int32 [n]; k, v
@@ -443,16 +437,16 @@ class KVCache:
         workspace: None, or a device tensor of at least
         qdr_kv_attend_workspace(n, T, q_heads, max_pages) bytes."""
         import torch
-        n, T = _rows(cu, q=q, o=o)
+        n, bf = _sequences(cu), torch.bfloat16
         if q.dim() != 3 or q.shape[2] != DIM:
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected ({T}, q_heads, {DIM})")
-        _shape(o, q.shape, "o")
-        where = self._where(pages, cu, context)
-        need = 0 if workspace is not None else self.qdr_kv_attend_workspace(n, T, q.shape[1], where[1])
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected (T, q_heads, {DIM})")
+        T, heads, _ = rows = q.shape
+        where = self._where(n, pages, cu, context)
+        need = 0 if workspace is not None else self.qdr_kv_attend_workspace(n, T, heads, where[1])
         ws, size, keep = _workspace(workspace, need, stream)
-        _check("qdr_kv_attend", load().qdr_kv_attend(
-            self._h, *where, n, T, q.shape[1], _dptr(q, torch.bfloat16, "q"), DIM ** -0.5 if scale is None else float(scale),
-            _dptr(o, torch.bfloat16, "o"), ws, size, _stream(stream)))
+        _check("qdr_kv_attend", _lib.qdr_kv_attend(
+            self._h, *where, T, heads, _ptr(q, bf, "q", rows), DIM ** -0.5 if scale is None else scale, _ptr(o, bf, "o", rows),
+            ws, size, _stream(stream)))
 
     def qdr_kv_poll_device_error(self) -> int:
         f = ctypes.c_uint32(0)
