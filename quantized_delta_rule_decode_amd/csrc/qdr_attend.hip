@@ -109,7 +109,7 @@ __device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int page, in
 }
 
 // ---- few rows: up to 16 (one token of up to 16 heads, a few tokens of fewer)
-// Four waves take every fourth block of 32 keys, each with its own running
+// Eight waves take every eighth block of 32 keys, each with its own running
 // maximum, straight from memory into operands; they meet in LDS at the end.
 template <int KIND>
 struct FewIn {
@@ -119,10 +119,10 @@ struct FewIn {
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan plan) {
+__global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, AttendPlan plan) {
   const KvArgs &P = A.kv;
-  __shared__ float sm[4][16], sl[4][16];
-  __shared__ f32x4 so[4][8][64];
+  __shared__ float sm[kFewWaves][16], sl[kFewWaves][16];
+  __shared__ f32x4 so[kFewWaves][8][64];
   if (blockIdx.x == 0) check_counts(P);
   const int split = blockIdx.x % plan.few_splits;
   const int part = blockIdx.x / plan.few_splits % plan.few_parts;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
   int page = lo < hi ? page_of(P, t.b, min(lo + w, blocks - 1)) : 0;
   auto load = [&](int block, FewIn<KIND> &in) {
     const uint8_t *blk = block_at(P, page, kvh, min(block, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
-    page = page_of(P, t.b, min(block + 4, blocks - 1));
+    page = page_of(P, t.b, min(block + kFewWaves, blocks - 1));
     in.good = blk != nullptr;
     if (!blk) blk = P.base;
     constexpr int N = KIND == 8 ? 4 : 8;
@@ -259,12 +259,12 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
   if (lo < hi) {
     FewIn<KIND> even, odd;
     load(lo + w, even);
-    for (int block = lo + w; block < hi; block += 8) {
-      load(block + 4, odd);
+    for (int block = lo + w; block < hi; block += 2 * kFewWaves) {
+      load(block + kFewWaves, odd);
       take(block, even);
-      if (block + 4 >= hi) break;
-      load(block + 8, even);
-      take(block + 4, odd);
+      if (block + kFewWaves >= hi) break;
+      load(block + 2 * kFewWaves, even);
+      take(block + kFewWaves, odd);
     }
   }
   sum += __shfl_xor(sum, 16);
@@ -274,32 +274,33 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A, AttendPlan pla
     sl[w][i16] = sum;
   }
   __syncthreads();
-  const float top = fmaxf(fmaxf(sm[0][i16], sm[1][i16]), fmaxf(sm[2][i16], sm[3][i16]));
+  float top = kNone;
+#pragma unroll
+  for (int x = 0; x < kFewWaves; ++x) top = fmaxf(top, sm[x][i16]);
   const float ref = top == kNone ? 0.0f : top;
   float total = 0.0f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) total = __builtin_fmaf(sl[x][i16], ex2(sm[x][i16] - ref), total);
+  for (int x = 0; x < kFewWaves; ++x) total = __builtin_fmaf(sl[x][i16], ex2(sm[x][i16] - ref), total);
   const float fade = ex2(m - ref);
 #pragma unroll
   for (int d = 0; d < 8; ++d) so[w][d][l] = o[d] * fade;
   __syncthreads();
-  // lane (g, i16) of wave w: channels 16 d + 4 g .. of column i16, d = 2 w, 2 w + 1
+  // lane (g, i16) of wave w: channels 16 w + 4 g .. of column i16
+  static_assert(kFewWaves == 8, "a wave to sixteen channels");
+  f32x4 y = so[0][w][l];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int d = 2 * w + x;
-    const f32x4 y = (so[0][d][l] + so[1][d][l]) + (so[2][d][l] + so[3][d][l]);
-    if (plan.few_splits == 1) {
-      if (row) {
-        const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-        *(u32x2_a4 *)(A.o + at + 16 * d + 4 * g) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
-      }
-    } else {
-      float *to = A.part + (size_t)blockIdx.x * (kFewRows * (kD + 2));
-      *(f32x4 *)(to + (size_t)i16 * kD + 16 * d + 4 * g) = y;
-      if (w == 0 && x == 0 && g == 0) {
-        to[kFewRows * kD + i16] = top;
-        to[kFewRows * kD + kFewRows + i16] = total;
-      }
+  for (int x = 1; x < kFewWaves; ++x) y += so[x][w][l];
+  if (plan.few_splits == 1) {
+    if (row) {
+      const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+      *(u32x2_a4 *)(A.o + at + 16 * w + 4 * g) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+    }
+  } else {
+    float *to = A.part + (size_t)blockIdx.x * (kFewRows * (kD + 2));
+    *(f32x4 *)(to + (size_t)i16 * kD + 16 * w + 4 * g) = y;
+    if (w == 0 && g == 0) {
+      to[kFewRows * kD + i16] = top;
+      to[kFewRows * kD + kFewRows + i16] = total;
     }
   }
 }
@@ -580,7 +581,7 @@ template <int KIND>
 static hipError_t attend(const AttendArgs &a, const AttendPlan &p, hipStream_t st) {
   if (p.few) {
     const uint32_t units = (uint32_t)p.few_tiles * a.kv.heads * p.few_parts;
-    hipLaunchKernelGGL(k_attend_few<KIND>, dim3(units * p.few_splits), dim3(256), 0, st, a, p);
+    hipLaunchKernelGGL(k_attend_few<KIND>, dim3(units * p.few_splits), dim3(64 * kFewWaves), 0, st, a, p);
     if (p.few_splits > 1) hipLaunchKernelGGL(k_attend_join<true>, dim3(units * (kFewRows / 4)), dim3(256), 0, st, a, p);
   }
   if (p.many) {

@@ -415,7 +415,7 @@ static qdr_status make_plan(const qdr_kv *kv, int32_t n, int32_t T, int32_t q_he
   QDR_TRY(check_groups(((int64_t)T + n) * q_heads));
   *plan = qdr::plan_attend(n, T, q_heads, kv->desc.num_heads, max_pages, kv->page_shift);
   const int64_t few = (int64_t)plan->few_tiles * heads * plan->few_parts, many = (int64_t)plan->many_tiles * heads * plan->many_parts;
-  QDR_TRY(check_groups(few * (plan->few_splits > 4 ? plan->few_splits : 4)));
+  QDR_TRY(check_groups(few * 2 * (plan->few_splits > 4 ? plan->few_splits : 4)));
   return check_groups(many * (plan->many_splits > 32 ? plan->many_splits : 32));
 }
 

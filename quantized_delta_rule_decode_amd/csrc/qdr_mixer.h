@@ -91,9 +91,9 @@ hipError_t launch_kv_write(const KvArgs &, int kind, hipStream_t);
 hipError_t launch_kv_read(const KvArgs &, int kind, hipStream_t);
 
 // Rows (tokens x query heads of one key/value head) of the two kinds of
-// tiles, and the fewest blocks of keys that a piece of them has.
+// tiles, waves of a few-row tile, and the fewest blocks of keys of a piece.
 constexpr int kFewRows = 16, kManyRows = 128;
-constexpr int kFewLeast = 4, kManyLeast = 4;
+constexpr int kFewWaves = 8, kFewLeast = 8, kManyLeast = 4;
 // Up to so many blocks the keys are not cut: one workgroup takes 32 blocks in
 // about the time that the second launch costs.
 constexpr int kOnePiece = 32;
