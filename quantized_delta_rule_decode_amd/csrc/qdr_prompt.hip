@@ -148,24 +148,34 @@ __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
       if (t >= nt) f[s].w = (u32x4){0, 0, 0, 0};
     }
   };
-  Frag k[4];
+  // all asked for at once: one latency instead of one a tile
+  Frag k[4], kj[4][4];
   load(w, k);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < w) load(j, kj[j]);
   if (w == 0) {
     lg[l] = put_decays(P, t0, nt, h, l, ws);
     bt[l] = l < nt ? P.beta[(t0 + l) * P.H + h] : 0.0f;
   }
-  __syncthreads();
-  for (int j = 0; j <= w; ++j) {
-    Frag kj[4];
-    load(j, kj);
-    f32x4 kk = {0, 0, 0, 0};
+  f32x4 kk[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) kk = mma(k[s], kj[s], kk);
+  for (int j = 0; j < 4; ++j) kk[j] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j > w) continue;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) kk[j] = mma(k[s], j < w ? kj[j][s] : k[s], kk[j]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j > w) continue;
     const int col = 16 * j + i16;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * w + 4 * g + r;
-      L[t][col] = t > col ? bt[t] * (kk[r] * exp2f((float)(lg[t] - lg[col]))) : 0.0f;
+      L[t][col] = t > col ? bt[t] * (kk[j][r] * exp2f((float)(lg[t] - lg[col]))) : 0.0f;
     }
   }
   if ((w & 1) == 0) {   // the block above the diagonal that shares a fragment with it
