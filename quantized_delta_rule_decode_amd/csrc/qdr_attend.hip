@@ -52,6 +52,21 @@ __device__ __forceinline__ u32x4 keep_tokens(u32x4 v, int g, int left) {
   return f.w;
 }
 
+// bfloat16 values that are not finite, in blocks where some rows of a tile do
+// not see every token: 0 times them is not 0.  There they enter the product as
+// 0, and where any was found they are added afterwards to the rows that see
+// them (add_not_finite): infinities and NaN need no weight.
+__device__ __forceinline__ bool is_finite16(uint32_t x) { return (x & 0x7F80u) != 0x7F80u; }
+__device__ __forceinline__ u32x4 keep_finite(u32x4 v, bool *all) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i];
+    v[i] = (is_finite16(w) ? w & 0xFFFFu : 0u) | (is_finite16(w >> 16) ? w & 0xFFFF0000u : 0u);
+    *all = *all && v[i] == w;
+  }
+  return v;
+}
+
 // The rows of a tile: `tokens` tokens from `token` on, times `heads` query
 // heads from `head` on; row r is token r / heads, head r % heads.
 struct Tile {
@@ -108,6 +123,23 @@ __device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int page, in
   return P.base + (((size_t)page * P.heads + kvh) * per + (block & (per - 1))) * bytes;
 }
 
+// Adds a bfloat16 block's values that are not finite to one column's eight
+// results (lane (g, i): channels 16 d + 4 g .. of its row).
+__device__ __forceinline__ void add_not_finite(const uint8_t *blk, int first_key, int limit, int g, f32x4 *o) {
+#pragma unroll 1
+  for (int x = 0; x < kBlock; ++x) {
+    const int e = 4 * (x >> 4) + (x & 3), from = 16 * ((x >> 2) & 3) + 4 * g;
+    const bool sees = first_key + x <= limit;
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t v = *(const uint16_t *)(blk + kKv16Half + (64 * d + from + r) * 16 + 2 * e);
+        if (sees && !is_finite16(v)) o[d][r] += __uint_as_float(v << 16);
+      }
+  }
+}
+
 // ---- few rows: up to 16 (one token of up to 16 heads, a few tokens of fewer)
 // Eight waves take every eighth block of 32 keys, each with its own running
 // maximum, straight from memory into operands; they meet in LDS at the end.
@@ -152,6 +184,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
 #pragma unroll
   for (int d = 0; d < 8; ++d) o[d] = (f32x4){0, 0, 0, 0};
   float m = kNone, sum = 0.0f;
+  bool finite = true;
 
   // A block's loads are always there: one behind the last, or of a bad page,
   // is some block of the cache, and its keys are not looked at.
@@ -242,6 +275,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
 #pragma unroll
       for (int d = 0; d < 8; ++d)
         in.v[d & (KIND == 8 ? 3 : 7)] = keep_tokens(in.v[d & (KIND == 8 ? 3 : 7)], g, left);
+    if (KIND == 16 && (block + 1) * kBlock > t.position + 1)
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+        in.v[d & (KIND == 8 ? 3 : 7)] = keep_finite(in.v[d & (KIND == 8 ? 3 : 7)], &finite);
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
       Frag v;
@@ -266,6 +303,12 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
       load(block + 2 * kFewWaves, even);
       take(block + kFewWaves, odd);
     }
+    if (KIND == 16 && __any(!finite))
+      for (int block = lo + w; block < hi; block += kFewWaves) {
+        if ((block + 1) * kBlock <= t.position + 1) continue;
+        const uint8_t *blk = block_at(P, page_of(P, t.b, block), kvh, block, kKv16Block);
+        if (blk) add_not_finite(blk, block * kBlock, limit, g, o);
+      }
   }
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
@@ -401,7 +444,8 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
       }
     }
   };
-  auto store = [&](const ManyIn<KIND> &in, ManyShared<KIND> &to) {
+  bool finite = true;
+  auto store = [&](int block, const ManyIn<KIND> &in, ManyShared<KIND> &to) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       if (KIND == 8) {
@@ -417,6 +461,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
           u32x4 v = in.v[2 * y + (KIND == 8 ? 0 : x)];
           // values behind the last key may be anything: 0 times them is not 0
           if (in.left[y] < kBlock) v = keep_tokens(v, g, in.left[y]);
+          if ((block + 2) * kBlock > t.position + 1) v = keep_finite(v, &finite);
           to.v[y][4 * x + w][l] = v;
         }
       }
@@ -427,7 +472,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   if (lo < hi) load(lo, in);
   for (int block = lo; block < hi; block += 2) {
     ManyShared<KIND> &now = sh[((block - lo) >> 1) & 1];
-    store(in, now);
+    store(block, in, now);
     const int left0 = in.left[0], left1 = in.left[1];
     lds_barrier();
     load(block + 2, in);        // always there: the waits stay exact
@@ -513,6 +558,17 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
         o[0][d] = mma(v, pf[0][y], o[0][d]);
         o[1][d] = mma(v, pf[1][y], o[1][d]);
       }
+  }
+  if (KIND == 16) {
+    if (__syncthreads_or(!finite)) {
+      for (int block = max(lo, (t.position + 1) / kBlock - 1); block < hi; ++block) {
+        const uint8_t *blk = block_at(P, page_of(P, t.b, block), kvh, block, kKv16Block);
+        // a pair of blocks before the rows' first position was not looked at
+        if (!blk || (((block - lo) & ~1) + lo + 2) * kBlock <= t.position + 1) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) add_not_finite(blk, block * kBlock, limit[c], g, o[c]);
+      }
+    }
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {

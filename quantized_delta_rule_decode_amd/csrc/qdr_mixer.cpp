@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -88,11 +89,17 @@ PromptSpace prompt_space(const qdr::PoolView &v, int32_t n, int32_t T) {
   s.ordered = n > 1 && n <= qdr::kMostOrdered;
   s.tables = up((size_t)n * ((v.all_fp32 ? 0 : 2) + (s.ordered ? 1 : 0)) * sizeof(int32_t));
   s.states = v.all_fp32 ? 0 : (size_t)n * state;
-  // segments for two rounds of workgroups, none below kSegmentLeast chunks: a
-  // segment's state costs four passes over 64 KiB, as much as four chunks' rows
-  const int64_t chunks = (int64_t)T / qdr::kChunk * v.num_heads;
+  // SUM's segments: as many as there are places for workgroups (two to each of
+  // 256 compute units), four chunks at least.  16385 tokens of 16 heads in
+  // segments of 4, 8, 16, 32 chunks and uncut: 170, 148, 173, 271, 1396 us.
+  // Where the sequences alone fill the places, only one of twice the mean
+  // length is cut: 32 x 1024 tokens of 16 heads cut at the half 273 us, uncut
+  // 200, and one long sequence among short ones still does not run alone.
+  const int64_t places = 2 * 256, pairs = (int64_t)n * v.num_heads;
+  int64_t want = (int64_t)T / qdr::kChunk * v.num_heads / places;
+  if (pairs >= places) want = std::max<int64_t>(want, 2 * ((int64_t)T / qdr::kChunk / n));
   int64_t segment = qdr::kSegmentLeast;
-  while (segment * qdr::kSegmentGroups < chunks) segment *= 2;
+  while (segment < want) segment *= 2;
   if (segment * qdr::kChunk < T) {
     s.segment = (int32_t)segment;
     s.segments = T / (segment * qdr::kChunk) + n;

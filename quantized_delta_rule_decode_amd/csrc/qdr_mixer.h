@@ -21,9 +21,7 @@ constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
 // decays from the chunk's start and to its end (64 fp32 each), and for DELTA
 // one triangular matrix.
 constexpr size_t kDecayFloats = 4 * kChunk, kChunkFloats = kDecayFloats + kTriFloats;
-// Chunks of a segment at least, and segments that a call is cut into at most
-// about (of all heads).
-constexpr int kSegmentLeast = 8, kSegmentGroups = 1024;
+constexpr int kSegmentLeast = 4;   // chunks of a segment
 // Sequences of a call that are put in order of length (n^2 comparisons).
 constexpr int kMostOrdered = 1024;
 

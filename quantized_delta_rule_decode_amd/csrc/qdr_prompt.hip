@@ -960,9 +960,10 @@ hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st)
 hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
   if (delta) {
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
-    // few heads: their chains side by side, four workgroups to each, as long as
-    // all of them are resident at once (256 compute units)
-    if ((int64_t)a.n * a.H <= 64) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
+    // Few heads: four workgroups to a chain, a workgroup a compute unit.  4096
+    // tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight
+    // sequences of 1024 tokens and 32 heads: 255 us, the scan 168.
+    if ((int64_t)a.n * a.H <= 128) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
     else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
   }

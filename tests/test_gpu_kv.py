@@ -304,6 +304,48 @@ def test_attend_non_finite(torch_dev, kind, rows):
 
 
 @pytest.mark.parametrize("kind", [INT8, BF16])
+@pytest.mark.parametrize("rows", [3, 40, 150])
+def test_attend_values_that_are_not_finite(torch_dev, kind, rows):
+    """A value that is NaN or infinite reaches the rows that see its token, in
+    its own head and (bfloat16) channel, and no row before it."""
+    torch = torch_dev
+    H, c, Q = 2, 200, 4
+    cache, pages, k, v = fill(torch, [c], 32, H, kind)
+    q = vectors(torch, 9, rows, Q)
+    cu, ctx = i32(torch, [0, rows]), i32(torch, [c])
+    clean, o = torch.empty_like(q), torch.empty_like(q)
+    cache.qdr_kv_attend(pages, cu, ctx, q, clean, scale=0.02)
+    ref, room = reference(torch, q, k, v, [rows], [c], 0.02)
+    assert ((clean.double() - ref).abs() <= room).all()
+    places = [(c - 1, 7, float("inf")), (c - 2, 7, float("-inf")), (c - 3 if rows == 3 else c - 20, 99, float("nan"))]
+    for at, channel, bad in places:
+        vv = v[at:at + 1].bfloat16()
+        vv[0, 1, channel] = bad
+        cache.qdr_kv_write(pages, i32(torch, [0, 1]), i32(torch, [at + 1]), k[at:at + 1].bfloat16(), vv)
+    cache.qdr_kv_attend(pages, cu, ctx, q, o, scale=0.02)
+    position = torch.arange(c - rows, c, device="cuda")
+    same_as = o[:, :2]
+    assert torch.isfinite(same_as).all() and ((same_as.double() - ref[:, :2]).abs() <= room[:, :2]).all()
+    for row in range(rows):
+        seen = [(ch, x) for at, ch, x in places if at <= position[row]]
+        got = o[row, 2:]
+        if kind == INT8:       # the scale of the vector is NaN: all its channels
+            assert got.isnan().all() if seen else torch.isfinite(got).all()
+        else:
+            bad = torch.zeros(D, dtype=torch.bool, device="cuda")
+            for ch, _ in seen:
+                bad[ch] = True
+            assert torch.isfinite(got[:, ~bad]).all(), f"row {row}"
+            if any(ch == 99 for ch, _ in seen):
+                assert got[:, 99].isnan().all()
+            if bad[7]:         # the older token first: -inf alone, then both
+                both = position[row] >= c - 1
+                assert got[:, 7].isnan().all() if both else (got[:, 7] == float("-inf")).all()
+        if not seen:
+            assert ((got.double() - ref[row, 2:]).abs() <= room[row, 2:]).all()
+
+
+@pytest.mark.parametrize("kind", [INT8, BF16])
 def test_attend_graphs_and_streams(torch_dev, kind):
     """The cache as a decode loop uses it, captured: write the token, attend.
     Two graphs with workspaces of their own replay beside each other and equal

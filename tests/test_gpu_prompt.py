@@ -150,11 +150,44 @@ def test_prompt_gates(torch_dev, rule, gates):
 def test_prompt_many_heads(torch_dev, rule):
     """Enough (sequence, head) pairs for the launch that takes wider slices."""
     torch = torch_dev
-    lens, H = [70, 1, 90, 65], 33
+    lens, H = [70, 1, 90, 0, 65, 129], 33
     x = make(torch, 6, sum(lens), H)
-    pool = fp32_pool(4, H)
-    o = run(torch, pool, rule, [3, 1, 0, 2], lens, x)
-    check(torch, x, rule, lens, 0, o, states(torch, pool, [3, 1, 0, 2]), torch.zeros((4, H, D, D), device="cuda"))
+    pool = fp32_pool(6, H)
+    S0 = torch.randn((6, H, D, D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    slots, carry = [3, 1, 0, 5, 2, 4], [1, 0, 0, 1, 1, 0]
+    pool.qdr_pack(i32(torch, slots), S0)
+    o = run(torch, pool, rule, slots, lens, x, carry)
+    check(torch, x, rule, lens, 0, o, states(torch, pool, slots), S0 * torch.tensor(carry, device="cuda")[:, None, None, None])
+    pool.qdr_slot_reset(i32(torch, slots))
+    p = run(torch, pool, rule, [3, 1, -1, 5, 2, 9], lens, x)
+    assert torch.equal(p[71 + 90:71 + 90 + 65], run(torch, pool, rule, [0, 1, 2, 3, 4, 5], lens, x)[71 + 90:71 + 90 + 65])
+    assert (p[71:161] == 0).all() and (p[226:] == 0).all()
+    assert pool.qdr_poll_device_error() == qdr.DEVERR_SLOT
+
+
+@pytest.mark.parametrize("lens,carried", [([1200], True), ([700, 0, 257, 64, 1], False), ([256, 512, 300], True)], ids=str)
+def test_long_additive_prompts(torch_dev, lens, carried):
+    """Prompts of several segments, with padding and gates that forget."""
+    torch = torch_dev
+    n, H = len(lens), 2
+    x = make(torch, 16, sum(lens), H, "zeros" if carried else "mixed")
+    pool = fp32_pool(n, H)
+    slots = list(range(n))[::-1]
+    S0 = torch.randn((n, H, D, D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    pool.qdr_pack(i32(torch, slots), S0)
+    o = run(torch, pool, SUM, slots, lens, x, [1] * n if carried else None)
+    check(torch, x, SUM, lens, 0, o, states(torch, pool, slots), S0 * float(carried))
+    packed = qdr.Pool(n, H, [8, 16], np.ones((H, D), np.float32))
+    packed.qdr_pack(i32(torch, slots), S0)
+    start = states(torch, packed, slots)
+    o = run(torch, packed, SUM, slots[:1] + [-1] * (n - 1), lens, x, [1] * n if carried else None)
+    assert (o[lens[0]:] == 0).all()
+    dense = fp32_pool(1, H)
+    dense.qdr_pack(i32(torch, [0]), start[:1].contiguous())
+    first = {k: y[:lens[0]].contiguous() for k, y in x.items()}
+    ref = run(torch, dense, SUM, [0], lens[:1], first, [1] if carried else None)
+    check(torch, first, SUM, lens[:1], 0, o[:lens[0]], states(torch, dense, [0]), start[:1] * float(carried))
+    check(torch, first, SUM, lens[:1], 0, ref, states(torch, dense, [0]), start[:1] * float(carried))
 
 
 def test_parts_of_a_prompt_equal_the_whole(torch_dev):
