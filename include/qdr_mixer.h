@@ -105,7 +105,8 @@ qdr_status qdr_kv_bytes(const qdr_kv_desc *desc, size_t *bytes);
  * (at least qdr_kv_bytes, 256-byte aligned, outlives the cache; NULL: the
  * library allocates).  The memory is zero-filled.  Synchronises the device. */
 qdr_status qdr_kv_create(const qdr_kv_desc *desc, void *dev_mem, size_t dev_bytes, qdr_kv **out);
-/* Free the cache.  Synchronises the device first.  NULL is accepted. */
+/* Free the cache.  Synchronises its device first, which need not be current.
+ * NULL is accepted. */
 qdr_status qdr_kv_destroy(qdr_kv *kv);
 
 /* Pages and contexts.  pages: int32 [n][max_pages], the page of tokens
@@ -113,8 +114,9 @@ qdr_status qdr_kv_destroy(qdr_kv *kv);
  * last page are not read.  context: int32 [n], the tokens of sequence b in
  * the cache, those of this call among them: its cu[b+1]-cu[b] rows are the
  * LAST of them, at positions context[b]-(cu[b+1]-cu[b]) .. context[b]-1.  A
- * context below a sequence's rows or above max_pages*page_tokens sets
- * QDR_DEVERR_LENGTH, and the sequence is skipped (rows to be returned are 0).
+ * context below a sequence's rows, above max_pages*page_tokens or above 2^30
+ * sets QDR_DEVERR_LENGTH, and the sequence is skipped (rows to be returned
+ * are 0).
  * A page outside [0, num_pages) sets QDR_DEVERR_PAGE: its tokens are not
  * written, read back as 0, and take no part in the attention. */
 
@@ -136,7 +138,8 @@ qdr_status qdr_kv_attend_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32
 /* Attention of new tokens over the cache, their own keys and values among it
  * (written before by qdr_kv_write on the same stream): for row t of sequence
  * b at position p and query head j, with key/value head j / (q_heads /
- * num_heads),   o = sum_{i <= p} softmax_i(scale q.k_i) v_i.
+ * num_heads),   o = sum_{i <= p} softmax_i(scale q.k_i) v_i.   scale: any sign,
+ * with scale log2(e) finite in fp32.
  * q, o: [T][q_heads][128] bfloat16; q_heads a multiple of num_heads.  One new
  * token a sequence, many, or both in one call.  Scores, the softmax and the
  * sums are fp32; the weights enter their product as bfloat16, twice where a

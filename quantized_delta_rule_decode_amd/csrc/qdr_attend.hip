@@ -98,8 +98,7 @@ __device__ __forceinline__ bool tile_of(const AttendArgs &A, const AttendPlan &p
   t.head = kvh * plan.group + part * heads;
   t.heads = min(heads, plan.group - part * heads);
   const int ctx = P.context[t.b];
-  const long long room = (long long)P.max_pages << P.page_shift;
-  t.skipped = ctx < t.len || ctx > room;
+  t.skipped = ctx < t.len || ctx > room_of(P);
   t.position = ctx - t.len + t.token;
   t.keys = t.skipped ? 0 : t.position + t.tokens;
   return true;

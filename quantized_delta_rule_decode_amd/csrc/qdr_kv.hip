@@ -39,8 +39,7 @@ __device__ __forceinline__ bool locate(const KvArgs &P, Where &at) {
   const int i = place - ((counts ? first / kBlock : 0) + 2 * b);
   if (!counts || len == 0 || i < 0) return false;
   const int ctx = P.context[b];
-  const long long room = (long long)P.max_pages << P.page_shift;
-  const bool fits = ctx >= len && ctx <= room;
+  const bool fits = ctx >= len && ctx <= room_of(P);
   const int p0 = fits ? ctx - len : 0;            // position of row 0; rows stay in place where they are only cleared
   const int block = p0 / kBlock + i;
   const int pos = block * kBlock;

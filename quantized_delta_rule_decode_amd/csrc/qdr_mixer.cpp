@@ -108,6 +108,12 @@ PromptSpace prompt_space(const qdr::PoolView &v, int32_t n, int32_t T) {
   return s;
 }
 
+// Whether a prompt's launches can be counted.
+qdr_status check_prompt(const qdr::PoolView &v, const PromptSpace &s, int32_t n) {
+  QDR_TRY(check_groups(s.places * v.num_heads));
+  return check_groups((n + s.segments) * v.num_heads * 16);   // of 512 threads, eight a head
+}
+
 }  // namespace
 
 namespace qdr {
@@ -217,7 +223,13 @@ extern "C" {
 qdr_status qdr_prompt_workspace(const qdr_pool *pool, int32_t n, int32_t T, size_t *bytes) {
   if (!pool || !bytes) return fail(QDR_E_INVAL, "pool or bytes is NULL");
   QDR_TRY(check_counts(n, T));
-  *bytes = n == 0 ? 0 : prompt_space(qdr::pool_view(pool), n, T).total();
+  *bytes = 0;
+  if (n == 0) return qdr::set_ok();
+  const qdr::PoolView view = qdr::pool_view(pool);
+  if (view.num_heads > kMostHeads) return fail(QDR_E_UNSUPPORTED, "the prompt form takes at most %d heads (got %d)", kMostHeads, view.num_heads);
+  const PromptSpace space = prompt_space(view, n, T);
+  QDR_TRY(check_prompt(view, space, n));
+  *bytes = space.total();
   return qdr::set_ok();
 }
 
@@ -238,8 +250,7 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
   if (view.num_heads > kMostHeads) return fail(QDR_E_UNSUPPORTED, "the prompt form takes at most %d heads (got %d)", kMostHeads, view.num_heads);
   QDR_TRY(check_device(view.device));
   const PromptSpace space = prompt_space(view, n, T);
-  QDR_TRY(check_groups(space.places * view.num_heads));
-  QDR_TRY(check_groups((n + space.segments) * view.num_heads * 16));   // of 512 threads, eight a head
+  QDR_TRY(check_prompt(view, space, n));
   QDR_TRY(check_workspace(workspace, workspace_bytes, space.total()));
   hipStream_t st = static_cast<hipStream_t>(stream);
   QDR_TRY(qdr::pool_check_slots(pool, slots, n, st));
@@ -380,8 +391,13 @@ qdr_status qdr_kv_create(const qdr_kv_desc *desc, void *dev_mem, size_t dev_byte
 
 qdr_status qdr_kv_destroy(qdr_kv *kv) {
   if (!kv) return qdr::set_ok();
+  const int own = kv->device;
+  int now = own;
+  (void)hipGetDevice(&now);
+  if (now != own) (void)hipSetDevice(own);
   (void)hipDeviceSynchronize();
   free_kv(kv);
+  if (now != own) (void)hipSetDevice(now);
   return qdr::set_ok();
 }
 
@@ -449,18 +465,21 @@ qdr_status qdr_kv_attend(qdr_kv *kv, const int32_t *pages, int32_t max_pages, co
   qdr::AttendPlan plan;
   QDR_TRY(make_plan(kv, n, T, q_heads, max_pages, &plan));
   QDR_TRY(check_workspace(workspace, workspace_bytes, (plan.few_floats + plan.many_floats) * sizeof(float)));
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return fail(QDR_E_INVAL, "scale is too large (%g)", (double)scale);
   qdr::AttendArgs a{};
   a.kv = kv_args(kv, pages, max_pages, cu, context, n, T);
   a.q = q;
   a.o = o;
   a.q_heads = q_heads;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.part = static_cast<float *>(workspace);
   return launched(qdr::launch_attend(a, plan, kv->desc.kind, static_cast<hipStream_t>(stream)));
 }
 
 qdr_status qdr_kv_poll_device_error(qdr_kv *kv, uint32_t *flags) {
   if (!kv || !flags) return fail(QDR_E_INVAL, "kv or flags is NULL");
+  QDR_TRY(check_device(kv->device));
   hipError_t e = hipDeviceSynchronize();
   if (e == hipSuccess) e = hipMemcpy(flags, kv->d_err, sizeof(uint32_t), hipMemcpyDeviceToHost);
   if (e == hipSuccess) e = hipMemset(kv->d_err, 0, sizeof(uint32_t));

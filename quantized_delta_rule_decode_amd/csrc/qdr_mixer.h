@@ -72,6 +72,7 @@ hipError_t launch_linear_step(const LinearArgs &, bool bf16, hipStream_t);
 //       8-bit codes keep the two tiles of a pair in one lane's 16 B
 //   8-bit only: fp32 scales of the 32 keys, then of the 32 values.
 constexpr int kBlock = 32;
+constexpr int kMostContext = 1 << 30;
 constexpr uint32_t kKv8Half = 4096, kKv8Scale = 2 * kKv8Half, kKv8Block = kKv8Scale + 2 * kBlock * 4;
 constexpr uint32_t kKv16Half = 8192, kKv16Block = 2 * kKv16Half;
 

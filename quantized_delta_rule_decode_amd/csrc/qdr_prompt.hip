@@ -905,7 +905,11 @@ __global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
   const int l = threadIdx.x & 63, per = P.segment * kChunk;
   int first, len;
   const int slot = P.slots[b];
-  if (!rows_of(P.cu, P.T, b, &first, &len) || slot < 0 || slot >= P.num_slots) return;
+  if (!rows_of(P.cu, P.T, b, &first, &len)) {   // no segment of k_prompt_scan may be this sequence's
+    if (threadIdx.x == 0) atomicOr(P.err, kErrLength);
+    return;
+  }
+  if (slot < 0 || slot >= P.num_slots) return;
   const int segments = (len + per - 1) / per, place = first / per + b;
   if (segments < 2) return;
   f32x4 S = {0, 0, 0, 0};

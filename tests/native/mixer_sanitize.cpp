@@ -21,6 +21,7 @@ static int device = 0, launches = 0;
 static bool no_memory = false;
 extern "C" {
 hipError_t hipGetDevice(int *d) { *d = device; return hipSuccess; }
+hipError_t hipSetDevice(int d) { device = d; return hipSuccess; }
 hipError_t hipGetLastError(void) { return hipSuccess; }
 const char *hipGetErrorString(hipError_t) { return "stub"; }
 hipError_t hipMalloc(void **p, size_t n) {
@@ -93,6 +94,11 @@ static int prompts() {
   REFUSED(qdr_prompt_workspace(&pool, 1, 1, nullptr), QDR_E_INVAL);
   REFUSED(qdr_prompt_workspace(&pool, -1, 1, &need), QDR_E_INVAL);
   REFUSED(qdr_prompt_workspace(&pool, 1, -1, &need), QDR_E_INVAL);
+  REFUSED(qdr_prompt_workspace(&pool, 1 << 23, 5, &need), QDR_E_INVAL);      // launch too large
+  REFUSED(qdr_prompt_workspace(&pool, 1, 1 << 30, &need), QDR_E_INVAL);
+  view.num_heads = 1 << 20;
+  REFUSED(qdr_prompt_workspace(&pool, 1, 5, &need), QDR_E_UNSUPPORTED);
+  view.num_heads = 2;
   auto call = [&](int rule, const int32_t *slots, const int32_t *cu, int n, int T, const uint16_t *q, const float *beta,
                   const float *gate, uint16_t *o, void *w, size_t bytes) {
     return qdr_prompt(&pool, rule, slots, nullptr, cu, n, T, q, x, x, beta, gate, o, w, bytes, nullptr);
@@ -212,6 +218,9 @@ static int caches() {
   REFUSED(attend(i, 1, 5, 4, odd, 0.1f, mem, n), QDR_E_INVAL);
   REFUSED(attend(i, 1, 5, 4, x, NAN, mem, n), QDR_E_INVAL);
   REFUSED(attend(i, 1, 5, 4, x, INFINITY, mem, n), QDR_E_INVAL);
+  REFUSED(attend(i, 1, 5, 4, x, 3e38f, mem, n), QDR_E_INVAL);     // times log2(e): infinity
+  REFUSED(attend(i, 1, 5, 4, x, -3e38f, mem, n), QDR_E_INVAL);
+  CHECK(attend(i, 1, 5, 4, x, -2e38f, mem, n) == QDR_OK);
   REFUSED(attend(i, 1 << 22, 5, 4, x, 0.1f, mem, n), QDR_E_INVAL);
   size_t large = 0;
   CHECK(qdr_kv_attend_workspace(kv, 1, 64, 4, 4096, &large) == QDR_OK && large > 0);
@@ -221,7 +230,10 @@ static int caches() {
   REFUSED(qdr_kv_attend_workspace(kv, 1, 64, 4, -1, &n), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_workspace(kv, 1, 64, 4, 1, nullptr), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_workspace(nullptr, 1, 64, 4, 1, &n), QDR_E_INVAL);
-  CHECK(qdr_kv_destroy(kv) == QDR_OK);
+  device = 1;
+  REFUSED(qdr_kv_poll_device_error(kv, &flags), QDR_E_INVAL);
+  CHECK(qdr_kv_destroy(kv) == QDR_OK && device == 1);    // any device may be current
+  device = 0;
   return 0;
 }
 

@@ -417,6 +417,65 @@ def test_a_prompt_in_chunks_and_tokens(torch_dev):
             assert ((o.double() - ref).abs() <= room).all()
 
 
+@pytest.mark.parametrize("kind", [INT8, BF16])
+def test_cache_beyond_32_bits(torch_dev, kind):
+    """Pages that lie above 2^32 bytes of the cache."""
+    torch = torch_dev
+    H, page = 2, 1024
+    pages = (2 ** 32 + 2 ** 30) // qdr.qdr_kv_bytes(1, page, H, kind)
+    cache, small = qdr.KVCache(pages, page, H, kind), qdr.KVCache(4, page, H, kind)
+    lens, contexts = [1, 200], [1500, 2000]
+    k, v = vectors(torch, 31, 3500, H), vectors(torch, 32, 3500, H)
+    q = vectors(torch, 33, 201, 4 * H)
+    got = []
+    for c, where in ((small, [[2, 0], [1, 3]]), (cache, [[pages - 1, pages - 4], [0, pages - 2]])):
+        t, all_of = i32(torch, where), counts(torch, contexts)
+        c.qdr_kv_write(t, all_of, i32(torch, contexts), k, v)
+        rk, rv, o = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+        c.qdr_kv_read(t, all_of, i32(torch, contexts), rk, rv)
+        c.qdr_kv_attend(t, counts(torch, lens), i32(torch, contexts), q, o)
+        assert c.qdr_kv_poll_device_error() == 0
+        got.append((rk, rv, o))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.equal(got[0][0], held(torch, k, kind).bfloat16())
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_largest_context(torch_dev, rows):
+    """2^30 tokens, a cache's pages over and over; one token more is refused."""
+    torch = torch_dev
+    page, most = 1024, 2 ** 30
+    cache = qdr.KVCache(1, page, 1, INT8)
+    k, v = vectors(torch, 34, page, 1), vectors(torch, 35, page, 1)
+    table_ = torch.zeros((1, most // page + 1), dtype=torch.int32, device="cuda")
+    cache.qdr_kv_write(table_, i32(torch, [0, page]), i32(torch, [page]), k, v)
+    q, cu = vectors(torch, 36, rows, 1), i32(torch, [0, rows])
+    for context in (most + 1, most + page):
+        o, x = torch.full_like(q, 7), torch.full_like(q, 7)
+        cache.qdr_kv_attend(table_, cu, i32(torch, [context]), q, o)
+        assert cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH and not o.any()
+        cache.qdr_kv_read(table_, cu, i32(torch, [context]), x, x.clone())
+        assert cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH and not x.any()
+        cache.qdr_kv_write(table_, cu, i32(torch, [context]), q, q)
+        assert cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH
+    x, y = torch.empty_like(k), torch.empty_like(v)
+    cache.qdr_kv_read(table_, i32(torch, [0, page]), i32(torch, [most]), x, y)      # its last page's tokens
+    assert torch.equal(x, held(torch, k, INT8).bfloat16()) and torch.equal(y, held(torch, v, INT8).bfloat16())
+    # The whole context: every key 2^20 times, so the result is the page's own
+    # attention.  A row misses up to 40 of the 2^30 tokens (40 / 2^20 of the
+    # weights' sum at most), and no running sum has more than 2^20 terms
+    # (2^20 u = 2^-4 of the weighted values).
+    o = torch.empty_like(q)
+    cache.qdr_kv_attend(table_, cu, i32(torch, [most]), q, o)
+    K, V = held(torch, k, INT8).double(), held(torch, v, INT8).double()
+    for i in range(rows):
+        ref, room = reference(torch, q[i:i + 1], K, V, [1], [page], D ** -0.5)
+        room = room + (2.0 ** -4 + 80 / 2 ** 20) * V.abs().amax(0)
+        assert ((o[i:i + 1].double() - ref).abs() <= room).all(), i
+    assert cache.qdr_kv_poll_device_error() == 0
+
+
 def test_refusals(torch_dev):
     torch = torch_dev
     cache = qdr.KVCache(2, 32, 2, INT8)

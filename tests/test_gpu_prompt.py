@@ -303,6 +303,32 @@ def test_prompt_errors_on_the_device(torch_dev):
         o = torch.full((100, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
         pool.qdr_prompt(DELTA, i32(torch, [0, 1]), i32(torch, cu), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
         assert pool.qdr_poll_device_error() == qdr.DEVERR_LENGTH, cu
+    # and where sequences are cut into segments
+    x = make(torch, 52, 900, H)
+    for cu in ([0, 900, 5, 900], [0, 901, 901, 901], [0, 400, 400, 2 ** 31 - 1], [0, -7, 300, 900], [900, 0, 0, 0], [0, 300, 700, 699]):
+        for rule in (SUM, DELTA):
+            o = torch.full((900, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+            pool.qdr_prompt(rule, i32(torch, [0, -1, 1]), i32(torch, cu), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
+            assert pool.qdr_poll_device_error() == qdr.DEVERR_LENGTH, cu
+    pool.close()
+
+
+@pytest.mark.parametrize("rule", [DELTA, SUM])
+def test_prompt_rows_beyond_32_bits(torch_dev, rule):
+    """Rows whose elements and bytes are numbered above 2^31 and 2^32."""
+    torch = torch_dev
+    H, far, L = 64, 262_200, 300
+    pool = fp32_pool(2, H)
+    y = make(torch, 53, L, H)
+    x = {m: torch.empty((far + L, *t.shape[1:]), dtype=t.dtype, device="cuda") for m, t in y.items()}
+    for m in y:
+        x[m][far:] = y[m]
+    o = torch.full((far + L, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    # the sequence before it is skipped: its rows of o are cleared
+    pool.qdr_prompt(rule, i32(torch, [-1, 1]), i32(torch, [0, far, far + L]), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
+    check(torch, y, rule, [L], 0, o[far:], states(torch, pool, [1]), torch.zeros((1, H, D, D), device="cuda"))
+    assert not o[:far].any() and pool.qdr_poll_device_error() == 0
+    pool.close()
 
 
 def test_prompt_refusals(torch_dev, monkeypatch):
