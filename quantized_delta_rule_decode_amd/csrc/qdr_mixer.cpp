@@ -71,11 +71,53 @@ bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Sequences cut into segments of so many chunks (0: not cut), and places of
+// segments of one head.
+struct Cut {
+  int32_t chunks;
+  int64_t places;
+};
+
+// SUM: as many segments as there are places for workgroups (two to each of 256
+// compute units), four chunks at least.  16385 tokens of 16 heads in segments
+// of 4, 8, 16, 32 chunks and uncut: 170, 148, 173, 271, 1396 us.  Where the
+// sequences alone fill the places, only one of twice the mean length is cut:
+// 32 x 1024 tokens of 16 heads cut at the half 273 us, uncut 200, and one long
+// sequence among short ones still does not run alone.
+Cut cut_sum(int32_t heads, int32_t n, int32_t T) {
+  const int64_t chunks = T / qdr::kChunk, places = 2 * 256;
+  int64_t want = chunks * heads / places;
+  if ((int64_t)n * heads >= places) want = std::max<int64_t>(want, 2 * (chunks / n));
+  int64_t segment = qdr::kSegmentLeast;
+  while (segment < want) segment *= 2;
+  if (segment * qdr::kChunk >= T) return {0, 0};
+  return {(int32_t)segment, T / (segment * qdr::kChunk) + n};
+}
+
+// DELTA: a segment's map of states costs twice what its chunks cost, so only
+// calls of few heads are cut, where most compute units would have nothing to
+// do, and only if the longest sequence (a call of several: taken as twice the
+// mean) is worth three launches.  One sequence, chain against segments, us:
+//   4 heads   16 chunks 57 / 67   24 chunks 79 / 72    512 chunks 1434 / 258
+//   16 heads  24 chunks 82 / 80   64 chunks 199 / 135  512 chunks 1612 / 613
+//   32 heads  32 chunks 108 / 125 64 chunks 213 / 201  256 chunks 854 / 595
+//   48 heads  187 chunks 689 / 788   512 chunks 1780 / 1835
+// Their length: one workgroup a compute unit, and not so many that joining
+// them one by one takes longer than their chunks (4 heads, 512 chunks, in
+// segments of 4, 8, 16, 32: 395, 273, 258, 386 us).
+Cut cut_delta(int32_t heads, int32_t n, int32_t T) {
+  const int64_t chunks = T / qdr::kChunk, pairs = (int64_t)n * heads;
+  const int64_t longest = n == 1 ? chunks : 2 * (chunks / n);
+  if (pairs > 32 || longest < std::max<int64_t>(24, 2 * pairs)) return {0, 0};
+  int64_t segment = qdr::kSegmentLeast;
+  while (segment * 256 < chunks * heads || 4 * segment * segment < chunks) segment *= 2;
+  return {(int32_t)segment, T / (segment * qdr::kChunk) + n};
+}
+
 // Parts of a prompt's workspace.  It is the same for both rules.
 struct PromptSpace {
   int64_t places;                // chunk places of one head
-  int32_t segment;               // chunks of a segment (0: sequences are not cut)
-  int64_t segments;              // segment places of one head
+  Cut sum, delta;
   bool ordered;
   size_t chunks, tables, states, parts;  // bytes
   size_t total() const { return chunks + tables + states + parts; }
@@ -89,29 +131,18 @@ PromptSpace prompt_space(const qdr::PoolView &v, int32_t n, int32_t T) {
   s.ordered = n > 1 && n <= qdr::kMostOrdered;
   s.tables = up((size_t)n * ((v.all_fp32 ? 0 : 2) + (s.ordered ? 1 : 0)) * sizeof(int32_t));
   s.states = v.all_fp32 ? 0 : (size_t)n * state;
-  // SUM's segments: as many as there are places for workgroups (two to each of
-  // 256 compute units), four chunks at least.  16385 tokens of 16 heads in
-  // segments of 4, 8, 16, 32 chunks and uncut: 170, 148, 173, 271, 1396 us.
-  // Where the sequences alone fill the places, only one of twice the mean
-  // length is cut: 32 x 1024 tokens of 16 heads cut at the half 273 us, uncut
-  // 200, and one long sequence among short ones still does not run alone.
-  const int64_t places = 2 * 256, pairs = (int64_t)n * v.num_heads;
-  int64_t want = (int64_t)T / qdr::kChunk * v.num_heads / places;
-  if (pairs >= places) want = std::max<int64_t>(want, 2 * ((int64_t)T / qdr::kChunk / n));
-  int64_t segment = qdr::kSegmentLeast;
-  while (segment < want) segment *= 2;
-  if (segment * qdr::kChunk < T) {
-    s.segment = (int32_t)segment;
-    s.segments = T / (segment * qdr::kChunk) + n;
-    s.parts = up((size_t)s.segments * (state + v.num_heads * sizeof(float)));
-  }
+  s.sum = cut_sum(v.num_heads, n, T);
+  s.delta = cut_delta(v.num_heads, n, T);
+  s.parts = up(std::max((size_t)s.sum.places * (state + v.num_heads * sizeof(float)),
+                        (size_t)s.delta.places * (state + v.num_heads * qdr::kMapFloats * sizeof(float))));
   return s;
 }
 
 // Whether a prompt's launches can be counted.
 qdr_status check_prompt(const qdr::PoolView &v, const PromptSpace &s, int32_t n) {
   QDR_TRY(check_groups(s.places * v.num_heads));
-  return check_groups((n + s.segments) * v.num_heads * 16);   // of 512 threads, eight a head
+  // of 512 threads: segments, and to join them eight a head
+  return check_groups((n + std::max(s.sum.places, s.delta.places)) * v.num_heads * 16);
 }
 
 }  // namespace
@@ -283,11 +314,14 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
     table += 2 * (size_t)n;
     a.S = reinterpret_cast<float *>(ws + space.chunks + space.tables);
   }
-  if (delta && space.ordered) a.order = table;
-  if (!delta && space.segment) {
-    a.segment = space.segment;
-    a.segments = (int32_t)space.segments;
+  const Cut cut = delta ? space.delta : space.sum;
+  if (cut.chunks) {
+    a.segment = cut.chunks;
+    a.segments = (int32_t)cut.places;
     a.segment_ws = reinterpret_cast<float *>(ws + space.chunks + space.tables + space.states);
+    a.map_ws = a.segment_ws + (size_t)cut.places * view.num_heads * QDR_DIM * QDR_DIM;
+  } else if (delta && space.ordered) {
+    a.order = table;
   }
   hipError_t e = qdr::pool_after_writeback(pool, st);
   if (e == hipSuccess && !a.pool) e = qdr::launch_prompt_slots(a, st);

@@ -22,6 +22,7 @@ constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
 // one triangular matrix.
 constexpr size_t kDecayFloats = 4 * kChunk, kChunkFloats = kDecayFloats + kTriFloats;
 constexpr int kSegmentLeast = 4;   // chunks of a segment
+constexpr size_t kMapFloats = (size_t)8 * 4 * 3 * 64 * 4;   // a 128 x 128 left operand in three parts
 // Sequences of a call that are put in order of length (n^2 comparisons).
 constexpr int kMostOrdered = 1024;
 
@@ -39,10 +40,11 @@ struct PromptArgs {
   float *S;                   // [n][H][128][128]
   int32_t *slots_in, *slots_out;   // dense: slots to unpack and to pack (-1: none)
   int32_t *order;             // DELTA: [n] sequences by falling length; NULL: as they come
-  // SUM: a sequence is cut into segments of so many chunks that are taken side
-  // by side (0: not cut); places of segments of a head, and their states
+  // a sequence is cut into segments of so many chunks that are taken side by
+  // side (0: not cut); places of segments of a head, and their states
   int32_t segment, segments;
-  float *segment_ws;          // [segments][H][128*128], then [segments][H] decays
+  float *segment_ws;          // [segments][H][128*128]
+  float *map_ws;              // SUM: [segments][H] decays, DELTA: [segments][H][kMapFloats]
   uint32_t *err;
 };
 hipError_t launch_prompt_slots(const PromptArgs &, hipStream_t);

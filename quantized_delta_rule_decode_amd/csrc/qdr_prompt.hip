@@ -522,11 +522,11 @@ __device__ __forceinline__ bool scan_at(const PromptArgs &P, int place, int *b, 
 // A segment's state in the workspace: a thread's eight results side by side
 // with its neighbours'; before k_prompt_join what the segment adds to a state,
 // and the decay over it, then the state that it starts from.
-__device__ __forceinline__ f32x4 *segment_ws(const PromptArgs &P, int place, int h) {
-  return (f32x4 *)P.segment_ws + ((size_t)place * P.H + h) * (kD * kD / 4) + threadIdx.x;
+__device__ __forceinline__ f32x4 *segment_ws(const PromptArgs &P, int place, int h, int tid) {
+  return (f32x4 *)P.segment_ws + ((size_t)place * P.H + h) * (kD * kD / 4) + tid;
 }
 __device__ __forceinline__ float *segment_decay(const PromptArgs &P, int place, int h) {
-  return (float *)((f32x4 *)P.segment_ws + (size_t)P.segments * P.H * (kD * kD / 4)) + (size_t)place * P.H + h;
+  return P.map_ws + (size_t)place * P.H + h;
 }
 
 // The state of a (sequence, head) where it lives.
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
   f32x4 S[8];
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    if (segments > 1) S[m] = segment_ws(P, place, A.h)[m * 512];
+    if (segments > 1 && (!DELTA || from > 0)) S[m] = segment_ws(P, place, A.h, threadIdx.x)[m * 512];
     else if (carried) S[m] = state.get(state_row(m, g), col);
     else S[m] = (f32x4){0, 0, 0, 0};
   }
@@ -894,7 +894,7 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
     lds_barrier();
   }
 #pragma unroll
-  for (int m = 0; m < 8; ++m) segment_ws(P, place, A.h)[m * 512] = S[m];
+  for (int m = 0; m < 8; ++m) segment_ws(P, place, A.h, threadIdx.x)[m * 512] = S[m];
   if (threadIdx.x == 0) *segment_decay(P, place, A.h) = decay;
 }
 
@@ -914,13 +914,171 @@ __global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
   if (segments < 2) return;
   f32x4 S = {0, 0, 0, 0};
   if (P.carry != nullptr && P.carry[b] != 0) S = StateAt(P, b, slot, h).get(state_row(m, l >> 4), (threadIdx.x >> 6) * 16 + (l & 15));
-  f32x4 next = segment_ws(P, place, h)[m * 512];
+  f32x4 next = segment_ws(P, place, h, threadIdx.x)[m * 512];
   for (int i = 0; i < segments; ++i) {
     const f32x4 add = next;
     const float decay = *segment_decay(P, place + i, h);   // (the last one's is not used)
-    if (i + 1 < segments) next = segment_ws(P, place + i + 1, h)[m * 512];
-    segment_ws(P, place + i, h)[m * 512] = S;
+    if (i + 1 < segments) next = segment_ws(P, place + i + 1, h, threadIdx.x)[m * 512];
+    segment_ws(P, place + i, h, threadIdx.x)[m * 512] = S;
     S = S * decay + add;
+  }
+}
+
+// DELTA: what a segment makes of the state S it starts from is P S + B.  A
+// workgroup computes B (from S = 0; of a sequence's first segment the state
+// that it ends in) or P (from S = 1 and without values), which goes out as the
+// left operands of the join: [result][contraction step][part][lane].
+__device__ __forceinline__ u32x4 *map_ws(const PromptArgs &P, int place, int h) {
+  return (u32x4 *)P.map_ws + ((size_t)place * P.H + h) * (kMapFloats / 4);
+}
+
+__global__ void __launch_bounds__(512, 2) k_prompt_map(PromptArgs P) {
+  __shared__ __attribute__((aligned(16))) union {
+    Stage<true> st;
+    float S[kD][kD + 4];
+  } sh;
+  const int l = threadIdx.x & 63, g = l >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int bh = blockIdx.x >> 1, place = bh / P.H, col = 16 * wave + (l & 15);
+  const bool turn = blockIdx.x & 1;      // P
+  int b, from, to, segments;
+  ScanAt A;
+  A.h = bh % P.H;
+  if (!scan_at(P, place, &b, &from, &to, &segments, A) || to >= A.chunks || (turn && from == 0)) return;
+  const int slot = P.slots[b];
+  if (slot < 0 || slot >= P.num_slots) return;
+  const bool carried = from == 0 && P.carry != nullptr && P.carry[b] != 0;
+  const StateAt state(P, b, slot, A.h);
+  f32x4 S[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    S[m] = carried ? state.get(state_row(m, g), col) : (f32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (turn && state_row(m, g) + r == col) S[m][r] = 1.0f;
+  }
+  StageIn<true, false> in;
+  fetch<true, false>(P, A, from, threadIdx.x, in);
+  for (int c = from; c < to; ++c) {
+    put<true, false>(A, c, threadIdx.x, in, sh.st);
+    lds_barrier();
+    fetch<true, false>(P, A, min(c + 1, to - 1), threadIdx.x, in);
+    f32x4 r[4], u[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) r[t] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      Frag f[3], k[4];
+      split8<3>(S[2 * s], S[2 * s + 1], f);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) k[t] = rows_operand(sh.st.K[t], s, l);
+#pragma unroll
+      for (int x = 2; x >= 0; --x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[x], r[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const f32x4 decay = *(const f32x4 *)&sh.st.dec[16 * t + 4 * g];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float v = turn ? 0.0f : __uint_as_float((uint32_t)sh.st.V[16 * t + 4 * g + x][col] << 16);
+        r[t][x] = __builtin_fmaf(-decay[x], r[t][x], v);
+      }
+    }
+    solve(sh.st.T, r, u, l);
+    update_state<false>(sh.st.K, sh.st.dec, u, S, l);
+    lds_barrier();
+  }
+  if (!turn) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) segment_ws(P, place, A.h, threadIdx.x)[m * 512] = S[m];
+    return;
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sh.S[state_row(m, g) + r][col] = S[m][r];
+  lds_barrier();
+  // row i of result m is channel state_row(m, i >> 2) + (i & 3)
+  const int m = wave, i = l & 15, row = state_row(m, i >> 2) + (i & 3);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    Frag f[3];
+    split8<3>(*(const f32x4 *)&sh.S[row][32 * s + 8 * g], *(const f32x4 *)&sh.S[row][32 * s + 8 * g + 4], f);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) map_ws(P, place, A.h)[((m * 4 + s) * 3 + x) * 64 + l] = f[x].w;
+  }
+}
+
+// DELTA: the states that the segments from the second on start from.  A
+// workgroup takes sixteen columns of a (sequence, head); wave w makes results
+// 2 w and 2 w + 1, which are what contraction step w needs of the next state,
+// and has the next segment's operands on their way.
+__global__ void __launch_bounds__(256, 1) k_prompt_join_maps(PromptArgs P) {
+  __shared__ __attribute__((aligned(16))) u32x4 sf[2][4][3][64];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int cols = blockIdx.x % 8, h = blockIdx.x / 8 % P.H, b = blockIdx.x / (8 * P.H);
+  const int per = P.segment * kChunk;
+  int first, len;
+  const int slot = P.slots[b];
+  if (!rows_of(P.cu, P.T, b, &first, &len) || slot < 0 || slot >= P.num_slots) return;   // (k_prompt_scan tells)
+  const int segments = (len + per - 1) / per, place = first / per + b;
+  if (segments < 2) return;
+  struct In {
+    u32x4 a[2][4][3];
+    f32x4 add[2];
+  };
+  auto state = [&](int i) { return segment_ws(P, place + i, h, 64 * cols + l) + 2 * w * 512; };
+  auto load = [&](int i, In &in) {   // (there is none of the last segment: that of the one before again)
+    const u32x4 *map = map_ws(P, place + min(i, segments - 2), h) + l;
+    const f32x4 *add = state(min(i, segments - 2));
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      in.add[y] = add[y * 512];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) in.a[y][s][x] = map[(((2 * w + y) * 4 + s) * 3 + x) * 64];
+    }
+  };
+  f32x4 S[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) S[y] = state(0)[y * 512];
+  auto step = [&](int i, In &in) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) state(i)[y * 512] = S[y];
+    if (i + 1 == segments) return;
+    Frag f[3];
+    split8<3>(S[0], S[1], f);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) sf[i & 1][w][x][l] = f[x].w;
+    lds_barrier();
+#pragma unroll
+    for (int y = 0; y < 2; ++y) S[y] = in.add[y];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int z = 2; z >= 0; --z) {
+        Frag f, a;
+        f.w = sf[i & 1][s][z][l];
+#pragma unroll
+        for (int x = 2 - z; x >= 0; --x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            a.w = in.a[y][s][x];
+            S[y] = mma(a, f, S[y]);
+          }
+      }
+  };
+  In odd, even;
+  if (segments > 2) load(1, odd);
+  for (int i = 1; i < segments; i += 2) {
+    if (i + 1 < segments) load(i + 1, even);
+    step(i, odd);
+    if (i + 1 >= segments) break;
+    if (i + 2 < segments) load(i + 2, odd);
+    step(i + 1, even);
   }
 }
 
@@ -963,6 +1121,12 @@ hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st)
 
 hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
   if (delta) {
+    if (a.segment) {
+      hipLaunchKernelGGL(k_prompt_map, dim3(a.segments * a.H * 2), dim3(512), 0, st, a);
+      hipLaunchKernelGGL(k_prompt_join_maps, dim3(a.n * a.H * 8), dim3(256), 0, st, a);
+      hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.segments * a.H), dim3(512), 0, st, a);
+      return hipGetLastError();
+    }
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
     // Few heads: four workgroups to a chain, a workgroup a compute unit.  4096
     // tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight

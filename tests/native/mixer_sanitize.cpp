@@ -38,6 +38,7 @@ hipError_t hipDeviceSynchronize(void) { return hipSuccess; }
 static std::string message;
 static qdr::PoolView view;
 static qdr::AttendPlan last_plan;
+static qdr::PromptArgs last_prompt;
 struct qdr_pool { int unused; };
 namespace qdr {
 PoolView pool_view(const qdr_pool *) { return view; }
@@ -49,7 +50,11 @@ qdr_status pool_pack(qdr_pool *, const int32_t *, int32_t, const float *, hipStr
 qdr_status pool_unpack(qdr_pool *, const int32_t *, int32_t, float *, hipStream_t) { ++launches; return QDR_OK; }
 hipError_t launch_prompt_slots(const PromptArgs &, hipStream_t) { ++launches; return hipSuccess; }
 hipError_t launch_prompt_chunks(const PromptArgs &, bool, hipStream_t) { ++launches; return hipSuccess; }
-hipError_t launch_prompt_scan(const PromptArgs &, bool, hipStream_t) { ++launches; return hipSuccess; }
+hipError_t launch_prompt_scan(const PromptArgs &a, bool, hipStream_t) {
+  last_prompt = a;
+  ++launches;
+  return hipSuccess;
+}
 hipError_t launch_linear_step(const LinearArgs &, bool, hipStream_t) { ++launches; return hipSuccess; }
 hipError_t launch_kv_write(const KvArgs &, int, hipStream_t) { ++launches; return hipSuccess; }
 hipError_t launch_kv_read(const KvArgs &, int, hipStream_t) { ++launches; return hipSuccess; }
@@ -130,6 +135,27 @@ static int prompts() {
   view.gate = QDR_GATE_DIAG;
   REFUSED(call(QDR_RULE_SUM, i, i, 1, 5, x, f, f, x, ws, need), QDR_E_UNSUPPORTED);
   view.gate = QDR_GATE_SCALAR;
+
+  // which calls are cut into segments, and that their parts fit the workspace
+  struct { int rule, heads, n, T, segment; } cuts[] = {
+      {QDR_RULE_DELTA, 2, 1, 1500, 0},   {QDR_RULE_DELTA, 2, 1, 1700, 4},  {QDR_RULE_DELTA, 4, 1, 32768, 16}, {QDR_RULE_DELTA, 32, 1, 32768, 64},
+      {QDR_RULE_DELTA, 33, 1, 32768, 0}, {QDR_RULE_DELTA, 32, 1, 2048, 0}, {QDR_RULE_DELTA, 2, 5, 3865, 4},  {QDR_RULE_DELTA, 2, 5, 3000, 0},
+      {QDR_RULE_SUM, 2, 1, 256, 0},      {QDR_RULE_SUM, 2, 1, 257, 4},     {QDR_RULE_SUM, 16, 1, 16385, 8},  {QDR_RULE_SUM, 16, 32, 32768, 32}};
+  for (const auto &c : cuts) {
+    view.num_heads = c.heads;
+    CHECK(qdr_prompt_workspace(&pool, c.n, c.T, &need) == QDR_OK);
+    char *space = (char *)std::aligned_alloc(256, (need + 255) / 256 * 256);
+    CHECK(call(c.rule, i, i, c.n, c.T, x, f, f, x, space, need) == QDR_OK && last_prompt.segment == c.segment);
+    const size_t cells = (size_t)last_prompt.segments * c.heads;
+    if (c.segment) {
+      CHECK(last_prompt.segments == c.T / (64 * c.segment) + c.n && (char *)(last_prompt.segment_ws + cells * 16384) == (char *)last_prompt.map_ws);
+      CHECK((char *)(last_prompt.map_ws + cells * (c.rule == QDR_RULE_DELTA ? qdr::kMapFloats : 1)) <= space + need);
+      CHECK((char *)last_prompt.segment_ws >= space + (size_t)last_prompt.chunks * c.heads * qdr::kDecayFloats * 4);
+    }
+    std::free(space);
+  }
+  view.num_heads = 2;
+  CHECK(qdr_prompt_workspace(&pool, 1, 5, &need) == QDR_OK);
 
   // the step: uncompressed pools only
   CHECK(qdr_linear_step(&pool, i, 3, f, f, f, f, f, nullptr) == QDR_OK);

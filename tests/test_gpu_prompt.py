@@ -165,6 +165,54 @@ def test_prompt_many_heads(torch_dev, rule):
     assert pool.qdr_poll_device_error() == qdr.DEVERR_SLOT
 
 
+@pytest.mark.parametrize("lens,carried,gates", [([1700], True, "one"), ([2500, 0, 1300, 64, 1], False, "mixed"), ([1024, 1100], True, "zeros")], ids=str)
+def test_long_delta_prompts(torch_dev, lens, carried, gates):
+    """Prompts of several segments, joined by their maps of states."""
+    torch = torch_dev
+    n, H = len(lens), 2
+    x = make(torch, 17, sum(lens), H, gates)
+    pool = fp32_pool(n, H)
+    slots = list(range(n))[::-1]
+    S0 = torch.randn((n, H, D, D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    pool.qdr_pack(i32(torch, slots), S0)
+    o = run(torch, pool, DELTA, slots, lens, x, [1] * n if carried else None)
+    check(torch, x, DELTA, lens, 0, o, states(torch, pool, slots), S0 * float(carried))
+    # some are padding, and the first is the only one that continues
+    pool.qdr_pack(i32(torch, slots), S0)
+    p = run(torch, pool, DELTA, slots[:1] + [-1] * (n - 1), lens, x, [1] + [0] * (n - 1))
+    assert not p[lens[0]:].any()
+    first = {k: y[:lens[0]].contiguous() for k, y in x.items()}
+    check(torch, first, DELTA, lens[:1], 0, p[:lens[0]], states(torch, pool, slots[:1]), S0[:1])
+    assert torch.equal(states(torch, pool, slots[1:]), S0[1:])
+    packed = qdr.Pool(n, H, [8, 16], np.ones((H, D), np.float32))
+    packed.qdr_pack(i32(torch, slots), S0)
+    start = states(torch, packed, slots)
+    o = run(torch, packed, DELTA, slots, lens, x, [1] * n if carried else None)
+    dense = fp32_pool(n, H)
+    dense.qdr_pack(i32(torch, slots), start)
+    assert torch.equal(o, run(torch, dense, DELTA, slots, lens, x, [1] * n if carried else None))
+
+
+def test_prompt_non_finite_in_segments(torch_dev):
+    """Values that are not finite in one head of a long prompt."""
+    torch = torch_dev
+    H, T = 3, 2000
+    pool = fp32_pool(1, H)
+    x = make(torch, 19, T, H)
+    for rule in (DELTA, SUM):
+        ref = run(torch, pool, rule, [0], [T], x)
+        for name, value in (("k", float("nan")), ("v", float("inf")), ("gate", float("nan"))):
+            y = {m: t.clone() for m, t in x.items()}
+            y[name][700, 1] = value
+            o = run(torch, pool, rule, [0], [T], y)
+            assert torch.equal(o[:640], ref[:640]) and torch.equal(o[:, [0, 2]], ref[:, [0, 2]])
+            # (an infinite value times one score is an infinity, summed with others of its column NaN)
+            assert (~o[700:, 1].isfinite()).any(dim=-1).all(), (rule, name)
+            S = states(torch, pool, [0])[0].isfinite()
+            assert not S[1].all() and S[[0, 2]].all()
+    pool.close()
+
+
 @pytest.mark.parametrize("lens,carried", [([1200], True), ([700, 0, 257, 64, 1], False), ([256, 512, 300], True)], ids=str)
 def test_long_additive_prompts(torch_dev, lens, carried):
     """Prompts of several segments, with padding and gates that forget."""
@@ -304,10 +352,12 @@ def test_prompt_errors_on_the_device(torch_dev):
         pool.qdr_prompt(DELTA, i32(torch, [0, 1]), i32(torch, cu), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
         assert pool.qdr_poll_device_error() == qdr.DEVERR_LENGTH, cu
     # and where sequences are cut into segments
-    x = make(torch, 52, 900, H)
-    for cu in ([0, 900, 5, 900], [0, 901, 901, 901], [0, 400, 400, 2 ** 31 - 1], [0, -7, 300, 900], [900, 0, 0, 0], [0, 300, 700, 699]):
+    T = 4000
+    x = make(torch, 52, T, H)
+    for cu in ([0, T, 5, T], [0, T + 1, T + 1, T + 1], [0, 400, 400, 2 ** 31 - 1], [0, -7, 300, T], [T, 0, 0, 0], [0, 300, 700, 699],
+               [0, 2000, 1900, T], [0, 5, T, 3000]):
         for rule in (SUM, DELTA):
-            o = torch.full((900, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+            o = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
             pool.qdr_prompt(rule, i32(torch, [0, -1, 1]), i32(torch, cu), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
             assert pool.qdr_poll_device_error() == qdr.DEVERR_LENGTH, cu
     pool.close()
@@ -361,6 +411,33 @@ def test_prompt_refusals(torch_dev, monkeypatch):
     pool.qdr_prompt(**args(slots=i32(torch, [-1])))       # padding passes the check
     torch.cuda.synchronize()
     assert (o == 0).all()
+
+
+@pytest.mark.parametrize("rule", [DELTA, SUM])
+def test_long_prompts_in_graphs(torch_dev, rule):
+    """A prompt that is cut into segments, captured and replayed between eager
+    work on the same pool: every replay equals the eager call."""
+    torch = torch_dev
+    H, lens = 2, [1900, 700]
+    T = sum(lens)
+    pool, eager = fp32_pool(2, H), fp32_pool(2, H)
+    x, slots, cu, carry = make(torch, 91, T, H), i32(torch, [1, 0]), i32(torch, [0, lens[0], T]), i32(torch, [1, 1])
+    o, g = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda"), torch.cuda.CUDAGraph()
+    ws = torch.empty(pool.qdr_prompt_workspace(2, T), dtype=torch.uint8, device="cuda")
+    for p in (pool, eager):
+        p.qdr_slot_reset(slots)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        pool.qdr_prompt(rule, slots, cu, x["q"], x["k"], x["v"], x["beta"], x["gate"], o, carry=carry, workspace=ws)
+    for turn in range(3):
+        for m, t in make(torch, 92 + turn, T, H).items():
+            x[m].copy_(t)
+        g.replay()
+        ref = run(torch, eager, rule, [1, 0], lens, x, [1, 1])
+        assert torch.equal(o, ref), turn
+        assert torch.equal(states(torch, pool, [0, 1]), states(torch, eager, [0, 1]))
+        o.zero_()
+    del g
 
 
 def test_prompt_without_sequences_or_rows(torch_dev):
