@@ -29,6 +29,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Largest over a column's four lanes (l ^ 16, l ^ 32): a swap of rows of 16, then
+// of halves, gives every lane both sides without a trip through LDS.
+__device__ __forceinline__ float column_max(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = max3(__uint_as_float(a[0]), __uint_as_float(a[1]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max3(__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[1]));
+}
+
 // Eight codes as bfloat16 (exact).
 __device__ __forceinline__ Frag widen(uint32_t a, uint32_t b) {
   Frag f;
@@ -237,8 +246,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
     }
     float top = max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]);
     top = max3(max3(top, s[1][1], s[1][2]), s[1][3], s[1][3]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = column_max(top);
     if (__any(top > m)) {
       const float m1 = fmaxf(m, top);
       const float fade = ex2(m - (m1 == kNone ? 0.0f : m1));
@@ -517,8 +525,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
       top = max3(top, s[c][1][1], s[c][1][2]);
       top1 = max3(top1, s[c][3][1], s[c][3][2]);
       top = max3(max3(top, s[c][1][3], s[c][3][3]), top1, top1);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+      top = column_max(top) * scale;
       if (__any(top > m[c] + kSlack)) {
         const float m1 = fmaxf(m[c], top);
         const float fade = ex2(m[c] - (m1 == kNone ? 0.0f : m1));
