@@ -38,6 +38,12 @@ __device__ __forceinline__ float column_max(float x) {
   return max3(__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[1]));
 }
 
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) x = max3(x, __shfl_xor(x, d), x);
+  return column_max(x);
+}
+
 // Eight codes as bfloat16 (exact).
 __device__ __forceinline__ Frag widen(uint32_t a, uint32_t b) {
   Frag f;
@@ -91,16 +97,26 @@ template <bool FEW>
 __device__ __forceinline__ bool tile_of(const AttendArgs &A, const AttendPlan &plan, int tile, int part, int kvh, Tile &t) {
   const KvArgs &P = A.kv;
   const int per = FEW ? plan.few_tokens : plan.many_tokens;
-  if (FEW && plan.many) {
-    // a call with both launches: this one takes the sequences of one tile
+  if (FEW && tile < P.n) {
+    // a sequence's first tile; in a call with both launches of the sequences
+    // that have no other
     t.b = tile;
-    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len) || t.len == 0 || t.len > per) return false;
+    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len) || t.len == 0 || (plan.many && t.len > per)) return false;
     t.token = 0;
+  } else if (FEW) {
+    // The other tiles, ceil(len / per) - 1 from place cu[b] / per on: behind the
+    // first ones, so that in a call of single tokens no idle workgroup stands
+    // between those that have work (which then miss a compute unit and wait for
+    // a second turn: 64 requests of 8000 tokens, one head 46 us instead of 33).
+    t.b = sequence_of(P.cu, P.n, per, 0, tile - P.n);
+    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len)) return false;
+    t.token = (tile - P.n - t.first / per + 1) * per;
+    if (t.token < per || t.token >= t.len) return false;
   } else {
     t.b = sequence_of(P.cu, P.n, per, 1, tile);
     if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len)) return false;
     t.token = (tile - (t.first / per + t.b)) * per;
-    if (t.token < 0 || t.token >= t.len || (!FEW && plan.few && t.len <= plan.few_tokens)) return false;
+    if (t.token < 0 || t.token >= t.len || (plan.few && t.len <= plan.few_tokens)) return false;
   }
   t.tokens = min(per, t.len - t.token);
   const int heads = FEW ? plan.few_heads : plan.many_heads;
@@ -151,6 +167,11 @@ __device__ __forceinline__ void add_not_finite(const uint8_t *blk, int first_key
 // ---- few rows: up to 16 (one token of up to 16 heads, a few tokens of fewer)
 // Eight waves take every eighth block of 32 keys, each with its own running
 // maximum, straight from memory into operands; they meet in LDS at the end.
+// Bound by memory: 64 requests of 8192 cached tokens (ragged), 8 heads, 8-bit:
+// 155 us for 0.85 GB, 5.5 TB/s.  A block is on its way while another is taken;
+// one request of 777 keys: 9 us, the latency of page, block, and the exchange.
+// Up to sixteen rows it beats the many-row loop at every length (one sequence's
+// 4 new tokens and 777, 8192, 65536 cached: 10.5, 15.5, 48 us against 29, 26, 66).
 template <int KIND>
 struct FewIn {
   u32x4 k[KIND == 8 ? 4 : 8], v[KIND == 8 ? 4 : 8];
@@ -194,12 +215,14 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
   float m = kNone, sum = 0.0f;
   bool finite = true;
 
-  // A block's loads are always there: one behind the last, or of a bad page,
-  // is some block of the cache, and its keys are not looked at.
-  int page = lo < hi ? page_of(P, t.b, min(lo + w, blocks - 1)) : 0;
+  // A block's loads are always there: behind the wave's last it is the last
+  // again (which the caches have), on a bad page some block, and its keys are
+  // not looked at.
+  const int last = max(lo + w + (hi - 1 - lo - w) / kFewWaves * kFewWaves, lo);
+  int page = lo < hi ? page_of(P, t.b, min(lo + w, last)) : 0;
   auto load = [&](int block, FewIn<KIND> &in) {
-    const uint8_t *blk = block_at(P, page, kvh, min(block, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
-    page = page_of(P, t.b, min(block + kFewWaves, blocks - 1));
+    const uint8_t *blk = block_at(P, page, kvh, min(block, last), KIND == 8 ? kKv8Block : kKv16Block);
+    page = page_of(P, t.b, min(block + kFewWaves, last));
     in.good = blk != nullptr;
     if (!blk) blk = P.base;
     constexpr int N = KIND == 8 ? 4 : 8;
@@ -361,6 +384,17 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
 // the scale rides on the subtraction of the maximum, masks are only looked at
 // where a wave's rows end, and the maximum that the weights are taken from
 // moves (and with it the accumulators) only when a score exceeds it by 2^8.
+// The weights are rounded to bfloat16 once here, 2^-8 of each at most, which
+// averages out over the keys (relative error of the result 0.0021, of which
+// its own rounding is 0.0017); a second part would add half the products again.
+// 4 sequences of 1024 new tokens, 8192 cached, 32 query and 8 key heads: 518 us
+// for 357 GFLOP, 690 TFLOP/s.  For 64 keys and 32 rows a wave has 1024 cycles of
+// products and about 1600 of vector instructions, 1000 of them exponentials;
+// the matrix cores are busy 33% of the time and the vector units 39%, seldom
+// together, and the operands take 3/4 of the LDS bandwidth.  Tried and slower:
+// the next block's scores between the current one's exponentials (688 us),
+// 64 rows a wave with one wave a SIMD (the accumulators leave the vector
+// registers; 930 us), wave priorities around the products (596).
 constexpr float kSlack = 8.0f;
 
 template <int KIND>
@@ -429,12 +463,12 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
 
   int page[2] = {0, 0};
   if (lo < hi)
-    for (int y = 0; y < 2; ++y) page[y] = page_of(P, t.b, min(lo + y, blocks - 1));
+    for (int y = 0; y < 2; ++y) page[y] = page_of(P, t.b, min(lo + y, hi - 1));
   auto load = [&](int block, ManyIn<KIND> &in) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const uint8_t *blk = block_at(P, page[y], kvh, min(block + y, blocks - 1), KIND == 8 ? kKv8Block : kKv16Block);
-      page[y] = page_of(P, t.b, min(block + 2 + y, blocks - 1));
+      const uint8_t *blk = block_at(P, page[y], kvh, min(block + y, hi - 1), KIND == 8 ? kKv8Block : kKv16Block);
+      page[y] = page_of(P, t.b, min(block + 2 + y, hi - 1));
       in.left[y] = block + y < hi && blk ? min(t.keys - (block + y) * kBlock, kBlock) : 0;
       if (!blk && block + y < hi && tid == 0) atomicOr(P.err, kErrPage);
       if (!blk) blk = P.base;
@@ -602,7 +636,9 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   }
 }
 
-// Joins the pieces of the keys: one wave a row, two channels a lane.
+// Joins the pieces of the keys (64 at most): one wave a row.  A lane has a
+// piece's maximum and sum; then half a wave takes four channels a lane of every
+// other piece, sixteen pieces on their way at once.
 template <bool FEW>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, AttendPlan plan) {
   constexpr int kRows = FEW ? kFewRows : kManyRows;
@@ -621,20 +657,30 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, AttendPlan pl
   const int live = max((blocks + each - 1) / each, 1);
   const float *from = A.part + (FEW ? 0 : plan.few_floats) + (size_t)unit * splits * (kRows * (kD + 2));
   constexpr size_t kStep = kRows * (kD + 2);
-  float m = kNone;
-  for (int s = 0; s < live; ++s) m = fmaxf(m, from[s * kStep + kRows * kD + r]);
-  const float ref = m == kNone ? 0.0f : m;
-  float sum = 0.0f, a = 0.0f, b = 0.0f;
-  for (int s = 0; s < live; ++s) {
-    const float f = ex2(from[s * kStep + kRows * kD + r] - ref);
-    sum = __builtin_fmaf(from[s * kStep + kRows * kD + kRows + r], f, sum);
-    const f32x2 y = *(const f32x2 *)(from + s * kStep + (size_t)r * kD + 2 * l);
-    a = __builtin_fmaf(y[0], f, a);
-    b = __builtin_fmaf(y[1], f, b);
+  const float *stats = from + min(l, live - 1) * kStep + kRows * kD + r;
+  const float own = stats[0], own_sum = stats[kRows];
+  const float m = wave_max(own);
+  const float f = ex2(own - (m == kNone ? 0.0f : m));
+  float sum = l < live ? own_sum * f : 0.0f;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  const int half = l >> 5;
+  f32x4 o = {0, 0, 0, 0};
+  for (int s0 = 0; s0 < live; s0 += 16) {
+    f32x4 y[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) y[s] = *(const f32x4 *)(from + min(s0 + 2 * s + half, live - 1) * kStep + (size_t)r * kD + 4 * (l & 31));
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float fs = __shfl(f, s0 + 2 * s + half);
+      if (s0 + 2 * s + half < live) o += y[s] * fs;
+    }
   }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) o[x] += __shfl_xor(o[x], 32);
   const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
   const size_t at = ((size_t)(t.first + t.token + tok) * A.q_heads + t.head + hd) * kD;
-  *(uint32_t *)(A.o + at + 2 * l) = pack_bf16(a * inv, b * inv);
+  if (half == 0) *(u32x2_a4 *)(A.o + at + 4 * l) = (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 }  // namespace

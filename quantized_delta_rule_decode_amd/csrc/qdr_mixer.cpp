@@ -165,20 +165,28 @@ AttendPlan plan_attend(int n, int T, int q_heads, int heads, int max_pages, int 
   p.few_tiles = !p.few ? 0 : p.many ? n : T / p.few_tokens + n;
   p.many_tiles = p.many ? T / p.many_tokens + n : 0;
   const int64_t blocks = (int64_t)max_pages << (page_shift - 5);
-  // pieces: enough workgroups for the 256 compute units, a few each
-  auto cut = [&](int64_t units, int least, int target) {
-    int64_t want = units > 0 ? (target + units - 1) / units : 1;
-    const int64_t most = (blocks + least - 1) / least;
-    if (blocks <= kOnePiece) want = 1;
-    if (want > most) want = most;
-    if (want > 64) want = 64;
-    return (int)(want < 1 ? 1 : want);
+  // Pieces: as many as the compute units have places for, which is one few-row
+  // workgroup each or two many-row ones: more of them wait, and pay a start and
+  // partial results for nothing (32 query and 8 key heads, 8192 cached tokens,
+  // 8-bit: 8 requests in 4, 8, 16 pieces 32, 40, 52 us, one of 64 requests uncut
+  // and in 2 193 and 210).  None where that costs more than it gives:
+  //   few rows   up to 32 blocks (1 and 8 requests, bfloat16: 1024 tokens uncut
+  //              10.5 and 11.5 us, cut 10.5 and 13.3; 2048 14.5 and 18.5, 10.7
+  //              and 19.8); above 64 tiles pieces of 64 blocks (16 requests: 3000
+  //              tokens uncut 33, in two 37; 8192, 8-bit, 65 and 53);
+  //   many rows  up to 8 blocks, above 32 tiles up to 24 (20 new tokens: 512
+  //              cached uncut 21.8 us, cut 15.8; three times 100: 512 26.8 and
+  //              36.0, 1024 40.7 and 38.5).
+  auto cut = [&](int64_t units, int64_t least, int places, int64_t uncut) {
+    if (blocks <= uncut) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({places / std::max<int64_t>(units, 1), (blocks + least - 1) / least, 64}));
   };
-  // counted without the places that hold no tile: about T / tokens of them do
+  // tiles, as if the sequences were alike
+  const int64_t each = (T + (int64_t)n - 1) / n;
   const int64_t few_units = (int64_t)(T <= n ? T : n) * heads * p.few_parts;
-  const int64_t many_units = (int64_t)((T + p.many_tokens - 1) / p.many_tokens) * heads * p.many_parts;
-  p.few_splits = p.few ? cut(few_units, kFewLeast, 1024) : 1;
-  p.many_splits = p.many ? cut(many_units, kManyLeast, 512) : 1;
+  const int64_t many_units = n * ((each + p.many_tokens - 1) / p.many_tokens) * heads * p.many_parts;
+  p.few_splits = p.few ? cut(few_units, few_units > 64 ? 64 : kFewLeast, 256, 32) : 1;
+  p.many_splits = p.many ? cut(many_units, kManyLeast, 512, many_units > 32 ? 24 : 8) : 1;
   p.few_floats = p.few_splits > 1 ? (size_t)p.few_tiles * heads * p.few_parts * p.few_splits * kFewRows * (QDR_DIM + 2) : 0;
   p.many_floats = p.many_splits > 1 ? (size_t)p.many_tiles * heads * p.many_parts * p.many_splits * kManyRows * (QDR_DIM + 2) : 0;
   return p;

@@ -9,10 +9,17 @@
 //   O  = diag(2^g) Q S + A U,   A_ts = G_ts q_t.k_s (t >= s)
 //   S' = 2^g_63 S + K^T diag(2^(g_63 - g)) U
 // so all of it is matrix products.  Launches:
+//   k_prompt_slots    pools that hold no plain fp32 heads: which slots to unpack
+//                     before and to pack after;
 //   k_prompt_chunks   DELTA, every chunk at once: T = (I + L)^-1 diag(beta) and
 //                     the decays;  SUM: k_prompt_decays, the decays alone;
-//   k_prompt_segment, k_prompt_join   SUM, long sequences: cut into segments;
+//   k_prompt_segment, k_prompt_join    SUM, long sequences: cut into segments;
 //                     what each adds to a state, then the states they start from;
+//   k_prompt_map, k_prompt_join_maps   the same for DELTA, where a segment's
+//                     effect is a matrix and a sum;
+//   k_prompt_order    DELTA, not cut: the longest sequences first;
+//   k_prompt_chain    DELTA, few heads: the chunks in order, four workgroups a
+//                     head that work on three chunks at once;
 //   k_prompt_scan     the chunks of a sequence (segment) in order.
 // Precision: q, k and v are bfloat16 and enter exactly.  Whatever is computed
 // (S, U, T, A) enters a product as a sum of bfloat16 parts: three parts (24
@@ -108,7 +115,8 @@ __device__ __forceinline__ void inverse_column(const float (*L)[kLd], float (*X)
     for (int r = 0; r < 4; ++r) X[16 * i + 4 * g + r][16 * J + i16] = x[i][r];
 }
 
-// SUM: a wave to a (chunk, head).
+// SUM: a wave to a (chunk, head).  8 B in and 1 KiB out a token row's 64: 10 us
+// for 12288 of them, latency of the scan's six steps in fp64.
 __global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
   const int l = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -122,7 +130,11 @@ __global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
 // DELTA: T and the decays.  One workgroup per (chunk, head); wave w makes
 // rows 16 w .. 16 w + 15 of L, inverts the diagonal block w by substitution,
 // then block column w of the inverse.  Everything fp32 but the exact products
-// of k.
+// of k: the matrix cores' fp32 form for the blocks, whose rounding would be the
+// whole chunk's.  16 KiB in and 13 KiB out: 24576 of them (32768 tokens, 48
+// heads) 210 us, 3.9 TB/s of memory traffic, with the vector units busy 49% of
+// the time.  All rows of k asked for before the first product: one latency, not
+// one a tile (270 us).
 __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) float L[kChunk][kLd], X[kChunk][kLd];
   __shared__ double lg[kChunk];
@@ -425,7 +437,8 @@ __device__ __forceinline__ void solve(const u32x4 (*T)[3][64], const f32x4 *r, f
   }
 }
 
-// One wave, sixteen columns, one chunk.  Products of S, R and U take their
+// One wave, sixteen columns, one chunk: DELTA 186 products of 16 cycles and
+// 1030 vector instructions of 4, most of them the splitting into parts.  Products of S, R and U take their
 // right operands from the accumulators of the product before: nothing but the
 // shared left operands is read from LDS, and nothing waits for another wave.
 // (Products of one accumulator never follow each other: four at a time.)
@@ -548,8 +561,15 @@ struct StateAt {
   }
 };
 
-// The chunks in order, a wave to sixteen columns.  Two workgroups a compute
-// unit: one stages while the other computes.
+// The chunks in order, a wave to sixteen columns.  SUM: two workgroups a compute
+// unit, one stages while the other computes (asking a chunk ahead was no faster,
+// and the registers for it are not there).  DELTA: one, its rows on their way a
+// chunk ahead.  What bounds it is issue: 32 sequences, 16411 tokens, 32 heads
+// (DELTA) 300 us with the vector units busy 43% and the matrix cores 37% of the
+// time, and little of both at once; 8 sequences, 16000 tokens, 48 heads (SUM)
+// 290 us, 38% and 29%.  Tried for DELTA: workgroups of four waves and 64 columns,
+// two a compute unit, stage everything twice (316 against 277 us at 16 heads);
+// waves of 32 columns need more registers than two a SIMD leave.
 template <bool DELTA>
 __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
@@ -606,6 +626,10 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
 //   0, 1       K S, U (sixteen columns each)      U out, the state, S out
 //   2, 3       A U of the chunk before, Q S       A
 //   4 .. 7     the next chunk into LDS            A
+// 32768 tokens, 48 heads: 1570 us, 6000 cycles a chunk, all of them waves 0 and
+// 1: K S 1400, U 1300, U out 550, the state 1850, its parts 700 (a wave
+// alone on its SIMD waits for each of its products' results); k_prompt_scan
+// takes 14000.
 struct ChainShared {
   struct Part {                       // chunk c in part c & 1
     u32x4 Q[4][256], K[4][256], T[kTriFrags][3][64];
@@ -864,6 +888,7 @@ __global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
 }
 
 // SUM: what a segment adds to the state it starts from, and the decay over it.
+// 115 us of the 8 sequences above, bound as the scan is (42% and 34%).
 __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) Stage<false> st;
   const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
@@ -899,7 +924,8 @@ __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
 }
 
 // SUM: the states that the segments start from, a thread to one of its eight
-// results: S_0, then S = decay S + what the segment adds.
+// results: S_0, then S = decay S + what the segment adds.  11 us there, 17 us
+// for one sequence of 33 segments: a memory latency each.
 __global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
   const int m = blockIdx.x % 8, h = blockIdx.x / 8 % P.H, b = blockIdx.x / (8 * P.H);
   const int l = threadIdx.x & 63, per = P.segment * kChunk;
@@ -927,7 +953,9 @@ __global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
 // DELTA: what a segment makes of the state S it starts from is P S + B.  A
 // workgroup computes B (from S = 0; of a sequence's first segment the state
 // that it ends in) or P (from S = 1 and without values), which goes out as the
-// left operands of the join: [result][contraction step][part][lane].
+// left operands of the join: [result][contraction step][part][lane].  5 us a
+// chunk while there is a compute unit for every workgroup (16 chunks, 4 heads:
+// 82 us), 330 us for 32768 tokens and 16 heads; issue, as the scan.
 __device__ __forceinline__ u32x4 *map_ws(const PromptArgs &P, int place, int h) {
   return (u32x4 *)P.map_ws + ((size_t)place * P.H + h) * (kMapFloats / 4);
 }
@@ -1014,7 +1042,8 @@ __global__ void __launch_bounds__(512, 2) k_prompt_map(PromptArgs P) {
 // DELTA: the states that the segments from the second on start from.  A
 // workgroup takes sixteen columns of a (sequence, head); wave w makes results
 // 2 w and 2 w + 1, which are what contraction step w needs of the next state,
-// and has the next segment's operands on their way.
+// and has the next segment's operands on their way.  1.6 us a segment; one wave
+// for all eight results, without operands ahead, took 5.5.
 __global__ void __launch_bounds__(256, 1) k_prompt_join_maps(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) u32x4 sf[2][4][3][64];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
@@ -1130,7 +1159,7 @@ hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
     // Few heads: four workgroups to a chain, a workgroup a compute unit.  4096
     // tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight
-    // sequences of 1024 tokens and 32 heads: 255 us, the scan 168.
+    // sequences of 1024 tokens and 32 heads (256 chains): 255 us, the scan 168.
     if ((int64_t)a.n * a.H <= 128) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
     else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
