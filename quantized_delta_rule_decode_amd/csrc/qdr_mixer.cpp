@@ -78,39 +78,59 @@ struct Cut {
   int64_t places;
 };
 
-// SUM: as many segments as there are places for workgroups (two to each of 256
-// compute units), four chunks at least.  16385 tokens of 16 heads in segments
-// of 4, 8, 16, 32 chunks and uncut: 170, 148, 173, 271, 1396 us.  Where the
-// sequences alone fill the places, only one of twice the mean length is cut:
-// 32 x 1024 tokens of 16 heads cut at the half 273 us, uncut 200, and one long
-// sequence among short ones still does not run alone.
+// SUM: segments of one length for all, as if the sequences were alike: as many
+// as there are places for workgroups, two to each of 256 compute units (16385
+// tokens of 16 heads in segments of 4, 8, 16, 32 chunks and uncut: 165, 139,
+// 159, 263, 1396 us), that divide the mean length (eight sequences of 2000
+// tokens, 48 heads, in 16, 24, 32 chunks: 345, 441, 302 us); of four chunks at
+// least, and long ones of more, since they are joined one by one (32768 tokens
+// of 4 heads in 4, 8, 16: 120, 105, 142 us).  Where the sequences alone fill
+// the places, only one of twice the mean length is cut, which then does not run
+// alone.
 Cut cut_sum(int32_t heads, int32_t n, int32_t T) {
-  const int64_t chunks = T / qdr::kChunk, places = 2 * 256;
-  int64_t want = chunks * heads / places;
-  if ((int64_t)n * heads >= places) want = std::max<int64_t>(want, 2 * (chunks / n));
+  const int64_t pairs = (int64_t)n * heads, places = 2 * 256;
+  const int64_t mean = (T + (int64_t)n * qdr::kChunk - 1) / ((int64_t)n * qdr::kChunk);
   int64_t segment = qdr::kSegmentLeast;
-  while (segment < want) segment *= 2;
+  if (pairs > places) {
+    while (segment < 2 * mean) segment *= 2;
+  } else {
+    const int64_t each = places / pairs;
+    // (a last chunk that is nearly empty counts where it would be a segment by itself)
+    segment = std::max(segment, each == 1 ? mean : (T / ((int64_t)n * qdr::kChunk) + each - 1) / each);
+    while (8 * segment * segment < mean) ++segment;
+  }
   if (segment * qdr::kChunk >= T) return {0, 0};
   return {(int32_t)segment, T / (segment * qdr::kChunk) + n};
 }
 
-// DELTA: a segment's map of states costs twice what its chunks cost, so only
-// calls of few heads are cut, where most compute units would have nothing to
-// do, and only if the longest sequence (a call of several: taken as twice the
-// mean) is worth three launches.  One sequence, chain against segments, us:
-//   4 heads   16 chunks 57 / 67   24 chunks 79 / 72    512 chunks 1434 / 258
-//   16 heads  24 chunks 82 / 80   64 chunks 199 / 135  512 chunks 1612 / 613
-//   32 heads  32 chunks 108 / 125 64 chunks 213 / 201  256 chunks 854 / 595
+// DELTA: a segment's map of states costs twice what its chunks cost, so it is
+// calls of few heads that are cut, where most compute units would have nothing
+// to do.  Whether and where follows from what the launches take, in 0.1 us: a
+// chunk 51 in k_prompt_map and 70 in k_prompt_scan, one workgroup a compute
+// unit at a time, 16 to join a segment, 40 a round of workgroups, 160 for the
+// launches; 32 a chunk in k_prompt_chain.  Of a call of several sequences only
+// the mean length is known: the longest is taken as twice that, and segments
+// have to win by a fifth.  One sequence, chain against segments, us:
+//   4 heads   16 chunks 57 / 67   64 chunks 189 / 91   512 chunks 1434 / 258
+//   16 heads  32 chunks 105 / 88  64 chunks 199 / 135  512 chunks 1612 / 613
+//   32 heads  32 chunks 108 / 125 64 chunks 213 / 192  256 chunks 854 / 595
 //   48 heads  187 chunks 689 / 788   512 chunks 1780 / 1835
-// Their length: one workgroup a compute unit, and not so many that joining
-// them one by one takes longer than their chunks (4 heads, 512 chunks, in
-// segments of 4, 8, 16, 32: 395, 273, 258, 386 us).
 Cut cut_delta(int32_t heads, int32_t n, int32_t T) {
-  const int64_t chunks = T / qdr::kChunk, pairs = (int64_t)n * heads;
-  const int64_t longest = n == 1 ? chunks : 2 * (chunks / n);
-  if (pairs > 32 || longest < std::max<int64_t>(24, 2 * pairs)) return {0, 0};
-  int64_t segment = qdr::kSegmentLeast;
-  while (segment * 256 < chunks * heads || 4 * segment * segment < chunks) segment *= 2;
+  const int64_t pairs = (int64_t)n * heads, chunks = T / qdr::kChunk, mean = (chunks + n - 1) / n;
+  const int64_t longest = n == 1 ? mean : 2 * mean;
+  if (pairs > qdr::kMostChains) return {0, 0};
+  const auto rounds = [](int64_t groups) { return (groups + 255) / 256; };
+  int64_t least = std::max(longest * 32, chunks * heads * 4 * 32 / 256), segment = 0;
+  for (int64_t s = qdr::kSegmentLeast; s <= qdr::kSegmentMost; ++s) {
+    const int64_t each = (mean + s - 1) / s;
+    if (each < 2) break;
+    const int64_t cost = rounds(pairs * (2 * each - 3)) * (51 * s + 40) + rounds(pairs * each) * (70 * s + 40) + (longest + s - 1) / s * 16 + 160;
+    if ((n == 1 ? cost : cost * 5 / 4) < least) {
+      least = n == 1 ? cost : cost * 5 / 4;
+      segment = s;
+    }
+  }
+  if (!segment) return {0, 0};
   return {(int32_t)segment, T / (segment * qdr::kChunk) + n};
 }
 

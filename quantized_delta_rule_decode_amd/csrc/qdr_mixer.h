@@ -21,7 +21,12 @@ constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
 // decays from the chunk's start and to its end (64 fp32 each), and for DELTA
 // one triangular matrix.
 constexpr size_t kDecayFloats = 4 * kChunk, kChunkFloats = kDecayFloats + kTriFloats;
-constexpr int kSegmentLeast = 4;   // chunks of a segment
+constexpr int kSegmentLeast = 4, kSegmentMost = 64;   // chunks of a segment (SUM: no most)
+// Up to so many (sequence, head) pairs DELTA's chunks are taken by
+// k_prompt_chain: four workgroups to a pair, a workgroup a compute unit.  4096
+// tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight
+// sequences of 1024 tokens and 32 heads (256 pairs): 255 us, the scan 168.
+constexpr int kMostChains = 128;
 constexpr size_t kMapFloats = (size_t)8 * 4 * 3 * 64 * 4;   // a 128 x 128 left operand in three parts
 // Sequences of a call that are put in order of length.  n^2 comparisons: 5 us
 // for 32 sequences, which scans of unlike lengths gain back many times (the

@@ -1157,10 +1157,7 @@ hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
       return hipGetLastError();
     }
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
-    // Few heads: four workgroups to a chain, a workgroup a compute unit.  4096
-    // tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight
-    // sequences of 1024 tokens and 32 heads (256 chains): 255 us, the scan 168.
-    if ((int64_t)a.n * a.H <= 128) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
+    if ((int64_t)a.n * a.H <= kMostChains) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
     else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
   }

@@ -165,7 +165,7 @@ def test_prompt_many_heads(torch_dev, rule):
     assert pool.qdr_poll_device_error() == qdr.DEVERR_SLOT
 
 
-@pytest.mark.parametrize("lens,carried,gates", [([1700], True, "one"), ([2500, 0, 1300, 64, 1], False, "mixed"), ([1024, 1100], True, "zeros")], ids=str)
+@pytest.mark.parametrize("lens,carried,gates", [([2000], True, "one"), ([2500, 0, 1500], False, "mixed"), ([1024, 1100], True, "zeros")], ids=str)
 def test_long_delta_prompts(torch_dev, lens, carried, gates):
     """Prompts of several segments, joined by their maps of states."""
     torch = torch_dev
