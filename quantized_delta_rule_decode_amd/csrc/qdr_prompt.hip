@@ -233,8 +233,11 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, Frag *f) {
 
 // What a chunk shares with every column: left operands, 1 KiB each, values
 // and decays.  Rows of q and k lie in pieces of 8 channels; piece c of row i
-// of a tile is at 16 c + (i ^ c): whole rows come in without bank conflicts,
-// and operands and transposing reads go out so.
+// of a tile is at 16 c + (i ^ x(c)), so that what LDS takes in one step lies on
+// sixteen different 16-byte columns of its banks: four rows of four neighbouring
+// pieces (a transposing read), and of 16-byte accesses lanes 0-3, 12-15, 20-23
+// and 24-27, which are rows of two pieces (an operand) or pieces of two rows
+// (coming in).  x(4 P + j) = 4 {0, 3, 1, 2}[j] + {0, 2, 3, 1}[P].
 template <bool DELTA>
 struct Stage {
   u32x4 Q[4][256], K[4][256];                 // [token tile]
@@ -246,7 +249,7 @@ struct Stage {
 };
 static_assert(sizeof(Stage<true>) <= 80 * 1024, "two workgroups share a compute unit's 160 KiB");
 
-__device__ __forceinline__ int piece_at(int piece, int i) { return 16 * piece + (i ^ piece); }
+__device__ __forceinline__ int piece_at(int piece, int i) { return 16 * piece + (i ^ (int)(0x95D1B7F3A6E284C0ull >> (4 * piece) & 15)); }
 // Operand of rows: lane (g, i) has channels 32 s + 8 g .. of row i of a tile.
 __device__ __forceinline__ Frag rows_operand(const u32x4 *tile, int s, int l) {
   Frag f;
