@@ -625,10 +625,10 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
 // follow each other.  A workgroup takes 32 columns of one (sequence, head),
 // and its waves work on three chunks at once.  Between two barriers at a
 // chunk's ends there is one in its middle:
-//   waves      before it                          after it
-//   0, 1       K S, U (sixteen columns each)      U out, the state, S out
-//   2, 3       A U of the chunk before, Q S       A
-//   4 .. 7     the next chunk into LDS            A
+//   waves      before it                            after it
+//   0, 1       U, the state (sixteen columns each)  U out, S out, the next K S
+//   2, 3       A U of the chunk before, Q S         A
+//   4 .. 7     the next chunk into LDS              A
 // 32768 tokens, 48 heads: 1570 us, 6000 cycles a chunk, all of them waves 0 and
 // 1: K S 1400, U 1300, U out 550, the state 1850, its parts 700 (a wave
 // alone on its SIMD waits for each of its products' results); k_prompt_scan
@@ -646,32 +646,37 @@ struct ChainShared {
 };
 static_assert(sizeof(ChainShared) <= 160 * 1024, "one workgroup has a compute unit's LDS");
 
-__device__ __forceinline__ void split_state(const f32x4 *S, Frag (*f)[3], u32x4 (*to)[2][64], int l) {
+// Waves 0, 1: the state's parts for the readout (PUT), and K S of a chunk; one
+// step's parts are made beside the products of the step before.
+template <bool PUT, bool MULTIPLY>
+__device__ __forceinline__ void chain_scores(const f32x4 *S, const u32x4 (*K)[256], u32x4 (*to)[2][64], f32x4 *r, int l) {
+  if (MULTIPLY)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) r[t] = (f32x4){0, 0, 0, 0};
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    split8<3>(S[2 * s], S[2 * s + 1], f[s]);
+    Frag f[3];
+    split8<MULTIPLY ? 3 : 2>(S[2 * s], S[2 * s + 1], f);
+    if (PUT)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) to[s][x][l] = f[s][x].w;
+      for (int x = 0; x < 2; ++x) to[s][x][l] = f[x].w;
+    if (MULTIPLY) {
+      Frag k[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) k[t] = rows_operand(K[t], s, l);
+#pragma unroll
+      for (int x = 2; x >= 0; --x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[x], r[t]);
+    }
   }
 }
 
-// Waves 0, 1.
-__device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &sh, int group, Frag (*f)[3], f32x4 *S) {
+// Waves 0, 1: chunk c, whose K S is in r, then the next one's.
+__device__ __forceinline__ void chain_chunk(int c, bool more, int col, int l, ChainShared &sh, int group, f32x4 *r, f32x4 *S) {
   const int g = l >> 4;
   const ChainShared::Part &p = sh.part[c & 1];
-  f32x4 r[4], u[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) r[t] = (f32x4){0, 0, 0, 0};
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    Frag k[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) k[t] = rows_operand(p.K[t], s, l);
-#pragma unroll
-    for (int x = 2; x >= 0; --x)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) r[t] = mma(k[t], f[s][x], r[t]);
-  }
+  f32x4 u[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const f32x4 from = *(const f32x4 *)&p.dec[16 * t + 4 * g];
@@ -680,6 +685,7 @@ __device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &
       r[t][x] = __builtin_fmaf(-from[x], r[t][x], __uint_as_float((uint32_t)p.V[16 * t + 4 * g + x][col] << 16));
   }
   solve(p.T, r, u, l);
+  update_state<false>(p.K, p.dec, u, S, l);
   lds_barrier();
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -688,8 +694,7 @@ __device__ __forceinline__ void chain_chunk(int c, int col, int l, ChainShared &
 #pragma unroll
     for (int x = 0; x < 2; ++x) sh.U[group][s][x][l] = U[x].w;
   }
-  update_state<false>(p.K, p.dec, u, S, l);
-  split_state(S, f, sh.S[group], l);
+  if (more) chain_scores<true, true>(S, sh.part[(c + 1) & 1].K, sh.S[group], r, l);
 }
 
 // Waves 4 .. 7: a thread's share of a chunk on its way in.
@@ -877,11 +882,12 @@ __global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
 #pragma unroll
   for (int m = 0; m < 8; ++m) S[m] = carried ? state.get(state_row(m, g), col) : (f32x4){0, 0, 0, 0};
   if (chunks > 0) {
-    Frag f[4][3];
-    split_state(S, f, sh.S[group], l);
+    f32x4 r[4];
+    chain_scores<true, false>(S, nullptr, sh.S[group], r, l);
     lds_barrier();
+    chain_scores<false, true>(S, sh.part[0].K, nullptr, r, l);
     for (int c = 0; c < chunks; ++c) {
-      chain_chunk(c, 16 * group + (l & 15), l, sh, group, f, S);
+      chain_chunk(c, c + 1 < chunks, 16 * group + (l & 15), l, sh, group, r, S);
       lds_barrier();
     }
   }
