@@ -642,7 +642,7 @@ struct ChainShared {
   } part[2];
   u32x4 A[kTriFrags][2][64];
   u32x4 S[2][4][2][64];               // [columns][contraction step][part]: the state before the chunk
-  u32x4 U[2][2][2][64];
+  f32x4 U[2][4][64];
 };
 static_assert(sizeof(ChainShared) <= 160 * 1024, "one workgroup has a compute unit's LDS");
 
@@ -688,12 +688,7 @@ __device__ __forceinline__ void chain_chunk(int c, bool more, int col, int l, Ch
   update_state<false>(p.K, p.dec, u, S, l);
   lds_barrier();
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    Frag U[2];
-    split8<2>(u[2 * s], u[2 * s + 1], U);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) sh.U[group][s][x][l] = U[x].w;
-  }
+  for (int t = 0; t < 4; ++t) sh.U[group][t][l] = u[t];
   if (more) chain_scores<true, true>(S, sh.part[(c + 1) & 1].K, sh.S[group], r, l);
 }
 
@@ -792,8 +787,7 @@ __device__ __forceinline__ void read_chunk(const PromptArgs &P, const ScanAt &A,
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     Frag U[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) U[x].w = sh.U[group][s][x][l];
+    split8<2>(sh.U[group][2 * s][l], sh.U[group][2 * s + 1][l], U);
 #pragma unroll
     for (int x = 1; x >= 0; --x)
 #pragma unroll
