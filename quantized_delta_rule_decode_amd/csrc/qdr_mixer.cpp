@@ -108,7 +108,7 @@ Cut cut_sum(int32_t heads, int32_t n, int32_t T) {
 // to do.  Whether and where follows from what the launches take, in 0.1 us: a
 // chunk 51 in k_prompt_map and 70 in k_prompt_scan, one workgroup a compute
 // unit at a time, 16 to join a segment, 40 a round of workgroups, 160 for the
-// launches; 32 a chunk in k_prompt_chain.  Of a call of several sequences only
+// launches; 27 a chunk in k_prompt_chain.  Of a call of several sequences only
 // the mean length is known: the longest is taken as twice that, and segments
 // have to win by a fifth.  One sequence, chain against segments, us:
 //   4 heads   16 chunks 57 / 67   64 chunks 189 / 91   512 chunks 1434 / 258
@@ -118,9 +118,9 @@ Cut cut_sum(int32_t heads, int32_t n, int32_t T) {
 Cut cut_delta(int32_t heads, int32_t n, int32_t T) {
   const int64_t pairs = (int64_t)n * heads, chunks = T / qdr::kChunk, mean = (chunks + n - 1) / n;
   const int64_t longest = n == 1 ? mean : 2 * mean;
-  if (pairs > qdr::kMostChains) return {0, 0};
+  if (!qdr::in_chains(n, heads)) return {0, 0};
   const auto rounds = [](int64_t groups) { return (groups + 255) / 256; };
-  int64_t least = std::max(longest * 32, chunks * heads * 4 * 32 / 256), segment = 0;
+  int64_t least = std::max(longest * 27, chunks * heads * 4 * 27 / 256), segment = 0;
   for (int64_t s = qdr::kSegmentLeast; s <= qdr::kSegmentMost; ++s) {
     const int64_t each = (mean + s - 1) / s;
     if (each < 2) break;

@@ -22,11 +22,13 @@ constexpr size_t kTriFloats = (size_t)kTriFrags * 512;
 // one triangular matrix.
 constexpr size_t kDecayFloats = 4 * kChunk, kChunkFloats = kDecayFloats + kTriFloats;
 constexpr int kSegmentLeast = 4, kSegmentMost = 64;   // chunks of a segment (SUM: no most)
-// Up to so many (sequence, head) pairs DELTA's chunks are taken by
-// k_prompt_chain: four workgroups to a pair, a workgroup a compute unit.  4096
-// tokens of 96 and 128 heads: 456 and 476 us, the scan 481 and 497; eight
-// sequences of 1024 tokens and 32 heads (256 pairs): 255 us, the scan 168.
-constexpr int kMostChains = 128;
+// Whether DELTA's chunks are taken by k_prompt_chain: four workgroups to a
+// (sequence, head), a workgroup a compute unit, so few pairs.  4096 tokens of
+// 128 and 160 heads 422 and 575 us, by k_prompt_scan 487 and 507.  Of several
+// sequences the longest counts more than all together, and the chain is faster
+// at one: 8192 tokens of 32 heads in six sequences of unlike lengths 232 us, the
+// scan 399, of equal ones 224 and 190; in eight 240 and 230, 222 and 157.
+inline bool in_chains(int64_t n, int64_t heads) { return n * heads <= (n == 1 ? 128 : 192); }
 constexpr size_t kMapFloats = (size_t)8 * 4 * 3 * 64 * 4;   // a 128 x 128 left operand in three parts
 // Sequences of a call that are put in order of length.  n^2 comparisons: 5 us
 // for 32 sequences, which scans of unlike lengths gain back many times (the

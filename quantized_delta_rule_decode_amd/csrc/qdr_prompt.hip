@@ -629,10 +629,11 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
 //   0, 1       U, the state (sixteen columns each)  U out, S out, the next K S
 //   2, 3       A U of the chunk before, Q S         A
 //   4 .. 7     the next chunk into LDS              A
-// 32768 tokens, 48 heads: 1570 us, 6000 cycles a chunk, all of them waves 0 and
-// 1: K S 1400, U 1300, U out 550, the state 1850, its parts 700 (a wave
-// alone on its SIMD waits for each of its products' results); k_prompt_scan
-// takes 14000.
+// 32768 tokens, 48 heads: 1300 us, 5000 cycles a chunk, all of them waves 0 and
+// 1: U 1300, the state 1850, its parts and the next K S 1500 (132 products of 16
+// cycles and 430 vector instructions of 4); k_prompt_scan takes 14000.  With K S
+// after the barrier 6000, with U split here 5100.  A raised priority of the two
+// waves changes nothing.
 struct ChainShared {
   struct Part {                       // chunk c in part c & 1
     u32x4 Q[4][256], K[4][256], T[kTriFrags][3][64];
@@ -1160,7 +1161,7 @@ hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
       return hipGetLastError();
     }
     if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
-    if ((int64_t)a.n * a.H <= kMostChains) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
+    if (in_chains(a.n, a.H)) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
     else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
   }

@@ -138,7 +138,7 @@ static int prompts() {
 
   // which calls are cut into segments, and that their parts fit the workspace
   struct { int rule, heads, n, T, segment; } cuts[] = {
-      {QDR_RULE_DELTA, 2, 1, 1500, 0},   {QDR_RULE_DELTA, 2, 1, 2000, 4},  {QDR_RULE_DELTA, 4, 1, 32768, 8}, {QDR_RULE_DELTA, 32, 1, 32768, 64},
+      {QDR_RULE_DELTA, 2, 1, 1500, 0},   {QDR_RULE_DELTA, 2, 1, 2200, 4},  {QDR_RULE_DELTA, 4, 1, 32768, 8}, {QDR_RULE_DELTA, 32, 1, 32768, 64},
       {QDR_RULE_DELTA, 48, 1, 32768, 0}, {QDR_RULE_DELTA, 32, 1, 2048, 0}, {QDR_RULE_DELTA, 2, 3, 4000, 4},  {QDR_RULE_DELTA, 2, 5, 3000, 0},
       {QDR_RULE_SUM, 2, 1, 256, 0},      {QDR_RULE_SUM, 2, 1, 257, 4},     {QDR_RULE_SUM, 16, 1, 16385, 8},  {QDR_RULE_SUM, 17, 32, 32768, 32}};
   for (const auto &c : cuts) {

@@ -165,7 +165,7 @@ def test_prompt_many_heads(torch_dev, rule):
     assert pool.qdr_poll_device_error() == qdr.DEVERR_SLOT
 
 
-@pytest.mark.parametrize("lens,carried,gates", [([2000], True, "one"), ([2500, 0, 1500], False, "mixed"), ([1024, 1100], True, "zeros")], ids=str)
+@pytest.mark.parametrize("lens,carried,gates", [([2200], True, "one"), ([2500, 0, 1500], False, "mixed"), ([1344, 1656], True, "zeros")], ids=str)
 def test_long_delta_prompts(torch_dev, lens, carried, gates):
     """Prompts of several segments, joined by their maps of states."""
     torch = torch_dev
@@ -196,7 +196,7 @@ def test_long_delta_prompts(torch_dev, lens, carried, gates):
 def test_prompt_non_finite_in_segments(torch_dev):
     """Values that are not finite in one head of a long prompt."""
     torch = torch_dev
-    H, T = 3, 2000
+    H, T = 3, 2300
     pool = fp32_pool(1, H)
     x = make(torch, 19, T, H)
     for rule in (DELTA, SUM):
@@ -418,7 +418,7 @@ def test_long_prompts_in_graphs(torch_dev, rule):
     """A prompt that is cut into segments, captured and replayed between eager
     work on the same pool: every replay equals the eager call."""
     torch = torch_dev
-    H, lens = 2, [1900, 700]
+    H, lens = 2, [2100, 900]
     T = sum(lens)
     pool, eager = fp32_pool(2, H), fp32_pool(2, H)
     x, slots, cu, carry = make(torch, 91, T, H), i32(torch, [1, 0]), i32(torch, [0, lens[0], T]), i32(torch, [1, 1])
