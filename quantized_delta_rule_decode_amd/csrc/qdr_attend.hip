@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
   // A block's loads are always there: behind the wave's last it is the last
   // again (which the caches have), on a bad page some block, and its keys are
   // not looked at.
-  const int last = max(lo + w + (hi - 1 - lo - w) / kFewWaves * kFewWaves, lo);
+  const int last = lo + w < hi ? lo + w + (hi - 1 - lo - w) / kFewWaves * kFewWaves : hi - 1;
   int page = lo < hi ? page_of(P, t.b, min(lo + w, last)) : 0;
   auto load = [&](int block, FewIn<KIND> &in) {
     const uint8_t *blk = block_at(P, page, kvh, min(block, last), KIND == 8 ? kKv8Block : kKv16Block);
