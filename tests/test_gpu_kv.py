@@ -222,7 +222,7 @@ ATTEND = [
     ([5], [90], 32, 200, 1),
     # no more rows than sequences, and yet one of several tiles
     ([0] * 9 + [7] + [0] * 5 + [1], [5] * 9 + [40] + [8] * 5 + [2100], 32, 16, 2),
-    ([1, 0, 6, 0, 0, 3, 0, 0, 0, 0], [3000, 0, 2500, 1, 0, 3, 0, 70, 0, 0], 64, 16, 1),
+    ([1, 0, 6, 0, 0, 3, 0, 0, 0, 0], [3000, 4, 2500, 1, 2, 3, 9, 70, 1, 33], 64, 16, 1),
 ]
 
 
