@@ -59,16 +59,33 @@ __device__ __forceinline__ ChunkSpace chunk_space(const PromptArgs &P, int place
   return {(double *)ws, ws + 2 * kChunk, ws + kDecayFloats};
 }
 
-// One wave: the decays of a chunk, a token to a lane.
+// x plus the value that DPP control CTRL brings to the rows of MASK.
+template <int CTRL, int MASK>
+__device__ __forceinline__ double add_from(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)b, CTRL, MASK, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(b >> 32), CTRL, MASK, 0xF, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum of x over a wave's lanes up to each.
+__device__ __forceinline__ double sum_up(double x) {
+  x = add_from<0x111, 0xF>(x);   // from 1, 2, 4, 8 lanes below in the row of 16
+  x = add_from<0x112, 0xF>(x);
+  x = add_from<0x114, 0xF>(x);
+  x = add_from<0x118, 0xF>(x);
+  x = add_from<0x142, 0xA>(x);   // lane 15 of the row below, then lane 31
+  return add_from<0x143, 0xC>(x);
+}
+
+// One wave: the decays of a chunk, a token to a lane.  A logarithm is rounded to
+// fp32, which moves a decay 2^-g by a factor 1 + g 2^-24, less than rounding it;
+// their sums are not rounded (fp64).
 __device__ __forceinline__ double put_decays(const PromptArgs &P, size_t t0, int nt, int h, int l, const ChunkSpace &ws) {
   const float a = l < nt ? P.gate[(t0 + l) * P.H + h] : 1.0f;
-  double x = a == 0.0f ? kLogZero : log2((double)a);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(x, d);
-    if (l >= d) x += y;
-  }
-  const double end = __shfl(x, 63);
+  const double x = sum_up(a == 0.0f ? kLogZero : (double)log2f(a));
+  const uint64_t last = __builtin_bit_cast(uint64_t, x);
+  const double end = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 63) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 63));
   ws.lg[l] = x;
   ws.dec[l] = exp2f((float)x);
   ws.dec[kChunk + l] = exp2f((float)(end - x));
