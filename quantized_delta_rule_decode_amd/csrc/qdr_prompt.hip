@@ -132,8 +132,8 @@ __device__ __forceinline__ void inverse_column(const float (*L)[kLd], float (*X)
     for (int r = 0; r < 4; ++r) X[16 * i + 4 * g + r][16 * J + i16] = x[i][r];
 }
 
-// SUM: a wave to a (chunk, head).  8 B in and 1 KiB out a token row's 64: 10 us
-// for 12288 of them, latency of the scan's six steps in fp64.
+// SUM: a wave to a (chunk, head): 256 B in, 1 KiB out.  9 us for 12288 of them,
+// 2 TB/s; the vector units half busy with logarithms and exponentials.
 __global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
   const int l = threadIdx.x & 63;
   const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
 // then block column w of the inverse.  Everything fp32 but the exact products
 // of k: the matrix cores' fp32 form for the blocks, whose rounding would be the
 // whole chunk's.  16 KiB in and 13 KiB out: 24576 of them (32768 tokens, 48
-// heads) 210 us, 3.9 TB/s of memory traffic, with the vector units busy 49% of
+// heads) 200 us, 4.1 TB/s of memory traffic, with the vector units busy 49% of
 // the time.  All rows of k asked for before the first product: one latency, not
 // one a tile (270 us).
 __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
@@ -585,11 +585,11 @@ struct StateAt {
 // unit, one stages while the other computes (asking a chunk ahead was no faster,
 // and the registers for it are not there).  DELTA: one, its rows on their way a
 // chunk ahead.  What bounds it is issue: 32 sequences, 16411 tokens, 32 heads
-// (DELTA) 300 us with the vector units busy 43% and the matrix cores 37% of the
+// (DELTA) 286 us with the vector units busy 45% and the matrix cores 39% of the
 // time, and little of both at once; 8 sequences, 16000 tokens, 48 heads (SUM)
-// 290 us, 38% and 29%.  Tried for DELTA: workgroups of four waves and 64 columns,
-// two a compute unit, stage everything twice (316 against 277 us at 16 heads);
-// waves of 32 columns need more registers than two a SIMD leave.
+// 282 us, 39% and 29%.  Tried for DELTA: workgroups of four waves and 64 columns,
+// two a compute unit, stage everything twice (316 against 277 us, 16 heads in
+// segments); waves of 32 columns need more registers than two a SIMD leave.
 template <bool DELTA>
 __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) Stage<DELTA> st;
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
 //   0, 1       U, the state (sixteen columns each)  U out, S out, the next K S
 //   2, 3       A U of the chunk before, Q S         A
 //   4 .. 7     the next chunk into LDS              A
-// 32768 tokens, 48 heads: 1300 us, 5000 cycles a chunk, all of them waves 0 and
+// 32768 tokens, 48 heads: 1260 us, 5000 cycles a chunk, all of them waves 0 and
 // 1: U 1300, the state 1850, its parts and the next K S 1500 (132 products of 16
 // cycles and 430 vector instructions of 4); k_prompt_scan takes 14000.  With K S
 // after the barrier 6000, with U split here 5100.  A raised priority of the two
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(512, 2) k_prompt_chain(PromptArgs P) {
 }
 
 // SUM: what a segment adds to the state it starts from, and the decay over it.
-// 115 us of the 8 sequences above, bound as the scan is (42% and 34%).
+// 105 us of the 8 sequences above, bound as the scan is (44% and 36%).
 __global__ void __launch_bounds__(512, 4) k_prompt_segment(PromptArgs P) {
   __shared__ __attribute__((aligned(16))) Stage<false> st;
   const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
@@ -975,8 +975,8 @@ __global__ void __launch_bounds__(512) k_prompt_join(PromptArgs P) {
 // workgroup computes B (from S = 0; of a sequence's first segment the state
 // that it ends in) or P (from S = 1 and without values), which goes out as the
 // left operands of the join: [result][contraction step][part][lane].  5 us a
-// chunk while there is a compute unit for every workgroup (16 chunks, 4 heads:
-// 82 us), 330 us for 32768 tokens and 16 heads; issue, as the scan.
+// chunk while there is a compute unit for every workgroup (4 heads in segments
+// of 16 chunks: 82 us), 310 us for 32768 tokens and 16 heads; issue, as the scan.
 __device__ __forceinline__ u32x4 *map_ws(const PromptArgs &P, int place, int h) {
   return (u32x4 *)P.map_ws + ((size_t)place * P.H + h) * (kMapFloats / 4);
 }
