@@ -220,6 +220,8 @@ ATTEND = [
     ([129], [129], 256, 34, 2),
     ([1, 300, 1, 40], [900, 700, 31, 40], 64, 8, 2),
     ([5], [90], 32, 200, 1),
+    # single tokens among long chunks
+    ([1, 700, 2, 600], [900, 700, 31, 900], 64, 8, 2),
     # no more rows than sequences, and yet one of several tiles
     ([0] * 9 + [7] + [0] * 5 + [1], [5] * 9 + [40] + [8] * 5 + [2100], 32, 16, 2),
     ([1, 0, 6, 0, 0, 3, 0, 0, 0, 0], [3000, 4, 2500, 1, 2, 3, 9, 70, 1, 33], 64, 16, 1),
