@@ -636,51 +636,71 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   }
 }
 
-// Joins the pieces of the keys (64 at most): one wave a row.  A lane has a
-// piece's maximum and sum; then half a wave takes four channels a lane of every
-// other piece, sixteen pieces on their way at once.
-template <bool FEW>
+// Joins the pieces of the keys (64 at most): a wave takes OWN rows.  A lane has
+// a piece's maximum and sum of each row; then half a wave takes four channels a
+// lane of every other piece, sixteen loads on their way at once.  Eight rows a
+// wave where there are few pieces of many rows, so that it finds its tile once
+// (4 x 256 new tokens in two pieces 16 us, with one row 23; two of 961 in five
+// 11.8 and 10.7, 20 in 64 26 and 8).
+template <bool FEW, int OWN>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, AttendPlan plan) {
-  constexpr int kRows = FEW ? kFewRows : kManyRows;
+  constexpr int kRows = FEW ? kFewRows : kManyRows, kOwn = OWN, kLoads = OWN == 1 ? 8 : 2;
   const KvArgs &P = A.kv;
   const int parts = FEW ? plan.few_parts : plan.many_parts, splits = FEW ? plan.few_splits : plan.many_splits;
-  const int l = threadIdx.x & 63;
+  const int l = threadIdx.x & 63, half = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = (blockIdx.x % (kRows / 4)) * 4 + w, unit = blockIdx.x / (kRows / 4);
+  constexpr int kGroups = kRows / (4 * kOwn);
+  const int r0 = ((blockIdx.x % kGroups) * 4 + w) * kOwn, unit = blockIdx.x / kGroups;
   const int part = unit % parts, kvh = unit / parts % P.heads, tile = unit / (parts * P.heads);
   Tile t;
-  if (!tile_of<FEW>(A, plan, tile, part, kvh, t)) return;
-  const int tok = r / t.heads, hd = r % t.heads;
-  if (tok >= t.tokens) return;
+  if (!tile_of<FEW>(A, plan, tile, part, kvh, t) || r0 / t.heads >= t.tokens) return;
   const int blocks = (t.keys + kBlock - 1) / kBlock;
   const int each = piece_blocks(blocks, splits, FEW ? kFewLeast : kManyLeast);
   const int live = max((blocks + each - 1) / each, 1);
-  const float *from = A.part + (FEW ? 0 : plan.few_floats) + (size_t)unit * splits * (kRows * (kD + 2));
   constexpr size_t kStep = kRows * (kD + 2);
-  const float *stats = from + min(l, live - 1) * kStep + kRows * kD + r;
-  const float own = stats[0], own_sum = stats[kRows];
-  const float m = wave_max(own);
-  const float f = ex2(own - (m == kNone ? 0.0f : m));
-  float sum = l < live ? own_sum * f : 0.0f;
+  const float *from = A.part + (FEW ? 0 : plan.few_floats) + (size_t)unit * splits * kStep;
+  const float *stats = from + min(l, live - 1) * kStep + kRows * kD + r0;
+  float f[kOwn], sum[kOwn], own[kOwn];
+  f32x4 o[kOwn];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  const int half = l >> 5;
-  f32x4 o = {0, 0, 0, 0};
-  for (int s0 = 0; s0 < live; s0 += 16) {
-    f32x4 y[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) y[s] = *(const f32x4 *)(from + min(s0 + 2 * s + half, live - 1) * kStep + (size_t)r * kD + 4 * (l & 31));
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const float fs = __shfl(f, s0 + 2 * s + half);
-      if (s0 + 2 * s + half < live) o += y[s] * fs;
-    }
+  for (int x = 0; x < kOwn; ++x) {
+    own[x] = stats[x];
+    sum[x] = stats[kRows + x];
   }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) o[x] += __shfl_xor(o[x], 32);
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  const size_t at = ((size_t)(t.first + t.token + tok) * A.q_heads + t.head + hd) * kD;
-  if (half == 0) *(u32x2_a4 *)(A.o + at + 4 * l) = (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+  for (int x = 0; x < kOwn; ++x) {
+    const float m = wave_max(own[x]);
+    f[x] = ex2(own[x] - (m == kNone ? 0.0f : m));
+    sum[x] = l < live ? sum[x] * f[x] : 0.0f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum[x] += __shfl_xor(sum[x], d);
+    o[x] = (f32x4){0, 0, 0, 0};
+  }
+  for (int s0 = 0; s0 < live; s0 += 2 * kLoads) {
+    f32x4 y[kOwn][kLoads];
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x)
+#pragma unroll
+      for (int s = 0; s < kLoads; ++s)
+        y[x][s] = *(const f32x4 *)(from + min(s0 + 2 * s + half, live - 1) * kStep + (size_t)(r0 + x) * kD + 4 * (l & 31));
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x)
+#pragma unroll
+      for (int s = 0; s < kLoads; ++s) {
+        const float fs = __shfl(f[x], s0 + 2 * s + half);
+        if (s0 + 2 * s + half < live) o[x] += y[x][s] * fs;
+      }
+  }
+#pragma unroll
+  for (int x = 0; x < kOwn; ++x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[x][i] += __shfl_xor(o[x][i], 32);
+    const int tok = (r0 + x) / t.heads, hd = (r0 + x) % t.heads;
+    if (tok >= t.tokens || half) continue;
+    const float inv = sum[x] > 0.0f || sum[x] != sum[x] ? 1.0f / sum[x] : 0.0f;
+    const size_t at = ((size_t)(t.first + t.token + tok) * A.q_heads + t.head + hd) * kD;
+    *(u32x2_a4 *)(A.o + at + 4 * l) = (u32x2){pack_bf16(o[x][0] * inv, o[x][1] * inv), pack_bf16(o[x][2] * inv, o[x][3] * inv)};
+  }
 }
 
 }  // namespace
@@ -690,12 +710,13 @@ static hipError_t attend(const AttendArgs &a, const AttendPlan &p, hipStream_t s
   if (p.few) {
     const uint32_t units = (uint32_t)p.few_tiles * a.kv.heads * p.few_parts;
     hipLaunchKernelGGL(k_attend_few<KIND>, dim3(units * p.few_splits), dim3(64 * kFewWaves), 0, st, a, p);
-    if (p.few_splits > 1) hipLaunchKernelGGL(k_attend_join<true>, dim3(units * (kFewRows / 4)), dim3(256), 0, st, a, p);
+    if (p.few_splits > 1) hipLaunchKernelGGL((k_attend_join<true, 1>), dim3(units * (kFewRows / 4)), dim3(256), 0, st, a, p);
   }
   if (p.many) {
     const uint32_t units = (uint32_t)p.many_tiles * a.kv.heads * p.many_parts;
     hipLaunchKernelGGL(k_attend_many<KIND>, dim3(units * p.many_splits), dim3(256), 0, st, a, p);
-    if (p.many_splits > 1) hipLaunchKernelGGL(k_attend_join<false>, dim3(units * (kManyRows / 4)), dim3(256), 0, st, a, p);
+    if (p.many_splits > 4) hipLaunchKernelGGL((k_attend_join<false, 1>), dim3(units * (kManyRows / 4)), dim3(256), 0, st, a, p);
+    else if (p.many_splits > 1) hipLaunchKernelGGL((k_attend_join<false, 8>), dim3(units * (kManyRows / 32)), dim3(256), 0, st, a, p);
   }
   return hipGetLastError();
 }
