@@ -160,7 +160,7 @@ PromptSpace prompt_space(const qdr::PoolView &v, int32_t n, int32_t T) {
 
 // Whether a prompt's launches can be counted.
 qdr_status check_prompt(const qdr::PoolView &v, const PromptSpace &s, int32_t n) {
-  QDR_TRY(check_groups(s.places * v.num_heads));
+  QDR_TRY(check_groups(s.places * v.num_heads + qdr::kMostOrdered / 256));
   // of 512 threads: segments, and to join them eight a head
   return check_groups((n + std::max(s.sum.places, s.delta.places)) * v.num_heads * 16);
 }
@@ -352,7 +352,7 @@ qdr_status qdr_prompt(qdr_pool *pool, int32_t rule, const int32_t *slots, const 
     a.segments = (int32_t)cut.places;
     a.segment_ws = reinterpret_cast<float *>(ws + space.chunks + space.tables + space.states);
     a.map_ws = a.segment_ws + (size_t)cut.places * view.num_heads * QDR_DIM * QDR_DIM;
-  } else if (delta && space.ordered) {
+  } else if (delta && space.ordered && T > 0) {   // (without rows there is no launch that orders)
     a.order = table;
   }
   hipError_t e = qdr::pool_after_writeback(pool, st);

@@ -30,10 +30,10 @@ constexpr int kSegmentLeast = 4, kSegmentMost = 64;   // chunks of a segment (SU
 // scan 399, of equal ones 224 and 190; in eight 240 and 230, 222 and 157.
 inline bool in_chains(int64_t n, int64_t heads) { return n * heads <= (n == 1 ? 128 : 192); }
 constexpr size_t kMapFloats = (size_t)8 * 4 * 3 * 64 * 4;   // a 128 x 128 left operand in three parts
-// Sequences of a call that are put in order of length.  n^2 comparisons: 5 us
-// for 32 sequences, which scans of unlike lengths gain back many times (the
-// longest, started last, would run alone); where there are thousands of
-// sequences one of them is a small share of the whole.
+// Sequences of a call that are put in order of length, which scans of unlike
+// lengths gain from (the longest, started last, would run alone).  n^2
+// comparisons beside the chunks' kernel; where there are thousands of sequences
+// one of them is a small share of the whole.
 constexpr int kMostOrdered = 1024;
 
 struct PromptArgs {

@@ -12,12 +12,12 @@
 //   k_prompt_slots    pools that hold no plain fp32 heads: which slots to unpack
 //                     before and to pack after;
 //   k_prompt_chunks   DELTA, every chunk at once: T = (I + L)^-1 diag(beta) and
-//                     the decays;  SUM: k_prompt_decays, the decays alone;
+//                     the decays, and which sequences are longest;
+//   k_prompt_decays   SUM: the decays alone;
 //   k_prompt_segment, k_prompt_join    SUM, long sequences: cut into segments;
 //                     what each adds to a state, then the states they start from;
 //   k_prompt_map, k_prompt_join_maps   the same for DELTA, where a segment's
 //                     effect is a matrix and a sum;
-//   k_prompt_order    DELTA, not cut: the longest sequences first;
 //   k_prompt_chain    DELTA, few heads: the chunks in order, four workgroups a
 //                     head that work on three chunks at once;
 //   k_prompt_scan     the chunks of a sequence (segment) in order.
@@ -144,7 +144,19 @@ __global__ void __launch_bounds__(256) k_prompt_decays(PromptArgs P) {
   put_decays(P, t0, nt, h, l, chunk_space(P, place, h));
 }
 
-// DELTA: T and the decays.  One workgroup per (chunk, head); wave w makes
+// Sequences by falling length, so that the longest ones start first: the place
+// of sequence b.
+__device__ __forceinline__ void put_order(const PromptArgs &P, int b) {
+  if (b >= P.n) return;
+  auto length = [&](int i) { return (long long)P.cu[i + 1] - P.cu[i]; };
+  const long long mine = length(b);
+  int rank = 0;
+  for (int i = 0; i < P.n; ++i) rank += length(i) > mine || (length(i) == mine && i < b);
+  P.order[rank] = b;
+}
+
+// DELTA: T and the decays.  One workgroup per (chunk, head), and before them
+// those that order the sequences; wave w makes
 // rows 16 w .. 16 w + 15 of L, inverts the diagonal block w by substitution,
 // then block column w of the inverse.  Everything fp32 but the exact products
 // of k: the matrix cores' fp32 form for the blocks, whose rounding would be the
@@ -157,7 +169,12 @@ __global__ void __launch_bounds__(256) k_prompt_chunks(PromptArgs P) {
   __shared__ double lg[kChunk];
   __shared__ __attribute__((aligned(16))) float bt[kChunk];
 
-  const int place = blockIdx.x / P.H, h = blockIdx.x % P.H;
+  const int orders = P.order ? (P.n + 255) / 256 : 0;
+  if ((int)blockIdx.x < orders) {
+    put_order(P, blockIdx.x * 256 + threadIdx.x);
+    return;
+  }
+  const int place = (blockIdx.x - orders) / P.H, h = (blockIdx.x - orders) % P.H;
   size_t t0;
   int nt;
   if (!chunk_at(P, place, &t0, &nt)) return;
@@ -1132,17 +1149,6 @@ __global__ void __launch_bounds__(256, 1) k_prompt_join_maps(PromptArgs P) {
   }
 }
 
-// Sequences by falling length: the longest ones start first.
-__global__ void __launch_bounds__(256) k_prompt_order(PromptArgs P) {
-  const int b = blockIdx.x * 256 + threadIdx.x;
-  if (b >= P.n) return;
-  auto length = [&](int i) { return (long long)P.cu[i + 1] - P.cu[i]; };
-  const long long mine = length(b);
-  int rank = 0;
-  for (int i = 0; i < P.n; ++i) rank += length(i) > mine || (length(i) == mine && i < b);
-  P.order[rank] = b;
-}
-
 // Slots whose states are unpacked before and packed after the scan.
 __global__ void __launch_bounds__(256) k_prompt_slots(PromptArgs P) {
   const int b = blockIdx.x * 256 + threadIdx.x;
@@ -1164,7 +1170,7 @@ hipError_t launch_prompt_slots(const PromptArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_prompt_chunks(const PromptArgs &a, bool delta, hipStream_t st) {
-  if (delta) hipLaunchKernelGGL(k_prompt_chunks, dim3(a.chunks * a.H), dim3(256), 0, st, a);
+  if (delta) hipLaunchKernelGGL(k_prompt_chunks, dim3(a.chunks * a.H + (a.order ? (a.n + 255) / 256 : 0)), dim3(256), 0, st, a);
   else hipLaunchKernelGGL(k_prompt_decays, dim3((uint32_t)(((int64_t)a.chunks * a.H + 3) / 4)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
@@ -1177,7 +1183,6 @@ hipError_t launch_prompt_scan(const PromptArgs &a, bool delta, hipStream_t st) {
       hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.segments * a.H), dim3(512), 0, st, a);
       return hipGetLastError();
     }
-    if (a.order) hipLaunchKernelGGL(k_prompt_order, dim3((a.n + 255) / 256), dim3(256), 0, st, a);
     if (in_chains(a.n, a.H)) hipLaunchKernelGGL(k_prompt_chain, dim3((a.n * a.H + 7) / 8 * 32), dim3(512), 0, st, a);
     else hipLaunchKernelGGL(k_prompt_scan<true>, dim3(a.n * a.H), dim3(512), 0, st, a);
     return hipGetLastError();
