@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) k_prompt_scan(PromptArgs P
   f32x4 S[8];
 #pragma unroll
   for (int m = 0; m < 8; ++m) {
-    if (segments > 1 && (!DELTA || from > 0)) S[m] = segment_ws(P, place, A.h, threadIdx.x)[m * 512];
+    // (of a cut sequence the slot is written by another workgroup of this launch)
+    if (segments > 1) S[m] = segment_ws(P, place, A.h, threadIdx.x)[m * 512];
     else if (carried) S[m] = state.get(state_row(m, g), col);
     else S[m] = (f32x4){0, 0, 0, 0};
   }
@@ -1077,7 +1078,8 @@ __global__ void __launch_bounds__(512, 2) k_prompt_map(PromptArgs P) {
   }
 }
 
-// DELTA: the states that the segments from the second on start from.  A
+// DELTA: the states that the segments start from; the first one's is S_0, which
+// takes the place of what the segment makes of it.  A
 // workgroup takes sixteen columns of a (sequence, head); wave w makes results
 // 2 w and 2 w + 1, which are what contraction step w needs of the next state,
 // and has the next segment's operands on their way.  1.6 us a segment; one wave
@@ -1112,6 +1114,11 @@ __global__ void __launch_bounds__(256, 1) k_prompt_join_maps(PromptArgs P) {
   f32x4 S[2];
 #pragma unroll
   for (int y = 0; y < 2; ++y) S[y] = state(0)[y * 512];
+  const bool carried = P.carry != nullptr && P.carry[b] != 0;
+  const StateAt start(P, b, slot, h);
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    state(0)[y * 512] = carried ? start.get(state_row(2 * w + y, l >> 4), 16 * cols + (l & 15)) : (f32x4){0, 0, 0, 0};
   auto step = [&](int i, In &in) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) state(i)[y * 512] = S[y];

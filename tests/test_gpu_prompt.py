@@ -193,6 +193,29 @@ def test_long_delta_prompts(torch_dev, lens, carried, gates):
     assert torch.equal(o, run(torch, dense, DELTA, slots, lens, x, [1] * n if carried else None))
 
 
+@pytest.mark.parametrize("packed", [False, True], ids=["uncompressed", "quantised"])
+def test_long_delta_prompts_hand_on_the_state_they_continue(torch_dev, packed):
+    """The first segment's readout starts from the workspace, as the others'
+    do: the last segment's workgroup writes the slot in the same launch.  So
+    the state a prompt continues from stands there when the call is done."""
+    torch = torch_dev
+    lens, H = [2500, 40, 1460], 2
+    x = make(torch, 18, sum(lens), H)
+    pool = qdr.Pool(3, H, [8, 16], np.ones((H, D), np.float32)) if packed else fp32_pool(3, H)
+    slots, carry = [2, 0, 1], [1, 1, 0]
+    S0 = torch.randn((3, H, D, D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))
+    pool.qdr_pack(i32(torch, slots), S0)
+    S0 = states(torch, pool, slots)
+    ws = torch.zeros(pool.qdr_prompt_workspace(3, sum(lens)), dtype=torch.uint8, device="cuda")
+    o = run(torch, pool, DELTA, slots, lens, x, carry, workspace=ws)
+    held = torch.isin(S0[0].view(torch.int32), ws.view(torch.int32))
+    assert held.all(), f"{(~held).sum().item()} of {held.numel()} values of the state are not handed on"
+    dense = fp32_pool(3, H)
+    dense.qdr_pack(i32(torch, slots), S0)
+    assert torch.equal(o, run(torch, dense, DELTA, slots, lens, x, carry))
+    check(torch, x, DELTA, lens, 0, o, states(torch, dense, slots), S0 * torch.tensor(carry, device="cuda")[:, None, None, None])
+
+
 def test_prompt_non_finite_in_segments(torch_dev):
     """Values that are not finite in one head of a long prompt."""
     torch = torch_dev
