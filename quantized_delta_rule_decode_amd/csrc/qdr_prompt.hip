@@ -1091,7 +1091,11 @@ __global__ void __launch_bounds__(256, 1) k_prompt_join_maps(PromptArgs P) {
   const int per = P.segment * kChunk;
   int first, len;
   const int slot = P.slots[b];
-  if (!rows_of(P.cu, P.T, b, &first, &len) || slot < 0 || slot >= P.num_slots) return;   // (k_prompt_scan tells)
+  if (!rows_of(P.cu, P.T, b, &first, &len)) {   // (as in k_prompt_join)
+    if (threadIdx.x == 0) atomicOr(P.err, kErrLength);
+    return;
+  }
+  if (slot < 0 || slot >= P.num_slots) return;
   const int segments = (len + per - 1) / per, place = first / per + b;
   if (segments < 2) return;
   struct In {

@@ -387,6 +387,19 @@ def test_prompt_errors_on_the_device(torch_dev):
 
 
 @pytest.mark.parametrize("rule", [DELTA, SUM])
+@pytest.mark.parametrize("cu", [[0, 512, 256, 4000], [0, 256, 0, 4000], [0, 4000, 3999, 4000]], ids=str)
+def test_counts_that_decrease_between_segments(torch_dev, rule, cu):
+    """A decreasing pair is told of also where no segment falls to its sequence."""
+    torch = torch_dev
+    H, T = 2, 4000
+    pool, x = fp32_pool(3, H), make(torch, 54, T, H)
+    o = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    pool.qdr_prompt(rule, i32(torch, [0, 1, 2]), i32(torch, cu), x["q"], x["k"], x["v"], x["beta"], x["gate"], o)
+    assert pool.qdr_poll_device_error() == qdr.DEVERR_LENGTH
+    pool.close()
+
+
+@pytest.mark.parametrize("rule", [DELTA, SUM])
 def test_prompt_rows_beyond_32_bits(torch_dev, rule):
     """Rows whose elements and bytes are numbered above 2^31 and 2^32."""
     torch = torch_dev
