@@ -143,10 +143,12 @@ qdr_status qdr_kv_attend_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32
  * q, o: [T][q_heads][128] bfloat16; q_heads a multiple of num_heads.  One new
  * token a sequence, many, or both in one call.  Scores, the softmax and the
  * sums are fp32; the weights enter their product as bfloat16, in two parts
- * for sequences of few rows, unless those are a small share of a call.  A key or
- * value that is not finite reaches the rows that see its token, in its own head,
- * and no others.  Rows of a skipped sequence are 0, and so is a row that sees no
- * key. */
+ * (2^-16) for a sequence that brings up to 16 rows a key/value head (tokens x
+ * q_heads / num_heads; a single token always), whatever the others bring, in
+ * one (2^-8) for a longer one.  Of a call of one sequence T counts as its
+ * length.  A key or value that is not finite reaches the rows that see its
+ * token, in its own head, and no others.  Rows of a skipped sequence are 0, and
+ * so is a row that sees no key. */
 qdr_status qdr_kv_attend(qdr_kv *kv, const int32_t *pages, int32_t max_pages, const int32_t *cu,
                          const int32_t *context, int32_t n, int32_t T, int32_t q_heads,
                          const uint16_t *q, float scale, uint16_t *o, void *workspace,

@@ -179,12 +179,10 @@ AttendPlan plan_attend(int n, int T, int q_heads, int heads, int max_pages, int 
   p.many_tokens = kManyRows / p.many_heads;
   p.many_parts = (p.group + p.many_heads - 1) / p.many_heads;
   // T <= n: hardly a sequence has more than one token.  One sequence: its
-  // length is T.  Else the two launches share the sequences out by length, but
-  // where eight many-row tiles come to a sequence, the few-row launch costs more
-  // than tiles of few rows among so many (two of 961 new tokens of 6 and 2 heads
-  // over 1852, 8-bit, 45.9 us with it, 42.0 without; 4 x 256 of 32 and 8 over
-  // 2048, bfloat16, 76.8 and 72.8).
-  p.few = T <= p.few_tokens || (n > 1 && T < (int64_t)8 * p.many_tokens * n);
+  // length is T.  Else the two launches share the sequences out by length, also
+  // where T says that most are long: a token among long chunks would walk its
+  // whole context in one workgroup, and its weights would lose their second part.
+  p.few = n > 1 || T <= p.few_tokens;
   p.many = T > n && !(n == 1 && T <= p.few_tokens);
   p.few_tiles = !p.few ? 0 : p.many ? n : T / p.few_tokens + n;
   p.many_tiles = p.many ? T / p.many_tokens + n : 0;
