@@ -22,6 +22,9 @@
  * skipped; the other sequences' results are then unspecified as well (what
  * is read and written stays inside the arrays).
  *
+ * Sizes.  n and T are at most 2^30.  A call that would take 2^24 workgroups (of
+ * 256 threads) or more in one launch is refused with QDR_E_INVAL: cut it up.
+ *
  * Workspaces.  A call that takes one uses it until the work it enqueued has
  * finished.  Calls that may run at the same time (other streams, other
  * captured graphs) need workspaces of their own.  16-byte aligned.

@@ -498,12 +498,14 @@ static qdr_status check_heads(const qdr_kv *kv, int32_t q_heads) {
 // The plan of a call, and whether its launches and partial results can be counted.
 static qdr_status make_plan(const qdr_kv *kv, int32_t n, int32_t T, int32_t q_heads, int32_t max_pages, qdr::AttendPlan *plan) {
   const int64_t heads = kv->desc.num_heads;
-  // an upper bound on the workgroups of either launch (64 pieces at most)
-  QDR_TRY(check_groups(((int64_t)T + n) * q_heads));
+  // heads, sequences and with them tiles fit 32 bits; each is a part of the counts below
+  QDR_TRY(check_groups(q_heads));
+  QDR_TRY(check_groups(n));
   *plan = qdr::plan_attend(n, T, q_heads, kv->desc.num_heads, max_pages, kv->page_shift);
   const int64_t few = (int64_t)plan->few_tiles * heads * plan->few_parts, many = (int64_t)plan->many_tiles * heads * plan->many_parts;
-  QDR_TRY(check_groups(few * 2 * (plan->few_splits > 4 ? plan->few_splits : 4)));
-  return check_groups(many * (plan->many_splits > 32 ? plan->many_splits : 32));
+  // of 512 threads a few-row tile and piece, and four workgroups to join its pieces
+  QDR_TRY(check_groups(std::max(few * 2 * plan->few_splits, plan->few_splits > 1 ? few * 4 : 0)));
+  return check_groups(many * std::max(plan->many_splits, plan->many_splits > 4 ? 32 : plan->many_splits > 1 ? 4 : 1));
 }
 
 qdr_status qdr_kv_attend_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32_t q_heads, int32_t max_pages, size_t *bytes) {

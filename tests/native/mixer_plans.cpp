@@ -25,8 +25,32 @@ static int few_rows_beside_long() {
   return 0;
 }
 
+// A call is refused for the workgroups that it has, not for more than those.
+static int sizes() {
+  qdr_kv_desc d{4, 64, 8, 128, QDR_KV_BF16};
+  qdr_kv *kv = nullptr;
+  CHECK(qdr_kv_create(&d, nullptr, 0, &kv) == QDR_OK && kv);
+  size_t need = 0;
+  CHECK(qdr_kv_attend_workspace(kv, 1, 262144, 64, 4096, &need) == QDR_OK);
+  CHECK(qdr_kv_attend_workspace(kv, 4096, 262144, 64, 1, &need) == QDR_OK && need == 0);
+  CHECK(qdr_kv_attend_workspace(kv, 1, 1 << 22, 64, 1 << 16, &need) == QDR_OK && need == 0);
+  // just under 2^24: tiles of sixteen tokens, eight heads; of a single token a few-row one
+  CHECK(qdr_kv_attend_workspace(kv, 1, (1 << 25) - 32, 64, 1, &need) == QDR_OK);
+  REFUSED(qdr_kv_attend_workspace(kv, 1, 1 << 25, 64, 1, &need), QDR_E_INVAL);
+  CHECK(qdr_kv_attend_workspace(kv, (1 << 20) - 1, 1, 8, 1, &need) == QDR_OK);
+  REFUSED(qdr_kv_attend_workspace(kv, 1 << 20, 1, 8, 1, &need), QDR_E_INVAL);
+  // far over: nothing overflows on the way
+  for (int n : {1, 2, 1 << 24, 1 << 30})
+    for (int T : {1 << 28, 1 << 30})
+      for (int q_heads : {8, 8 << 10, (1 << 24) - 8, (1 << 30), 0x7FFFFFF8})
+        for (int pages : {0, 1, 0x7FFFFFFF}) REFUSED(qdr_kv_attend_workspace(kv, n, T, q_heads, pages, &need), QDR_E_INVAL);
+  for (int q_heads : {(1 << 24), 0x7FFFFFF8}) REFUSED(qdr_kv_attend_workspace(kv, 1, 1, q_heads, 1, &need), QDR_E_INVAL);
+  CHECK(qdr_kv_destroy(kv) == QDR_OK);
+  return 0;
+}
+
 int main() {
-  if (few_rows_beside_long()) return 1;
+  if (few_rows_beside_long() || sizes()) return 1;
   std::printf("ok %d\n", checks);
   return 0;
 }

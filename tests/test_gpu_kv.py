@@ -481,6 +481,22 @@ def test_largest_context(torch_dev, rows):
     assert cache.qdr_kv_poll_device_error() == 0
 
 
+def test_attend_of_very_many_rows(torch_dev):
+    """2^24 (token, head) rows in one call: 4096 sequences of 64 tokens and 64
+    query heads; every fourth has the same queries and pages, and results."""
+    torch = torch_dev
+    n, m, H, Q = 4096, 64, 8, 64
+    cache, pages, k, v = fill(torch, [m] * 4, 64, H, BF16)
+    few = vectors(torch, 9, 4 * m, Q)
+    q = few.repeat(n // 4, 1, 1)
+    o = torch.full_like(q, 7)
+    cache.qdr_kv_attend(pages.repeat(n // 4, 1), counts(torch, [m] * n), i32(torch, [m] * n), q, o)
+    assert cache.qdr_kv_poll_device_error() == 0
+    ref, room = reference(torch, few, k, v, [m] * 4, [m] * 4, D ** -0.5)
+    assert ((o[:4 * m].double() - ref).abs() <= room).all()
+    assert (o.view(n // 4, 4 * m, Q, D) == o[:4 * m]).all()
+
+
 def test_refusals(torch_dev):
     torch = torch_dev
     cache = qdr.KVCache(2, 32, 2, INT8)
