@@ -102,7 +102,8 @@ typedef struct {
   int32_t kind;          /* QDR_KV_*                                        */
 } qdr_kv_desc;
 
-/* Device bytes of the cache (pure host computation). */
+/* Device bytes of the cache (pure host computation).  QDR_E_INVAL where they
+ * do not fit 63 bits. */
 qdr_status qdr_kv_bytes(const qdr_kv_desc *desc, size_t *bytes);
 /* Create a cache on the current HIP device.  dev_mem as in qdr_pool_create
  * (at least qdr_kv_bytes, 256-byte aligned, outlives the cache; NULL: the

@@ -237,7 +237,10 @@ qdr_status check_kv_desc(const qdr_kv_desc *d, size_t *bytes, int *shift) {
   while (s <= 10 && (1 << s) != d->page_tokens) ++s;
   if (s > 10) return fail(QDR_E_INVAL, "page_tokens must be a power of two from 32 to 1024 (got %d)", d->page_tokens);
   const size_t block = d->kind == QDR_KV_INT8 ? qdr::kKv8Block : qdr::kKv16Block;
-  *bytes = (size_t)d->num_pages * d->num_heads * (d->page_tokens / qdr::kBlock) * block;
+  const size_t page = (size_t)d->num_heads * (d->page_tokens / qdr::kBlock) * block;   // under 2^50
+  if (page > (size_t)INT64_MAX / d->num_pages)
+    return fail(QDR_E_INVAL, "%d pages of %zu bytes do not fit 64 bits", d->num_pages, page);
+  *bytes = (size_t)d->num_pages * page;
   *shift = s;
   return QDR_OK;
 }

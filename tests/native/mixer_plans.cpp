@@ -49,8 +49,25 @@ static int sizes() {
   return 0;
 }
 
+// A cache whose bytes do not fit 64 bits is refused, not made smaller.
+static int large_caches() {
+  size_t n = 0;
+  const int32_t most = 0x7FFFFFFF;
+  qdr_kv_desc d{most, 1024, 8, 128, QDR_KV_BF16};
+  CHECK(qdr_kv_bytes(&d, &n) == QDR_OK && n == (size_t)most * 8 * 32 * 16384);
+  alignas(256) static char own[1 << 16];
+  for (int32_t heads : {1 << 20, 1 << 14, most}) {       // (2^31 - 1) 2^20 2^19 bytes: a small number modulo 2^64
+    d.num_heads = heads;
+    qdr_kv *kv = nullptr;
+    REFUSED(qdr_kv_bytes(&d, &n), QDR_E_INVAL);
+    REFUSED(qdr_kv_create(&d, own, sizeof own, &kv), QDR_E_INVAL);
+    CHECK(kv == nullptr);
+  }
+  return 0;
+}
+
 int main() {
-  if (few_rows_beside_long() || sizes()) return 1;
+  if (few_rows_beside_long() || sizes() || large_caches()) return 1;
   std::printf("ok %d\n", checks);
   return 0;
 }
