@@ -27,7 +27,10 @@
  *
  * Workspaces.  A call that takes one uses it until the work it enqueued has
  * finished.  Calls that may run at the same time (other streams, other
- * captured graphs) need workspaces of their own.  16-byte aligned.
+ * captured graphs) need workspaces of their own.  16-byte aligned.  What a call
+ * needs does not grow with its counts: a smaller one may cut its sequences or
+ * keys into pieces where a larger one does not, and need more.  A workspace for
+ * several shapes has the most bytes that any of them is said to need.
  */
 #ifndef QDR_MIXER_H
 #define QDR_MIXER_H
@@ -49,7 +52,8 @@ extern "C" {
  *   S_t = alpha_t S_{t-1} + k_t u_t^T,   o_t = S_t^T q_t                   */
 enum { QDR_RULE_DELTA = 0, QDR_RULE_SUM = 1 };
 
-/* Bytes of the workspace of a prompt call over n sequences and T rows. */
+/* Bytes of the workspace of a prompt call over n sequences and T rows, for just
+ * these counts (fewer can need more). */
 qdr_status qdr_prompt_workspace(const qdr_pool *pool, int32_t n, int32_t T, size_t *bytes);
 
 /* The prompt form: n sequences of any lengths, taken 64 tokens at a time on
@@ -136,7 +140,8 @@ qdr_status qdr_kv_read(qdr_kv *kv, const int32_t *pages, int32_t max_pages, cons
                        const int32_t *context, int32_t n, int32_t T, uint16_t *k, uint16_t *v,
                        void *stream);
 
-/* Bytes of the workspace of an attention call (0 is possible). */
+/* Bytes of the workspace of an attention call of just these counts (0 is
+ * possible, and fewer sequences or rows can need more). */
 qdr_status qdr_kv_attend_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32_t q_heads,
                                    int32_t max_pages, size_t *bytes);
 /* Attention of new tokens over the cache, their own keys and values among it

@@ -307,7 +307,7 @@ class Pool:
 
     # ---- token mixers over the pool's states (include/qdr_mixer.h)
     def qdr_prompt_workspace(self, n, T) -> int:
-        """Bytes of the workspace of a prompt call over n sequences and T rows."""
+        """Bytes of the workspace of a prompt call over n sequences and T rows, for just these counts (fewer can need more)."""
         b = ctypes.c_size_t(0)
         _check("qdr_prompt_workspace", load().qdr_prompt_workspace(self._h, int(n), int(T), ctypes.byref(b)))
         return int(b.value)
@@ -427,6 +427,7 @@ class KVCache:
         self._move("qdr_kv_read", pages, cu, context, k, v, stream)
 
     def qdr_kv_attend_workspace(self, n, T, q_heads, max_pages) -> int:
+        """Bytes of the workspace of an attention call of just these counts (fewer sequences or rows can need more)."""
         b = ctypes.c_size_t(0)
         _check("qdr_kv_attend_workspace", load().qdr_kv_attend_workspace(
             self._h, int(n), int(T), int(q_heads), int(max_pages), ctypes.byref(b)))
