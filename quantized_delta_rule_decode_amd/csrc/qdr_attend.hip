@@ -5,7 +5,7 @@
 // query's statistics are one value a lane, and the accumulators of S^T are the
 // B operand of O^T = V^T P^T (qdr_mfma.h); the cache keeps K and V in the
 // order of the A operands.  So nothing crosses lanes between the two products
-// except the column maximum (two shuffles).
+// except the column maximum (two lane swaps).
 // 8-bit caches: codes are exact in bfloat16, the key's scale multiplies its
 // scores and the value's scale its weights, both in fp32.
 #include "qdr_mfma.h"

@@ -550,8 +550,8 @@ __device__ __forceinline__ void columns(int wave, int l, Stage<DELTA> &st, f32x4
   update_state<!DELTA>(st.K, st.dec, u, S, l);
 }
 
-// Which chunks of which sequence a workgroup takes: a whole sequence, or with
-// SUM a segment of P.segment chunks of one.
+// Which chunks of which sequence a workgroup takes: a whole sequence, or a
+// segment of P.segment chunks of one.
 __device__ __forceinline__ bool scan_at(const PromptArgs &P, int place, int *b, int *from, int *to, int *segments, ScanAt &A) {
   const int per = P.segment * kChunk;
   *b = P.segment ? sequence_of(P.cu, P.n, per, 1, place) : P.order ? P.order[place] : place;
@@ -571,7 +571,8 @@ __device__ __forceinline__ bool scan_at(const PromptArgs &P, int place, int *b, 
 
 // A segment's state in the workspace: a thread's eight results side by side
 // with its neighbours'; before k_prompt_join what the segment adds to a state,
-// and the decay over it, then the state that it starts from.
+// and the decay over it (DELTA: what it makes of 0, and its map), then the state
+// that it starts from.
 __device__ __forceinline__ f32x4 *segment_ws(const PromptArgs &P, int place, int h, int tid) {
   return (f32x4 *)P.segment_ws + ((size_t)place * P.H + h) * (kD * kD / 4) + tid;
 }
