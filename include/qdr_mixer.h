@@ -156,8 +156,10 @@ qdr_status qdr_kv_attend_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32
  * q_heads / num_heads; a single token always), whatever the others bring, in
  * one (2^-8) for a longer one.  Of a call of one sequence T counts as its
  * length.  A key or value that is not finite reaches the rows that see its
- * token, in its own head, and no others.  Rows of a skipped sequence are 0, and
- * so is a row that sees no key. */
+ * token, in its own head, and no others; the weighted values are summed in fp32
+ * before they are divided (weights up to 2^8), so values have to stay that far
+ * from its end.  Rows of a skipped sequence are 0, and so is a row that sees no
+ * key or whose scores are all -infinity. */
 qdr_status qdr_kv_attend(qdr_kv *kv, const int32_t *pages, int32_t max_pages, const int32_t *cu,
                          const int32_t *context, int32_t n, int32_t T, int32_t q_heads,
                          const uint16_t *q, float scale, uint16_t *o, void *workspace,
