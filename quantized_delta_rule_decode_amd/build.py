@@ -28,7 +28,8 @@ SOURCES = ["qdr_head_int_step.hip", "qdr_head_int_pack.hip", "qdr_head_int_unpac
            "qdr_head_int_reset.hip", "qdr_head_int_readout.hip", "qdr_head_int_step_bf16.hip", "qdr_head_int_writeback.hip", "qdr_head_fp16.hip", "qdr_head_fp32.hip", "qdr_rows.hip", "qdr_dispatch.cpp",
            "qdr_runtime.cpp", "qdr_clock.hip"]
 # the token mixers beside the step (prompt form, additive step, key/value cache)
-MIXER_SOURCES = ["qdr_prompt.hip", "qdr_linear.hip", "qdr_kv.hip", "qdr_attend.hip", "qdr_mixer.cpp"]
+MIXER_SOURCES = ["qdr_prompt.hip", "qdr_linear.hip", "qdr_kv.hip", "qdr_attend.hip", "qdr_mixer.cpp",
+                 "qdr_rotary.hip", "qdr_pages.hip", "qdr_attend_shared.hip", "qdr_cache.cpp"]
 # every file the step's device code is built from (a change to any of them changes its kernels)
 # (the clock probe is a diagnostic kernel of its own, not part of the step)
 DEVICE_SOURCES = ["qdr_device.h", "qdr_internal.h"] + [s for s in SOURCES

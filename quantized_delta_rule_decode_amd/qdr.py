@@ -1,4 +1,5 @@
-"""Python binding of libqdr (include/qdr.h, include/qdr_mixer.h): argument marshalling only.
+"""Python binding of libqdr (include/qdr.h, include/qdr_mixer.h, include/qdr_cache.h): argument
+marshalling only.
 
 Every function here has the name of the C entry point it calls.  Tensors are
 torch tensors on the current HIP device; the library receives their device
@@ -20,9 +21,11 @@ GATE_SCALAR, GATE_DIAG = 0, 1
 UNIT_HEAD, UNIT_ROW = 0, 1
 SCALE_DUAL, SCALE_ROW_ABSMAX = 0, 1
 K_INT2, K_INT4, K_INT6, K_INT8, K_FP16, K_FP32 = 2, 4, 6, 8, 16, 32
-DEVERR_SLOT, DEVERR_LENGTH, DEVERR_PAGE = 1, 2, 4
+DEVERR_SLOT, DEVERR_LENGTH, DEVERR_PAGE, DEVERR_FULL = 1, 2, 4, 8
 RULE_DELTA, RULE_SUM = 0, 1
 KV_INT8, KV_BF16 = 8, 16
+ROTARY_HALF, ROTARY_PAIRS = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_TURNS, ROTARY_INDEX = 0, 1, 2, 3
 
 _STATUS = {0: "QDR_OK", -1: "QDR_E_INVAL", -2: "QDR_E_NOMEM", -3: "QDR_E_DEVICE",
            -4: "QDR_E_SLOT", -5: "QDR_E_UNSUPPORTED"}
@@ -57,6 +60,11 @@ class KVDesc(ctypes.Structure):
                 ("num_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32)]
 
 
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("channels", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("freq", ctypes.c_void_p), ("amplitude", ctypes.c_double)]
+
+
 EXPORTS = ["qdr_pool_bytes", "qdr_pool_create", "qdr_pool_destroy", "qdr_slot_reset",
            "qdr_pack", "qdr_unpack", "qdr_decode_step", "qdr_decode_step_split", "qdr_decode_step_bf16", "qdr_get_layout", "qdr_read_raw",
            "qdr_write_raw", "qdr_poll_device_error", "qdr_last_error", "qdr_clock_probe"]
@@ -64,6 +72,10 @@ EXPORTS = ["qdr_pool_bytes", "qdr_pool_create", "qdr_pool_destroy", "qdr_slot_re
 MIXER_EXPORTS = ["qdr_prompt_workspace", "qdr_prompt", "qdr_linear_step", "qdr_linear_step_bf16", "qdr_kv_bytes",
                  "qdr_kv_create", "qdr_kv_destroy", "qdr_kv_write", "qdr_kv_read", "qdr_kv_attend_workspace",
                  "qdr_kv_attend", "qdr_kv_poll_device_error"]
+
+CACHE_EXPORTS = ["qdr_rotary_frequencies", "qdr_rotary_create", "qdr_rotary_destroy", "qdr_rotate", "qdr_rotate_bf16",
+                 "qdr_kv_write_rotary", "qdr_kv_copy", "qdr_slot_copy", "qdr_kv_assign_workspace", "qdr_kv_assign",
+                 "qdr_kv_compact_workspace", "qdr_kv_compact", "qdr_kv_attend_shared_workspace", "qdr_kv_attend_shared"]
 
 _lib = None
 _raw_stream = None
@@ -81,7 +93,7 @@ def load():
     # instead of loading a second runtime instance.
     import torch
     L = ctypes.CDLL(LIB_PATH)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ, F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_double
     sig = {
         "qdr_pool_bytes": [ctypes.POINTER(PoolDesc), ctypes.POINTER(SZ)],
         "qdr_pool_create": [ctypes.POINTER(PoolDesc), P, SZ, ctypes.POINTER(P)],
@@ -109,6 +121,20 @@ def load():
         "qdr_kv_attend_workspace": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
         "qdr_kv_attend": [P, P, I32, P, P, I32, I32, I32, P, ctypes.c_float, P, P, SZ, P],
         "qdr_kv_poll_device_error": [P, ctypes.POINTER(ctypes.c_uint32)],
+        "qdr_rotary_frequencies": [I32, I32, F64, F64, F64, F64, F64, P, ctypes.POINTER(F64)],
+        "qdr_rotary_create": [ctypes.POINTER(RotaryDesc), ctypes.POINTER(P)],
+        "qdr_rotary_destroy": [P],
+        "qdr_rotate": [P, P, I32, I32, P, I64, P, I64, P],
+        "qdr_rotate_bf16": [P, P, I32, I32, P, I64, P, I64, P],
+        "qdr_kv_write_rotary": [P, P, P, I32, P, P, I32, I32, P, I64, I32, P, P, I64, P, I64, P],
+        "qdr_kv_copy": [P, P, P, P, I32, P],
+        "qdr_slot_copy": [P, P, P, I32, P],
+        "qdr_kv_assign_workspace": [P, I32, ctypes.POINTER(SZ)],
+        "qdr_kv_assign": [P, P, P, I32, I32, P, P, I32, P, P, P, P, P, SZ, P],
+        "qdr_kv_compact_workspace": [P, ctypes.POINTER(SZ)],
+        "qdr_kv_compact": [P, P, P, I32, I32, P, P, P, P, SZ, P],
+        "qdr_kv_attend_shared_workspace": [P, I32, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "qdr_kv_attend_shared": [P, P, I32, P, P, I32, I32, P, P, I32, I32, P, ctypes.c_float, P, P, SZ, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -160,6 +186,20 @@ def _ptr(t, dtype, name, shape):
         pass
     _dptr(t, dtype, name)
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _strided(t, dtype, name, heads):
+    """Address and distance between rows of a device tensor [T][heads][128] whose rows are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 3 or t.shape[2] != DIM or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (T, {'heads' if heads is None else heads}, {DIM})")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != DIM):
+        raise ValueError(f"{name} must have contiguous rows of [heads][{DIM}]")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * DIM
 
 
 def _sequences(cu):
@@ -346,6 +386,13 @@ class Pool:
         import torch
         self._linear_step("qdr_linear_step_bf16", torch.bfloat16, slots, q, k, v, gate, o, stream)
 
+    def qdr_slot_copy(self, src_slots, dst_slots, stream=None):
+        """Stored states of src_slots to dst_slots (int32 [m]; -1 on either side: the pair is skipped)."""
+        import torch
+        m = src_slots.numel()
+        _check("qdr_slot_copy", load().qdr_slot_copy(
+            self._h, _ptr(src_slots, torch.int32, "src_slots", (m,)), _ptr(dst_slots, torch.int32, "dst_slots", (m,)), m, _stream(stream)))
+
     def qdr_read_raw(self, slot, stream=None) -> np.ndarray:
         out = np.empty(self.slot_stride, np.uint8)
         _check("qdr_read_raw", load().qdr_read_raw(
@@ -449,10 +496,160 @@ class KVCache:
             self._h, *where, T, heads, _ptr(q, bf, "q", rows), DIM ** -0.5 if scale is None else scale, _ptr(o, bf, "o", rows),
             ws, size, _stream(stream)))
 
+    # ---- around the cache (include/qdr_cache.h)
+    def qdr_kv_write_rotary(self, rotary, pages, cu, context, k, v, q=None, q_out=None, stream=None):
+        """qdr_kv_write of turned keys, and q [T][q_heads][128] turned into
+        q_out (contiguous).  q, k and v may be parts of one projection's rows."""
+        import torch
+        bf = torch.bfloat16
+        n, T, heads = _sequences(cu), k.shape[0], 0 if q is None else q.shape[1]
+        (kp, ks), (vp, vs) = _strided(k, bf, "k", self.num_heads), _strided(v, bf, "v", self.num_heads)
+        qp, qs, out = None, 0, None
+        if q is not None:
+            qp, qs = _strided(q, bf, "q", None)
+            out = _ptr(q_out, bf, "q_out", (T, heads, DIM))
+        if v.shape[0] != T or (q is not None and q.shape[0] != T):
+            raise ValueError("q, k and v must have the same number of rows")
+        _check("qdr_kv_write_rotary", _lib.qdr_kv_write_rotary(
+            self._h, rotary._h, *self._where(n, pages, cu, context), T, qp, qs, heads, out, kp, ks, vp, vs, _stream(stream)))
+
+    def qdr_kv_copy(self, src_pages, dst_pages, to=None, stream=None):
+        """Pages src_pages to pages dst_pages (int32 [m]) of this cache, or of the cache `to`."""
+        import torch
+        m = src_pages.numel()
+        _check("qdr_kv_copy", _lib.qdr_kv_copy(
+            self._h, _ptr(src_pages, torch.int32, "src_pages", (m,)), (self if to is None else to)._h,
+            _ptr(dst_pages, torch.int32, "dst_pages", (m,)), m, _stream(stream)))
+
+    def qdr_kv_assign_workspace(self, m) -> int:
+        """Bytes of the workspace of an assignment of m rows."""
+        b = ctypes.c_size_t(0)
+        _check("qdr_kv_assign_workspace", load().qdr_kv_assign_workspace(self._h, int(m), ctypes.byref(b)))
+        return int(b.value)
+
+    def qdr_kv_assign(self, pages, context, parent, add, refs, new_pages, new_context, new_refs, workspace=None, stream=None):
+        """Page tables of the next step: row j goes on from row parent[j] (-1:
+        from none) by add[j] tokens.  pages int32 [n][max_pages], context int32
+        [n], parent, add int32 [m], refs int32 [num_pages]; the new arrays
+        [m][max_pages], [m], [num_pages] are written."""
+        import torch
+        i32 = torch.int32
+        if pages.dim() != 2 or parent.dim() != 1:
+            raise ValueError("pages must have two dimensions and parent one")
+        (n, most), m = pages.shape, parent.shape[0]
+        ws, size, keep = _workspace(workspace, 0 if workspace is not None else self.qdr_kv_assign_workspace(m), stream)
+        _check("qdr_kv_assign", _lib.qdr_kv_assign(
+            self._h, _ptr(pages, i32, "pages", (n, most)), _ptr(context, i32, "context", (n,)), n, most,
+            _ptr(parent, i32, "parent", (m,)), _ptr(add, i32, "add", (m,)), m, _ptr(refs, i32, "refs", (self.num_pages,)),
+            _ptr(new_pages, i32, "new_pages", (m, most)), _ptr(new_context, i32, "new_context", (m,)),
+            _ptr(new_refs, i32, "new_refs", (self.num_pages,)), ws, size, _stream(stream)))
+
+    def qdr_kv_compact_workspace(self) -> int:
+        """Bytes of qdr_kv_compact's workspace."""
+        b = ctypes.c_size_t(0)
+        _check("qdr_kv_compact_workspace", load().qdr_kv_compact_workspace(self._h, ctypes.byref(b)))
+        return int(b.value)
+
+    def qdr_kv_compact(self, refs, pages, moved, new_refs, new_pages, workspace=None, stream=None):
+        """Pages in use (refs int32 [num_pages], not 0) to the lowest numbers.
+        moved, new_refs int32 [num_pages] and new_pages like pages [n][max_pages] are written."""
+        import torch
+        i32, total = torch.int32, (self.num_pages,)
+        if pages.dim() != 2:
+            raise ValueError("pages must have two dimensions")
+        n, most = pages.shape
+        ws, size, keep = _workspace(workspace, 0 if workspace is not None else self.qdr_kv_compact_workspace(), stream)
+        _check("qdr_kv_compact", _lib.qdr_kv_compact(
+            self._h, _ptr(refs, i32, "refs", total), _ptr(pages, i32, "pages", (n, most)), n, most, _ptr(moved, i32, "moved", total),
+            _ptr(new_refs, i32, "new_refs", total), _ptr(new_pages, i32, "new_pages", (n, most)), ws, size, _stream(stream)))
+
+    def qdr_kv_attend_shared_workspace(self, n, T, groups, q_heads, max_pages) -> int:
+        """Bytes of the workspace of such a call of just these counts (smaller counts can need more)."""
+        b = ctypes.c_size_t(0)
+        _check("qdr_kv_attend_shared_workspace", load().qdr_kv_attend_shared_workspace(
+            self._h, int(n), int(T), int(groups), int(q_heads), int(max_pages), ctypes.byref(b)))
+        return int(b.value)
+
+    def qdr_kv_attend_shared(self, pages, cu, context, group_cu, shared, q, o, scale=None, workspace=None, stream=None):
+        """qdr_kv_attend where the sequences group_cu[i] .. group_cu[i+1]-1 have
+        their first shared[i] tokens in common.  group_cu int32 [groups+1], shared
+        int32 [groups]."""
+        import torch
+        i32, n, bf = torch.int32, _sequences(cu), torch.bfloat16
+        if q.dim() != 3 or q.shape[2] != DIM:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected (T, q_heads, {DIM})")
+        if shared.dim() != 1:
+            raise ValueError("shared must be one-dimensional")
+        T, heads, _ = rows = q.shape
+        where, groups = self._where(n, pages, cu, context), shared.shape[0]
+        need = 0 if workspace is not None else self.qdr_kv_attend_shared_workspace(n, T, groups, heads, where[1])
+        ws, size, keep = _workspace(workspace, need, stream)
+        _check("qdr_kv_attend_shared", _lib.qdr_kv_attend_shared(
+            self._h, *where, T, _ptr(group_cu, i32, "group_cu", (groups + 1,)), _ptr(shared, i32, "shared", (groups,)), groups, heads,
+            _ptr(q, bf, "q", rows), DIM ** -0.5 if scale is None else scale, _ptr(o, bf, "o", rows), ws, size, _stream(stream)))
+
     def qdr_kv_poll_device_error(self) -> int:
         f = ctypes.c_uint32(0)
         _check("qdr_kv_poll_device_error", load().qdr_kv_poll_device_error(self._h, ctypes.byref(f)))
         return int(f.value)
+
+
+def qdr_rotary_frequencies(rule, channels, base=10000.0, factor=1.0, context=8192.0, low=1.0, high=32.0):
+    """Frequencies (float64 [channels/2], radians a token) and amplitude of a ROTARY_ rule."""
+    freq, amplitude = np.empty(max(0, int(channels) // 2)), ctypes.c_double(0)
+    _check("qdr_rotary_frequencies", load().qdr_rotary_frequencies(
+        int(rule), int(channels), base, factor, context, low, high, freq.ctypes.data, ctypes.byref(amplitude)))
+    return freq, amplitude.value
+
+
+class Rotary:
+    """A rotation (qdr_rotary_create ... qdr_rotary_destroy): frequencies of the
+    pairs of a head's first 2 len(freq) channels."""
+
+    def __init__(self, freq, layout=ROTARY_HALF, amplitude=1.0):
+        freq = np.ascontiguousarray(freq, np.float64)
+        if freq.ndim != 1:
+            raise ValueError("freq must be one-dimensional")
+        self.channels, self.layout, self.amplitude = 2 * freq.size, int(layout), float(amplitude)
+        d, h = RotaryDesc(DIM, self.channels, self.layout, freq.ctypes.data, self.amplitude), ctypes.c_void_p(None)
+        _check("qdr_rotary_create", load().qdr_rotary_create(ctypes.byref(d), ctypes.byref(h)))
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            _check("qdr_rotary_destroy", load().qdr_rotary_destroy(self._h))
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def _turn(self, fn, dtype, positions, x, y, stream):
+        import torch
+        xp, xs = _strided(x, dtype, "x", None)
+        yp, ys = _strided(y, dtype, "y", x.shape[1])
+        T = x.shape[0]
+        if y.shape[0] != T:
+            raise ValueError(f"y has {y.shape[0]} rows, expected {T}")
+        _check(fn, getattr(_lib, fn)(self._h, _ptr(positions, torch.int32, "positions", (T,)), T, x.shape[1], xp, xs, yp, ys, _stream(stream)))
+
+    def qdr_rotate(self, positions, x, y, stream=None):
+        """y = x turned by positions (int32 [T]); x, y fp32 [T][heads][128], rows any distance apart; y may be x."""
+        import torch
+        self._turn("qdr_rotate", torch.float32, positions, x, y, stream)
+
+    def qdr_rotate_bf16(self, positions, x, y, stream=None):
+        """The same with torch.bfloat16 x and y."""
+        import torch
+        self._turn("qdr_rotate_bf16", torch.bfloat16, positions, x, y, stream)
 
 
 def qdr_last_error() -> str:
