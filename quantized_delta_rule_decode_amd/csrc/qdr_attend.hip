@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) k_attend_few(AttendArgs A, 
   const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   FewOut<kFewWaves> out;
-  few_tile<KIND, kFewWaves>(A, t, kvh, lo, hi, sh, out);
+  few_tile<KIND, kFewWaves, true>(A, t, threadIdx.x, kvh, lo, hi, sh, out);
   static_assert(kFewWaves == 8, "a wave to sixteen channels");
   const f32x4 y = out.o[0];
   if (plan.few_splits == 1) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_many(AttendArgs A, AttendPlan
   const int l = threadIdx.x & 63, g = l >> 4, i16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ManyOut out;
-  many_tile<KIND>(A, t, kvh, lo, hi, sh, out);
+  many_tile<KIND, false>(A, t, threadIdx.x, kvh, lo, hi, sh, out);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     if (plan.many_splits == 1) {

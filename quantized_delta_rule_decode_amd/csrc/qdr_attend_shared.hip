@@ -1,13 +1,17 @@
 // qdr_attend_shared.hip -- attention of new tokens over the paged cache where
 // sequences share their first tokens: a group's rows go through the shared keys
-// together, every sequence's rows through its own, in one launch; a second one
-// joins what each row's passes left (qdr_cache.h).
+// together, every sequence's rows through its own, in one launch whose
+// workgroups have equal parts of the groups' work or a sequence's tile; a second one joins what each
+// row's passes left (qdr_cache.h).
 #include "qdr_attend_tiles.h"
 #include "qdr_cache.h"
 
 namespace qdr {
 
 namespace {
+
+constexpr int kCell = kD + 2;   // floats of a row's result: 128 sums, maximum, sum of weights
+constexpr int kItems = 256;     // groups that a workgroup has at hand
 
 // Last i of 0 .. n - 1 with first(i) <= id, where first() does not fall; 64
 // candidates at a time.  The whole wave calls it.
@@ -34,37 +38,43 @@ struct Share {
   bool bad;            // the group is skipped
   int tokens;          // shared ones
   int blocks;          // whole blocks of keys that its rows go through together; 0: each sequence by itself
-  int begin;           // the group's first sequence
-  int first, len;      // and its rows
+  int begin, end;      // its sequences
+  int first, len;      // its rows
 };
 
-__device__ __forceinline__ Share share_of(const SharedArgs &S, const SharedPlan &plan, int group) {
+// (The loads of a step do not wait for each other: what may be out of range is
+// cut to it before, and looked at behind.)
+__device__ __forceinline__ Share share_of(const SharedArgs &S, const SharedPlan &plan, int begin, int end, int tokens) {
   const KvArgs &P = S.a.kv;
-  Share r{true, 0, 0, 0, 0, 0};
-  const int begin = S.group_cu[group], end = S.group_cu[group + 1];
-  if (begin < 0 || end < begin || end > P.n) return r;
-  r.begin = begin;
-  r.tokens = S.shared[group];
-  if (begin == end) {
-    r.bad = false;
-    return r;
-  }
-  const int room = room_of(P), c0 = P.cu[begin], c1 = P.cu[begin + 1], ce = P.cu[end], ctx = P.context[begin];
-  r.bad = r.tokens < 0 || r.tokens > room || c0 < 0 || c1 < c0 || ce < c1 || ce > P.T || ctx > room || (long long)ctx - (c1 - c0) < r.tokens;
+  const bool order = begin >= 0 && end >= begin && end <= P.n;
+  const int b0 = order ? min(begin, P.n - 1) : 0, b1 = order ? end : 0;
+  const int c0 = P.cu[b0], c1 = P.cu[b0 + 1], ce = P.cu[b1], ctx = P.context[b0], room = room_of(P);
+  const bool none = order && begin == end;
+  Share r;
+  r.tokens = tokens;
+  r.begin = b0;
+  r.end = b1;
+  const bool counts = c0 >= 0 && c1 >= c0 && ce >= c1 && ce <= P.T;
+  r.bad = !order || (!none && (tokens < 0 || tokens > room || !counts || ctx > room || (int64_t)ctx - (c1 - c0) < tokens));
   r.first = c0;
-  r.len = r.bad ? 0 : ce - c0;
+  r.len = r.bad || none ? 0 : ce - c0;
   // sequences that fill tiles by themselves gain nothing, and would leave partial results
-  const bool together = end - begin >= 2 && r.len < (long long)(end - begin) * plan.many_tokens;
-  r.blocks = !r.bad && together ? r.tokens / kBlock : 0;
+  const bool together = r.end - r.begin >= 2 && r.len < (int64_t)(r.end - r.begin) * plan.many_tokens;
+  r.blocks = r.len > 0 && together ? tokens / kBlock : 0;
   return r;
 }
 
-__device__ __forceinline__ Share share_of_sequence(const SharedArgs &S, const SharedPlan &plan, int b) {
-  Share none{false, 0, 0, 0, 0, 0};
-  if (S.groups == 0) return none;
-  const int group = last_of(S.groups, b, [&](int i) { return S.group_cu[i]; });
-  if (b < S.group_cu[group] || b >= S.group_cu[group + 1]) return none;
-  return share_of(S, plan, group);
+// The group of sequence b: the last i with group_cu[i] <= b.
+template <class F>
+__device__ __forceinline__ int group_of_sequence(int groups, int b, F group_cu) {
+  int lo = 0, len = groups;
+  while (len > 1) {
+    const int half = len >> 1;
+    const bool behind = group_cu(lo + half) <= b;
+    lo = behind ? lo + half : lo;
+    len = behind ? len - half : half;
+  }
+  return lo;
 }
 
 // Counts, contexts and groups out of order or range, found once a call.
@@ -72,215 +82,505 @@ __device__ __forceinline__ void check_groups(const SharedArgs &S, const SharedPl
   const KvArgs &P = S.a.kv;
   check_counts(P);
   bool bad = false;
-  for (int i = threadIdx.x; i < S.groups; i += 256) {
-    const Share s = share_of(S, plan, i);
-    bad = bad || s.bad;
-    if (s.bad) continue;
-    for (int b = S.group_cu[i] + 1; b < S.group_cu[i + 1]; ++b) {
-      int first, len;
-      if (rows_of(P.cu, P.T, b, &first, &len) && len > 0 && P.context[b] - len < s.tokens) bad = true;
-    }
+  for (int i = threadIdx.x; i < S.groups; i += 256) bad = bad || share_of(S, plan, S.group_cu[i], S.group_cu[i + 1], S.shared[i]).bad;
+  for (int b = threadIdx.x; b < P.n && S.groups > 0; b += 256) {
+    const int group = group_of_sequence(S.groups, b, [&](int i) { return S.group_cu[i]; });
+    int first, len;
+    if (b >= S.group_cu[group] && b < S.group_cu[group + 1] && rows_of(P.cu, P.T, b, &first, &len) && len > 0 && P.context[b] - len < S.shared[group]) bad = true;
   }
   if (bad) atomicOr(P.err, kErrLength);
 }
 
-// Where a sequence's or group's many-row tiles begin.
-__device__ __forceinline__ int many_place(const SharedArgs &S, const SharedPlan &plan, int first) {
-  first = min(max(first, 0), S.a.kv.T);
-  return first / plan.many_tokens + first / (plan.few_tokens + 1);
+// The rows of a group and its shared keys, or of a sequence.
+struct Item {
+  double start;        // where a group's tiles begin in the line (a whole number)
+  int tiles;           // 0: no rows
+  int b;               // whose page table
+  int first, len;      // rows
+  int position;        // of row 0; kMostContext: every row sees every key
+  int begin, blocks;   // blocks of keys: a sequence's own begin there; a group's
+  int flags;
+};
+constexpr int kFew = 1, kPrefix = 2, kSkipped = 4, kPooled = 8;   // kPooled: its rows have shared keys too
+
+// What a tile and each of its blocks cost, in 0.1 us of a workgroup (two a
+// compute unit): 128 rows and 32 keys are bound by issue, few rows by memory.
+constexpr int kTileCost = 60, kLeastCost = 100, kHalfCost = 400;   // (the last two of a workgroup)
+template <int KIND>
+__device__ __forceinline__ double block_cost(int flags) { return flags & kFew ? (KIND == 8 ? 8.0 : 14.0) : 8.0; }
+template <int KIND>
+__device__ __forceinline__ double tile_cost(int flags, int blocks) { return kTileCost + blocks * block_cost<KIND>(flags); }
+
+__device__ __forceinline__ Item item_of_group(const SharedArgs &S, const SharedPlan &plan, int i) {
+  Item t{0, 0, 0, 0, 0, 0, 0, 0, 0};
+  if (i >= S.groups) return t;
+  const Share share = share_of(S, plan, S.group_cu[i], S.group_cu[i + 1], S.shared[i]);
+  t.b = share.begin;
+  t.first = share.first;
+  t.len = share.blocks ? share.len : 0;
+  t.position = kMostContext;
+  t.blocks = share.blocks;
+  const bool few = t.len <= plan.few_tokens;
+  t.flags = kPrefix | (few ? kFew : 0);
+  t.tiles = t.len == 0 ? 0 : few ? plan.few_parts : (t.len + plan.many_tokens - 1) / plan.many_tokens * plan.many_parts;
+  return t;
 }
 
-constexpr float kDone = -1.0f;     // in a row's first sum of its own: o is written
+__device__ __forceinline__ Item item_of_sequence(const SharedArgs &S, const SharedPlan &plan, int b) {
+  const KvArgs &P = S.a.kv;
+  Item t{0, 0, 0, 0, 0, 0, 0, 0, 0};
+  const int s = P.cu[b], e = P.cu[b + 1], ctx = P.context[b];
+  Share share{false, 0, 0, 0, 0, 0, 0};
+  if (S.groups > 0) {
+    const int group = last_of(S.groups, b, [&](int i) { return S.group_cu[i]; });
+    const int g0 = S.group_cu[group], g1 = S.group_cu[group + 1];
+    if (b >= g0 && b < g1) share = share_of(S, plan, g0, g1, S.shared[group]);
+  }
+  t.b = b;
+  t.first = s;
+  t.len = s >= 0 && e >= s && e <= P.T ? e - s : 0;
+  const bool skipped = share.bad || ctx < t.len || ctx > room_of(P) || ctx - t.len < share.tokens;
+  t.flags = (skipped ? kSkipped : share.blocks ? kPooled : 0) | (t.len <= plan.few_tokens ? kFew : 0);
+  t.position = ctx - t.len;
+  t.begin = skipped ? 0 : share.blocks;
+  return t;
+}
+
+// A token's passes over keys: parts r0 .. r1 of the line (kPieces: pieces 0 .. r1
+// of sequence r0's few rows or of many-row tile r0), and the row of its first head
+// of the part in their tile.
+struct Passes {
+  int r0, r1, row;
+  int flags;           // kFew, kPooled, kPieces; kDone: o is written
+};
+constexpr int kDone = 16, kPieces = 128;
+
+// The line of the groups' work, cut into ranges of `step` (rounded down to whole costs,
+// the same everywhere).
+struct Line {
+  double total, step, inverse;
+  int ranges, range;       // of the workgroup
+  double a, b;             // its part
+};
+// Parts: of kLeastCost at least; half as many as there are places for (one
+// workgroup a compute unit, which leaves half the partial results) where they
+// then are no longer than kHalfCost.
+__device__ __forceinline__ int ranges_of(int most, double total) {
+  const double half = fmin((double)((most + 1) / 2), ceil(total * (1.0 / kLeastCost)));
+  return (int)fmin((double)most, fmax(half, ceil(total * (1.0 / kHalfCost))));
+}
+__device__ __forceinline__ double range_begin(const Line &line, int r) { return r < line.ranges ? floor(r * line.step) : line.total; }
+__device__ __forceinline__ int range_at(const Line &line, double x) {
+  int r = min((int)(x * line.inverse), line.ranges - 1);
+  if (range_begin(line, r) > x) --r;
+  if (range_begin(line, r + 1) <= x) ++r;
+  return min(max(r, 0), line.ranges - 1);
+}
+
+// One pass: a tile over blocks lo .. hi.
+struct Job {
+  Tile t;
+  int lo, hi;
+  int flags;               // of the item; kAlone: the rows' only pass; kCut: one of several over the tile
+  float *whole, *cell;     // results by row, and of the workgroup's cut tile
+  Passes *info, passes;    // of the tile's first token, and what to write there (NULL: another workgroup does)
+  int info_step;
+};
+constexpr int kAlone = 32, kCut = 64;
 
 template <int KIND>
-union Scratch {
-  ManyShared<KIND> many[2];
-  FewShared<kSharedWaves> few;
+struct Scratch {
+  union {
+    ManyShared<KIND> many[2];
+    FewShared<kSharedWaves> few;
+  };
+  Item items[kItems];
+  double sums[4];
+  double base;             // where this chunk of items begins in the line
+  SharedArgs args;
+  SharedPlan plan;
+  Line line;
+  Job job;
 };
+
+// Sum over the threads before this one, of 256; *all: over every thread.
+__device__ __forceinline__ double sum_before(double x, double *lds, double *all) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  double s = x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(s, d);
+    if (lane >= d) s += y;
+  }
+  __syncthreads();
+  if (lane == 63) lds[w] = s;
+  __syncthreads();
+  double before = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) before += i < w ? lds[i] : 0.0;
+  *all = lds[0] + lds[1] + lds[2] + lds[3];
+  return before + s - x;
+}
+
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Tile k of a group as the workgroup's next pass.
+template <int KIND>
+__device__ __forceinline__ void make_job(const SharedArgs &S, const SharedPlan &plan, const Line &line, const Item &it, int k, int kvh, Job &job) {
+  const KvArgs &P = S.a.kv;
+  const int flags = it.flags, blocks = it.blocks;
+  const bool few = flags & kFew;
+  const int parts = few ? plan.few_parts : plan.many_parts, per = few ? plan.few_tokens : plan.many_tokens, most = few ? plan.few_heads : plan.many_heads;
+  const double each = tile_cost<KIND>(flags, blocks), from = it.start + k * each;
+  const int r0 = from >= line.a ? line.range : range_at(line, from);
+  const int r1 = from + each <= line.b ? line.range : range_at(line, from + each - 1);
+  const double per_block = 1.0 / block_cost<KIND>(flags);
+  auto cut = [&](double at) { return (int)fmin(fmax(ceil((at - from - kTileCost) * per_block), 0.0), (double)blocks); };
+  const int tile = parts == 1 ? k : k / parts, part = k - tile * parts;
+  Tile t;
+  t.b = it.b;
+  t.first = it.first;
+  t.len = it.len;
+  t.token = tile * per;
+  t.tokens = min(per, it.len - t.token);
+  t.head = kvh * plan.group + part * most;
+  t.heads = min(most, plan.group - part * most);
+  t.skipped = false;
+  t.position = kMostContext;
+  t.keys = blocks * kBlock;
+  job.t = t;
+  job.lo = r0 == line.range ? 0 : cut(line.a);
+  job.hi = r1 == line.range ? blocks : cut(line.b);
+  job.flags = flags | (r0 == r1 ? 0 : kCut);
+  job.whole = S.a.part;
+  job.cell = S.a.part + plan.cut + (size_t)((line.range * P.heads + kvh) * 2 + (r0 == line.range)) * plan.slot_rows * kCell;
+  // each token's passes are written down once
+  Passes *info = (Passes *)(S.a.part + plan.info);
+  job.info = kvh == 0 && line.range == r0 ? info + (size_t)(t.first + t.token) * plan.few_parts + part : nullptr;
+  job.passes = {r0, r1, 0, flags & kFew};
+  job.info_step = plan.few_parts;
+}
+
+// Piece `split` of a sequence's tile from `token` on, whose number is `tile`;
+// false: there is none.
+__device__ __forceinline__ bool make_piece(const SharedArgs &S, const SharedPlan &plan, const Item &it, int tile, int token, int part, int split, int kvh, Job &job) {
+  const KvArgs &P = S.a.kv;
+  const bool few = it.flags & kFew;
+  const int most = few ? plan.few_heads : plan.many_heads, splits = few ? plan.few_splits : plan.many_splits, parts = few ? plan.few_parts : plan.many_parts;
+  Tile t;
+  t.b = it.b;
+  t.first = it.first;
+  t.len = it.len;
+  t.token = token;
+  t.tokens = min(few ? plan.few_tokens : plan.many_tokens, it.len - token);
+  t.head = kvh * plan.group + part * most;
+  t.heads = min(most, plan.group - part * most);
+  t.skipped = it.flags & kSkipped;
+  t.position = it.position + token;
+  t.keys = t.skipped ? 0 : t.position + t.tokens;
+  const int blocks = (t.keys + kBlock - 1) / kBlock - it.begin;
+  const int each = piece_blocks(blocks, splits, few ? kSharedLeast : kManyLeast), pieces = max((blocks + each - 1) / each, 1);
+  if (split >= pieces) return false;
+  const bool alone = pieces == 1 && !(it.flags & kPooled);
+  job.t = t;
+  job.lo = it.begin + split * each;
+  job.hi = min(job.lo + each, it.begin + blocks);
+  job.flags = it.flags | (alone ? kAlone : 0) | (pieces == 1 ? 0 : kCut);
+  job.whole = S.a.part + plan.cut / 2;
+  job.cell = S.a.part + (few ? plan.few_pieces : plan.many_pieces) + ((((size_t)tile * P.heads + kvh) * parts + part) * splits + split) * ((few ? kFewRows : kManyRows) * kCell);
+  Passes *info = (Passes *)(S.a.part + plan.info) + (size_t)P.T * plan.few_parts;
+  job.info = kvh == 0 && split == 0 ? info + (size_t)(t.first + token) * plan.few_parts + part : nullptr;
+  job.passes = {pieces == 1 ? 0 : tile, pieces - 1, 0, (it.flags & (kFew | kPooled)) | (alone ? kDone : 0) | (pieces == 1 ? 0 : kPieces)};
+  job.info_step = plan.few_parts;
+  return true;
+}
+
+template <int KIND>
+__device__ __forceinline__ void pass(const AttendArgs &A, int kvh, Scratch<KIND> &sh) {
+  // (not known to be the same in every pass: what follows from it is made anew
+  // instead of kept in registers that a pass has not got)
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int l = tid & 63, g = l >> 4, w = scalar(tid >> 6);
+  Tile t;
+  t.b = scalar(sh.job.t.b);
+  t.first = scalar(sh.job.t.first);
+  t.token = scalar(sh.job.t.token);
+  t.tokens = scalar(sh.job.t.tokens);
+  t.head = scalar(sh.job.t.head);
+  t.heads = scalar(sh.job.t.heads);
+  t.position = scalar(sh.job.t.position);
+  t.keys = scalar(sh.job.t.keys);
+  const int lo = scalar(sh.job.lo), hi = scalar(sh.job.hi);
+  if (sh.job.info && tid < t.tokens) {
+    Passes p = sh.job.passes;
+    p.row = tid * t.heads;
+    sh.job.info[(size_t)tid * sh.job.info_step] = p;
+  }
+  const volatile Job &job = sh.job;
+  auto place = [&](size_t at, int row) { return job.flags & kCut ? job.cell + (size_t)row * kCell : job.whole + at / kD * kCell; };
+  // channels c .. c + 3 of a row
+  auto put = [&](size_t at, int row, int c, f32x4 y, float sum) {
+    if (job.flags & kAlone) {
+      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      *(u32x2_a4 *)(A.o + at + c) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+    } else if (job.lo < job.hi) {
+      float *to = place(at, row) + c;
+      *(f32x2 *)to = (f32x2){y[0], y[1]};
+      *(f32x2 *)(to + 2) = (f32x2){y[2], y[3]};
+    }
+  };
+  auto note = [&](size_t at, int row, float m, float sum) {
+    if (!(job.flags & kAlone)) *(f32x2 *)(place(at, row) + kD) = (f32x2){m, sum};
+  };
+  if (scalar(sh.job.flags) & kFew) {
+    FewOut<kSharedWaves> out;
+    few_tile<KIND, kSharedWaves, KIND == 8>(A, t, tid, kvh, lo, hi, sh.few, out);
+    if (!out.row) return;
+#pragma unroll
+    for (int y = 0; y < 8 / kSharedWaves; ++y) put(out.at, l & 15, 16 * (8 / kSharedWaves * w + y) + 4 * g, out.o[y], out.sum);
+    if (w == 0 && g == 0) note(out.at, l & 15, out.m, out.sum);
+  } else {
+    ManyOut out;
+    many_tile<KIND, true>(A, t, tid, kvh, lo, hi, sh.many, out);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (!out.row[c]) continue;
+      const int row = 32 * w + 16 * c + (l & 15);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) put(out.at[c], row, 16 * d + 4 * g, out.o[c][d], out.sum[c]);
+      if (g == 0) note(out.at[c], row, out.m[c], out.sum[c]);
+    }
+  }
+}
+
+// Where a sequence's many-row tiles begin.
+__device__ __forceinline__ int many_place(const SharedArgs &S, const SharedPlan &plan, int b, int first) {
+  first = min(max(first, 0), S.a.kv.T);
+  return first / plan.many_tokens + (plan.by_tokens ? first / (plan.few_tokens + 1) : b);
+}
 
 template <int KIND>
 __global__ void __launch_bounds__(256, 2) k_attend_shared(SharedArgs S, SharedPlan plan) {
   __shared__ Scratch<KIND> sh;
-  const AttendArgs &A = S.a;
-  const KvArgs &P = A.kv;
-  // whose tile, of what
-  const int shared_many = plan.many_groups * plan.many_cuts * plan.many_parts * P.heads;
-  const int shared_few = plan.few_groups * plan.few_cuts * plan.few_parts * P.heads;
-  const int own_many = plan.many_tiles * plan.many_splits * plan.many_parts * P.heads;
-  const int own_few = plan.few_tiles * plan.few_splits * plan.few_parts * P.heads;
-  int x = blockIdx.x;
-  bool prefix = true, few = false;
-  if (x >= shared_many) {
-    x -= shared_many;
-    few = true;
-    if (x >= shared_few) {
-      x -= shared_few;
-      prefix = few = false;
-      if (x >= own_many) {
-        x -= own_many;
-        few = true;
-        if (x >= own_few) {
-          check_groups(S, plan);
-          return;
-        }
-      }
-    }
-  }
+  const int tid = threadIdx.x;
   // heads change fastest: workgroups are dealt to the eight XCDs in turn, so the
   // tiles that read the same keys share few L2s
-  const int kvh = x % P.heads;
-  const int parts = few ? plan.few_parts : plan.many_parts, part = x / P.heads % parts;
-  const int tiles = prefix ? (few ? plan.few_groups : plan.many_groups) : (few ? plan.few_tiles : plan.many_tiles);
-  const int tile = x / (P.heads * parts) % tiles, split = x / (P.heads * parts) / tiles;
-  const int splits = prefix ? (few ? plan.few_cuts : plan.many_cuts) : (few ? plan.few_splits : plan.many_splits);
-  const int per = few ? plan.few_tokens : plan.many_tokens, most = few ? plan.few_heads : plan.many_heads;
-
-  Tile t;
-  int begin = 0, blocks;
-  if (prefix) {
-    const int group = few ? tile : last_of(plan.few_groups, tile, [&](int i) {
-      const int b = S.group_cu[i];
-      return b < 0 || b > P.n ? 0 : many_place(S, plan, P.cu[b]);
-    });
-    const Share s = share_of(S, plan, group);
-    if (s.blocks == 0 || (s.len <= plan.few_tokens) != few) return;
-    t.b = s.begin;
-    t.first = s.first;
-    t.len = s.len;
-    t.token = few ? 0 : (tile - many_place(S, plan, s.first)) * per;
-    if (t.token < 0 || t.token >= t.len) return;
-    t.tokens = min(per, t.len - t.token);
-    t.skipped = false;
-    t.position = kMostContext;     // every row sees every key
-    t.keys = s.blocks * kBlock;
-    blocks = s.blocks;
-  } else {
-    t.b = few ? tile : last_of(P.n, tile, [&](int b) { return many_place(S, plan, P.cu[b]); });
-    if (!rows_of(P.cu, P.T, t.b, &t.first, &t.len) || (t.len <= plan.few_tokens) != few) return;
-    t.token = few ? 0 : (tile - many_place(S, plan, t.first)) * per;
-    if (t.token < 0 || t.token >= t.len) return;
-    t.tokens = min(per, t.len - t.token);
-    const Share s = share_of_sequence(S, plan, t.b);
-    const int ctx = P.context[t.b];
-    t.skipped = s.bad || ctx < t.len || ctx > room_of(P) || ctx - t.len < s.tokens;
-    t.position = ctx - t.len + t.token;
-    t.keys = t.skipped ? 0 : t.position + t.tokens;
-    begin = t.skipped ? 0 : s.blocks;
-    blocks = (t.keys + kBlock - 1) / kBlock - begin;
+  const int kvh = blockIdx.x % S.a.kv.heads;
+  int place = blockIdx.x / S.a.kv.heads;
+  if (place >= plan.ranges) {
+    // sequences' own keys: few rows, then many, those with most keys first
+    place -= plan.ranges;
+    const bool few = place < S.a.kv.n * plan.few_parts * plan.few_splits;
+    if (!few) place -= S.a.kv.n * plan.few_parts * plan.few_splits;
+    const int parts = few ? plan.few_parts : plan.many_parts, splits = few ? plan.few_splits : plan.many_splits;
+    const int part = place % parts, split = place / parts % splits;
+    int tile = place / (parts * splits), b = tile, token = 0;
+    if (!few) {
+      tile = plan.many_tiles - 1 - tile;
+      if (tile < 0) {      // one workgroup more
+        check_groups(S, plan);
+        return;
+      }
+      b = last_of(S.a.kv.n, tile, [&](int i) { return many_place(S, plan, i, S.a.kv.cu[i]); });
+      token = tile - many_place(S, plan, b, S.a.kv.cu[b]);
+    }
+    const Item mine = item_of_sequence(S, plan, b);
+    token *= few ? 1 : plan.many_tokens;
+    if (mine.len == 0 || (mine.len <= plan.few_tokens) != few || token < 0 || token >= mine.len) return;
+    Job job;
+    if (!make_piece(S, plan, mine, tile, token, part, split, kvh, job)) return;
+    if (tid == 0) sh.job = job;
+  } else if (tid == 0) {
+    // (a pass has no registers to spare: what deals out the work is at hand in LDS)
+    sh.args = S;
+    sh.plan = plan;
+    sh.base = 0;
+    sh.line.total = 0;
   }
-  t.head = kvh * plan.group + part * most;
-  t.heads = min(most, plan.group - part * most);
-  const int each = piece_blocks(blocks, splits, kSharedLeast);
-  const int lo = begin + split * each, hi = min(lo + each, begin + blocks);
-  const bool alone = !prefix && begin == 0 && each >= blocks;   // the rows' only pass
-  if (alone && split > 0) return;
-
-  // The rows' statistics also where a pass has no keys, and, by the last piece, in
-  // the places that the other kind of tiles has more pieces for; where nothing is
-  // shared, by the first piece, in those of shared keys.
-  const int place = prefix ? split : plan.shared_places + split;
-  const int end = split + 1 < splits ? place + 1 : prefix ? plan.shared_places : plan.places;
-  const bool clears = !prefix && begin == 0 && split == 0;
-  const int l = threadIdx.x & 63, g = l >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  auto note = [&](size_t at, float m, float sum) {
-    float *to = S.stats + at / kD * plan.places * 2;
-    if (alone) {
-      to[2 * plan.shared_places + 1] = kDone;
-      return;
+  __syncthreads();
+  // Every workgroup of the line makes it by itself, 256 groups at a time: once
+  // through for its length, and once (the only chunk is still at hand) for the
+  // groups of its part.
+  const bool line_part = (int)(blockIdx.x / S.a.kv.heads) < plan.ranges;
+  const int chunks = line_part ? (S.groups + kItems - 1) / kItems : 1;
+#pragma unroll 1
+  for (int c = 0; c < 2 * chunks; ++c) {
+    int x = 0, k = 0;
+    double all = 0;
+    bool here = true;
+    if (line_part) {
+      Item mine = item_of_group(sh.args, sh.plan, (c < chunks ? c : c - chunks) * kItems + tid);
+      const double before = sum_before(mine.tiles * tile_cost<KIND>(mine.flags, mine.blocks), sh.sums, &all);
+      if (c < chunks) {
+        if (tid == 0) {
+          Line line = sh.line;
+          line.total += all;
+          if (c + 1 == chunks) {
+            const int range = blockIdx.x / sh.args.a.kv.heads;
+            line.ranges = ranges_of(sh.plan.ranges, line.total);
+            line.step = line.total / line.ranges;
+            line.inverse = line.ranges / line.total;
+            line.range = range;
+            line.a = range < line.ranges ? range_begin(line, range) : line.total;
+            line.b = range < line.ranges ? range_begin(line, range + 1) : line.total;
+          }
+          sh.line = line;
+        }
+        __syncthreads();
+        if (c + 1 < chunks) continue;
+        if (sh.line.total == 0 || sh.line.a >= sh.line.b) return;
+        if (chunks > 1) continue;
+      }
+      here = sh.base + all > sh.line.a;
+      if (here) {
+        mine.start = sh.base + before;
+        sh.items[tid] = mine;
+        __syncthreads();
+        // the first group that ends behind the part's beginning, and from there on
+#pragma unroll 1
+        for (int step = kItems / 2; step > 0; step >>= 1)
+          if (sh.items[x + step].start <= sh.line.a) x += step;
+        if (sh.items[x].start < sh.line.a) {
+          const double each = tile_cost<KIND>(sh.items[x].flags, sh.items[x].blocks), into = sh.line.a - sh.items[x].start;
+          k = (int)(into / each);
+          if (k * each > into) --k;
+          if ((k + 1) * each <= into) ++k;
+        }
+        x = scalar(x);
+        k = scalar(k);
+      }
     }
-    *(f32x2 *)(to + 2 * place) = (f32x2){m, sum};
-    for (int p = place + 1; p < end; ++p) *(f32x2 *)(to + 2 * p) = (f32x2){kNone, 0.0f};
-    if (clears)
-      for (int p = 0; p < plan.shared_places; ++p) *(f32x2 *)(to + 2 * p) = (f32x2){kNone, 0.0f};
-  };
-  // sixteen channels' four of a lane: 16 d + 4 g ..
-  auto put = [&](size_t at, int d, f32x4 y, float sum) {
-    if (alone) {
-      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-      *(u32x2_a4 *)(A.o + at + 16 * d + 4 * g) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
-    } else if (lo < hi) {
-      *(f32x4 *)(A.part + (at / kD * plan.places + place) * kD + 16 * d + 4 * g) = y;
+    while (here) {
+      if (line_part) {
+        if (x == kItems || sh.items[x].start >= sh.line.b) break;
+        if (k >= scalar(sh.items[x].tiles)) {
+          ++x;
+          k = 0;
+          continue;
+        }
+        if (sh.items[x].start + k * tile_cost<KIND>(sh.items[x].flags, sh.items[x].blocks) >= sh.line.b) break;
+        if (tid == 0) make_job<KIND>(sh.args, sh.plan, sh.line, sh.items[x], k, kvh, sh.job);
+        ++k;
+        __syncthreads();
+      }
+      pass<KIND>(S.a, kvh, sh);
+      if (!line_part) return;
+      __syncthreads();
     }
-  };
-  if (few) {
-    FewOut<kSharedWaves> out;
-    few_tile<KIND, kSharedWaves>(A, t, kvh, lo, hi, sh.few, out);
-    if (!out.row) return;
-#pragma unroll
-    for (int y = 0; y < 8 / kSharedWaves; ++y) put(out.at, 8 / kSharedWaves * w + y, out.o[y], out.sum);
-    if (w == 0 && g == 0) note(out.at, out.m, out.sum);
-  } else {
-    ManyOut out;
-    many_tile<KIND>(A, t, kvh, lo, hi, sh.many, out);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (!out.row[c]) continue;
-#pragma unroll
-      for (int d = 0; d < 8; ++d) put(out.at[c], d, out.o[c][d], out.sum[c]);
-      if (g == 0) note(out.at[c], out.m[c], out.sum[c]);
-    }
+    if (chunks == 1) return;
+    __syncthreads();
+    if (tid == 0) sh.base += all;
+    __syncthreads();
+    if (sh.base >= sh.line.b) return;
   }
 }
 
-// Joins a row's passes (64 at most): a wave a row, a lane a pass's maximum and
-// sum; then half a wave takes four channels a lane of every other pass that had
-// keys, sixteen of them on their way at once.
+// Joins the passes of OWN rows a wave, those over shared keys first: a lane has a
+// pass's maximum and sum; then half a wave takes four channels a lane of every
+// other pass, sixteen of them on their way at once.
+template <int OWN>
 __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan plan) {
   constexpr int kLoads = 8;
   const AttendArgs &A = S.a;
   const KvArgs &P = A.kv;
   const int l = threadIdx.x & 63, half = l >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t token = row / A.q_heads;
-  if (token < P.cu[0] || token >= P.cu[P.n] || token >= P.T) return;
-  const f32x2 own = *(const f32x2 *)(S.stats + (row * plan.places + min(l, plan.places - 1)) * 2);
-  if (__shfl(own[1], plan.shared_places) == kDone) return;
-  const bool live = l < plan.places && !(own[0] == kNone && own[1] == 0.0f);
-  const float top = wave_max(live ? own[0] : kNone);
-  const float f = live ? ex2(own[0] - (top == kNone ? 0.0f : top)) : 0.0f;
-  float sum = live ? own[1] * f : 0.0f;
+  const int begin = P.cu[0], end = min(P.cu[P.n], P.T);
+#pragma unroll 1
+  for (int i = 0; i < OWN; ++i) {
+    const int64_t row = ((int64_t)blockIdx.x * 4 + scalar((int)threadIdx.x >> 6)) * OWN + i;
+    const int64_t token = row / A.q_heads;
+    if (token < begin || token >= end) continue;
+    const int head = (int)(row - token * A.q_heads), kvh = head / plan.group, h = head - kvh * plan.group;
+    const Passes *shared = (const Passes *)(A.part + plan.info) + token * plan.few_parts, *own = shared + (size_t)P.T * plan.few_parts;
+    Passes o = own[0], s{0, -1, 0, 0};
+    if (o.flags & kDone && plan.few_parts == 1) {
+      if (OWN > 1) i += min((int64_t)(OWN - 1 - i), (int64_t)A.q_heads - 1 - head);   // and the token's other rows are
+      continue;
+    }
+    int part = 0;
+    auto at_part = [&](const Passes *from, Passes &p) {
+      const int heads = p.flags & kFew ? plan.few_heads : plan.many_heads;
+      part = h / heads;
+      if (part > 0) p = from[part];
+      p.row += h - part * heads;
+    };
+    if (o.flags & kPooled) {
+      s = shared[0];
+      at_part(shared, s);
+    }
+    at_part(own, o);
+    if (o.flags & kDone) continue;
+    // (counts out of order leave rows without)
+    const bool pieces = o.flags & kPieces;
+    auto bad = [&](const Passes &p) { return p.r0 < 0 || p.r0 > p.r1 || p.r1 >= plan.ranges || p.row < 0 || p.row >= plan.slot_rows; };
+    const bool own_few = o.flags & kFew;
+    const int rows = own_few ? kFewRows : kManyRows, splits = own_few ? plan.few_splits : plan.many_splits, parts = own_few ? plan.few_parts : plan.many_parts;
+    if (pieces ? o.r0 < 0 || o.r0 >= (own_few ? P.n : plan.many_tiles) || o.r1 < 0 || o.r1 >= splits || o.row < 0 || o.row >= rows : o.r0 != 0 || o.r1 != 0) continue;
+    if (o.flags & kPooled && (plan.ranges == 0 || bad(s))) continue;
+    if (!pieces && !(o.flags & kPooled)) continue;
+    const int ns = s.r1 - s.r0 + 1, passes = ns + o.r1 + 1;
+    const float *own_cell = pieces ? A.part + (own_few ? plan.few_pieces : plan.many_pieces) + ((((size_t)o.r0 * P.heads + kvh) * parts + part) * splits * rows + o.row) * kCell
+                                   : A.part + plan.cut / 2 + row * kCell;
+    auto cell = [&](int p) -> const float * {
+      if (p >= ns) return own_cell + (size_t)(p - ns) * rows * kCell;
+      const int r = s.r0 + p;
+      return s.r0 == s.r1 ? A.part + row * kCell : A.part + plan.cut + ((size_t)((r * P.heads + kvh) * 2 + (r == s.r0)) * plan.slot_rows + s.row) * kCell;
+    };
+    float top = kNone, sum = 0.0f;
+    f32x4 y = (f32x4){0, 0, 0, 0};
+    for (int p0 = 0; p0 < passes; p0 += 64) {
+      const f32x2 x = *(const f32x2 *)(cell(min(p0 + l, passes - 1)) + kD);
+      const bool in = p0 + l < passes;
+      const float top1 = fmaxf(top, wave_max(in ? x[0] : kNone));
+      const float ref = top1 == kNone ? 0.0f : top1, fade = ex2(top - ref);
+      top = top1;
+      const float f = in ? ex2(x[0] - ref) : 0.0f;
+      // (a pass without keys left no result to read)
+      uint64_t left = __ballot(in && !(x[0] == kNone && x[1] == 0.0f));
+      float add = in ? x[1] * f : 0.0f;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  f32x4 o = (f32x4){0, 0, 0, 0};
-  uint64_t left = __ballot(live);
-  const float *from = A.part + row * plan.places * kD + 4 * (l & 31);
-  while (left) {
-    f32x4 y[kLoads];
-    int at[kLoads];
+      for (int d = 1; d < 64; d <<= 1) add += __shfl_xor(add, d);
+      sum = sum * fade + add;
+      y *= fade;
+      while (left) {
+        f32x2 z[kLoads][2];
+        int at[kLoads];
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) {
-      // the next two passes, one a half; behind the last one the last again, without weight
-      const int a = left ? __builtin_ctzll(left) : 0;
-      const bool one = left != 0;
-      left &= left - 1;
-      const int b = left ? __builtin_ctzll(left) : a;
-      const bool two = left != 0;
-      left &= left - 1;
-      at[x] = half ? (two ? b : -1) : (one ? a : -1);
-      y[x] = *(const f32x4 *)(from + (size_t)(half ? b : a) * kD);
+        for (int j = 0; j < kLoads; ++j) {
+          // the next two, one a half; behind the last one the first again, without weight
+          const int one = left ? __builtin_ctzll(left) : -1;
+          left &= left - 1;
+          const int two = left ? __builtin_ctzll(left) : -1;
+          left &= left - 1;
+          at[j] = half ? two : one;
+          const float *from = cell(p0 + max(at[j], 0)) + 4 * (l & 31);
+          z[j][0] = *(const f32x2 *)from;
+          z[j][1] = *(const f32x2 *)(from + 2);
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          const float fs = __shfl(f, max(at[j], 0));
+          if (at[j] >= 0) y += (f32x4){z[j][0][0], z[j][0][1], z[j][1][0], z[j][1][1]} * fs;
+        }
+      }
     }
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) {
-      const float fs = __shfl(f, at[x] < 0 ? 0 : at[x]);
-      if (at[x] >= 0) o += y[x] * fs;
-    }
+    for (int j = 0; j < 4; ++j) y[j] += __shfl_xor(y[j], 32);
+    if (half) continue;
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    *(u32x2_a4 *)(A.o + row * kD + 4 * l) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], 32);
-  if (half) return;
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  *(u32x2_a4 *)(A.o + row * kD + 4 * l) = (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 template <int KIND>
 hipError_t attend_shared(const SharedArgs &s, const SharedPlan &p, hipStream_t st) {
-  const int heads = s.a.kv.heads;
-  const uint32_t groups = (uint32_t)((p.many_groups * p.many_cuts + p.many_tiles * p.many_splits) * p.many_parts * heads) +
-                          (uint32_t)((p.few_groups * p.few_cuts + p.few_tiles * p.few_splits) * p.few_parts * heads);
-  hipLaunchKernelGGL(k_attend_shared<KIND>, dim3(groups + 1), dim3(256), 0, st, s, p);
+  const int places = p.ranges + s.a.kv.n * p.few_parts * p.few_splits + p.many_tiles * p.many_parts * p.many_splits;
+  hipLaunchKernelGGL(k_attend_shared<KIND>, dim3((uint32_t)places * (uint32_t)s.a.kv.heads + 1), dim3(256), 0, st, s, p);
+  // eight rows a wave where there are many: most are done, or have few passes
   const int64_t rows = (int64_t)s.a.kv.T * s.a.q_heads;
-  hipLaunchKernelGGL(k_join_shared, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, st, s, p);
+  if (rows > 8192) hipLaunchKernelGGL(k_join_shared<8>, dim3((uint32_t)((rows + 31) / 32)), dim3(256), 0, st, s, p);
+  else hipLaunchKernelGGL(k_join_shared<1>, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, st, s, p);
   return hipGetLastError();
 }
 

@@ -101,11 +101,33 @@ __device__ __forceinline__ int piece_blocks(int blocks, int splits, int least) {
   return max((blocks + splits - 1) / splits, least);
 }
 
-// Page of a block of sequence b; asked for ahead of the block's own loads,
-// which wait for it.
-__device__ __forceinline__ int page_of(const KvArgs &P, int b, int block) {
-  return P.pages[(size_t)b * P.max_pages + (block >> (P.page_shift - 5))];
-}
+// Pages of a wave's blocks: block number i of it is first + i * step, and those
+// behind `last` are the last again.  Lane x has the page of block x of 64, and of
+// the 64 behind them, which are asked for 64 blocks ahead: a page number read by
+// itself, block by block, would be waited for behind the keys and values that
+// are on their way (they arrive in the order of the loads), and so would they.
+struct PagesAhead {
+  const int32_t *row;
+  int first, step, last, shift;
+  int now, next;
+  __device__ __forceinline__ int fetch(int i) const {
+    return row[min(first + (i + (int)(threadIdx.x & 63)) * step, last) >> shift];
+  }
+  __device__ __forceinline__ PagesAhead(const KvArgs &P, int b, int first_, int step_, int last_)
+      : row(P.pages + (size_t)b * P.max_pages), first(first_), step(step_), last(last_), shift(P.page_shift - 5), now(0), next(0) {
+    if (first > last) return;
+    now = fetch(0);
+    next = fetch(64);
+  }
+  // The page of block number i; called for 0, 1, 2 ... in turn.
+  __device__ __forceinline__ int at(int i) {
+    if (i > 0 && (i & 63) == 0) {
+      now = next;
+      next = fetch(i + 64);
+    }
+    return __builtin_amdgcn_readlane(now, i & 63);
+  }
+};
 // The block's memory; NULL on a bad page.
 __device__ __forceinline__ const uint8_t *block_at(const KvArgs &P, int page, int kvh, int block, uint32_t bytes) {
   if (page < 0 || page >= P.num_pages) return nullptr;
@@ -162,11 +184,12 @@ struct FewOut {
   size_t at;
 };
 
-// Blocks lo .. hi of a tile's keys.
-template <int KIND, int WAVES>
-__device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int kvh, int lo, int hi, FewShared<WAVES> &sh, FewOut<WAVES> &out) {
+// Blocks lo .. hi of a tile's keys, by thread tid.  AHEAD: a wave's next block is
+// on its way while it takes one (and has registers of its own).
+template <int KIND, int WAVES, bool AHEAD>
+__device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int tid, int kvh, int lo, int hi, FewShared<WAVES> &sh, FewOut<WAVES> &out) {
   const KvArgs &P = A.kv;
-  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, i16 = l & 15;
+  const int l = tid & 63, g = l >> 4, i16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // column i16 of the products: one (token, head) of the tile
   const int tok = i16 / t.heads, hd = i16 % t.heads;
@@ -189,10 +212,10 @@ __device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int
   // again (which the caches have), on a bad page some block, and its keys are
   // not looked at.
   const int last = lo + w < hi ? lo + w + (hi - 1 - lo - w) / WAVES * WAVES : hi - 1;
-  int page = lo < hi ? page_of(P, t.b, min(lo + w, last)) : 0;
+  PagesAhead pages(P, t.b, lo + w, WAVES, last);
+  int taken = 0;
   auto load = [&](int block, FewIn<KIND> &in) {
-    const uint8_t *blk = block_at(P, page, kvh, min(block, last), KIND == 8 ? kKv8Block : kKv16Block);
-    page = page_of(P, t.b, min(block + WAVES, last));
+    const uint8_t *blk = block_at(P, pages.at(taken++), kvh, min(block, last), KIND == 8 ? kKv8Block : kKv16Block);
     in.good = blk != nullptr;
     if (!blk) blk = P.base;
     constexpr int N = KIND == 8 ? 4 : 8;
@@ -294,19 +317,27 @@ __device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int
   };
 
   if (lo < hi) {
-    FewIn<KIND> even, odd;
-    load(lo + w, even);
-    for (int block = lo + w; block < hi; block += 2 * WAVES) {
-      load(block + WAVES, odd);
-      take(block, even);
-      if (block + WAVES >= hi) break;
-      load(block + 2 * WAVES, even);
-      take(block + WAVES, odd);
+    if (AHEAD) {
+      FewIn<KIND> even, odd;
+      load(lo + w, even);
+      for (int block = lo + w; block < hi; block += 2 * WAVES) {
+        load(block + WAVES, odd);
+        take(block, even);
+        if (block + WAVES >= hi) break;
+        load(block + 2 * WAVES, even);
+        take(block + WAVES, odd);
+      }
+    } else {
+      FewIn<KIND> in;
+      for (int block = lo + w; block < hi; block += WAVES) {
+        load(block, in);
+        take(block, in);
+      }
     }
     if (KIND == 16 && __any(!finite))
       for (int block = lo + w; block < hi; block += WAVES) {
         if ((block + 1) * kBlock <= t.position + 1) continue;
-        const uint8_t *blk = block_at(P, page_of(P, t.b, block), kvh, block, kKv16Block);
+        const uint8_t *blk = block_at(P, P.pages[(size_t)t.b * P.max_pages + (block >> (P.page_shift - 5))], kvh, block, kKv16Block);
         if (blk) add_not_finite(blk, block * kBlock, limit, g, o);
       }
   }
@@ -381,11 +412,15 @@ struct ManyOut {
   bool row[2];
 };
 
-// Blocks lo .. hi of a tile's keys.
-template <int KIND>
-__device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, int kvh, int lo, int hi, ManyShared<KIND> (&sh)[2], ManyOut &out) {
+// Blocks lo .. hi of a tile's keys, by thread tid.  STEPS: the operands are read
+// four at a time, eight on their way while four are used, as they are written
+// here.  Left to itself the compiler does nearly so where it has all registers
+// (4 x 1024 new tokens over 8192: 386 us, in steps 398), and where it has not reads
+// each where it is used, and waits for it (behind shared prefixes 457, in steps 406).
+template <int KIND, bool STEPS>
+__device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, int tid, int kvh, int lo, int hi, ManyShared<KIND> (&sh)[2], ManyOut &out) {
   const KvArgs &P = A.kv;
-  const int tid = threadIdx.x, l = tid & 63, g = l >> 4, i16 = l & 15;
+  const int l = tid & 63, g = l >> 4, i16 = l & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   Frag q[2][4];
   auto &o = out.o;
@@ -419,14 +454,11 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
   const int all_see = t.position + first_tok + 1;
   const int some_see = first_tok < t.tokens ? t.position + last_tok + 1 : 0;
 
-  int page[2] = {0, 0};
-  if (lo < hi)
-    for (int y = 0; y < 2; ++y) page[y] = page_of(P, t.b, min(lo + y, hi - 1));
+  PagesAhead pages(P, t.b, lo, 1, hi - 1);
   auto load = [&](int block, ManyIn<KIND> &in) {
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const uint8_t *blk = block_at(P, page[y], kvh, min(block + y, hi - 1), KIND == 8 ? kKv8Block : kKv16Block);
-      page[y] = page_of(P, t.b, min(block + 2 + y, hi - 1));
+      const uint8_t *blk = block_at(P, pages.at(block + y - lo), kvh, min(block + y, hi - 1), KIND == 8 ? kKv8Block : kKv16Block);
       in.left[y] = block + y < hi && blk ? min(t.keys - (block + y) * kBlock, kBlock) : 0;
       if (!blk && block + y < hi && tid == 0) atomicOr(P.err, kErrPage);
       if (!blk) blk = P.base;
@@ -476,24 +508,39 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
     lds_barrier();
     load(block + 2, in);        // always there: the waits stay exact
     if (block * kBlock >= some_see) continue;
+    const auto here = [] {
+      if (STEPS) __builtin_amdgcn_sched_barrier(0);
+    };
+    // the 32 operands of K and V, four at a time
+    Frag f[2][4];
+    auto read = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[step & 1][i].w = step < 4 ? now.k[i >> 1][4 * (i & 1) + step][l] : now.v[(step - 4) >> 1][4 * (step & 1) + i][l];
+      here();
+    };
     f32x4 s[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = (f32x4){0, 0, 0, 0};
+    here();
+    read(0);
+    read(1);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < 4; ++x) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        Frag k;
-        k.w = now.k[i >> 1][4 * (i & 1) + x][l];
-        s[0][i] = mma(k, q[0][x], s[0][i]);
-        s[1][i] = mma(k, q[1][x], s[1][i]);
+        s[0][i] = mma(f[x & 1][i], q[0][x], s[0][i]);
+        s[1][i] = mma(f[x & 1][i], q[1][x], s[1][i]);
       }
+      here();
+      read(x + 2);
+    }
     if (KIND == 8)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f32x4 f = now.scale[i >> 1][0][4 * (i & 1) + g];
-        s[0][i] *= f;
-        s[1][i] *= f;
+        const f32x4 by = now.scale[i >> 1][0][4 * (i & 1) + g];
+        s[0][i] *= by;
+        s[1][i] *= by;
       }
     const bool masked = left0 < kBlock || left1 < kBlock || (block + 2) * kBlock > all_see;
     if (masked) {
@@ -537,30 +584,33 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
           add[r & 1] += p[r];
         }
         if (KIND == 8) {
-          const f32x4 f = now.scale[i >> 1][1][4 * (i & 1) + g];
+          const f32x4 by = now.scale[i >> 1][1][4 * (i & 1) + g];
           // a masked key's scale is not looked at
 #pragma unroll
-          for (int r = 0; r < 4; ++r) p[r] = masked && s[c][i][r] == kNone ? 0.0f : p[r] * f[r];
+          for (int r = 0; r < 4; ++r) p[r] = masked && s[c][i][r] == kNone ? 0.0f : p[r] * by[r];
         }
         pf[c][i >> 1].u[2 * (i & 1)] = pack_bf16(p[0], p[1]);
         pf[c][i >> 1].u[2 * (i & 1) + 1] = pack_bf16(p[2], p[3]);
       }
       sum[c] += add[0] + add[1];
     }
+    here();
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int x = 0; x < 4; ++x) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        Frag v;
-        v.w = now.v[y][d][l];
-        o[0][d] = mma(v, pf[0][y], o[0][d]);
-        o[1][d] = mma(v, pf[1][y], o[1][d]);
+      for (int i = 0; i < 4; ++i) {
+        const int d = 4 * (x & 1) + i;
+        o[0][d] = mma(f[x & 1][i], pf[0][x >> 1], o[0][d]);
+        o[1][d] = mma(f[x & 1][i], pf[1][x >> 1], o[1][d]);
       }
+      here();
+      if (x < 2) read(x + 6);
+    }
   }
   if (KIND == 16) {
     if (__syncthreads_or(!finite)) {
       for (int block = max(lo, (t.position + 1) / kBlock - 1); block < hi; ++block) {
-        const uint8_t *blk = block_at(P, page_of(P, t.b, block), kvh, block, kKv16Block);
+        const uint8_t *blk = block_at(P, P.pages[(size_t)t.b * P.max_pages + (block >> (P.page_shift - 5))], kvh, block, kKv16Block);
         // a pair of blocks before the rows' first position was not looked at
         if (!blk || (((block - lo) & ~1) + lo + 2) * kBlock <= t.position + 1) continue;
 #pragma unroll

@@ -141,16 +141,16 @@ qdr_status make_shared(const qdr_kv *kv, int32_t n, int32_t T, int32_t groups, i
   QDR_TRY(check_groups(q_heads));
   QDR_TRY(check_groups(n));
   QDR_TRY(check_groups(groups));
+  QDR_TRY(check_groups((int64_t)n * q_heads));
   *plan = qdr::plan_shared(n, T, groups, q_heads, kv->desc.num_heads, max_pages, kv->page_shift);
-  const qdr::SharedPlan &p = *plan;
-  const int64_t few = ((int64_t)p.few_tiles * p.few_splits + (int64_t)p.few_groups * p.few_cuts) * p.few_parts;
-  const int64_t many = ((int64_t)p.many_tiles * p.many_splits + (int64_t)p.many_groups * p.many_cuts) * p.many_parts;
+  QDR_TRY(check_groups(plan->many_tiles));
+  const int64_t few = (int64_t)n * plan->few_parts * plan->few_splits, many = (int64_t)plan->many_tiles * plan->many_parts * plan->many_splits;
   QDR_TRY(check_groups(few));
   QDR_TRY(check_groups(many));
-  QDR_TRY(check_groups((few + many) * heads + 1));
-  const int64_t rows = (int64_t)T * q_heads;
-  QDR_TRY(check_groups((rows + 3) / 4));
-  *bytes = (size_t)rows * p.places * (QDR_DIM + 2) * sizeof(float);
+  QDR_TRY(check_groups((few + many + plan->ranges) * heads + 1));
+  QDR_TRY(check_groups(((int64_t)T + 3) / 4 * heads));
+  QDR_TRY(check_groups((int64_t)T * q_heads / 4));
+  *bytes = plan->floats * sizeof(float);
   return QDR_OK;
 }
 
@@ -167,24 +167,32 @@ SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max
   p.many_heads = std::min(p.group, kManyRows);
   p.many_tokens = kManyRows / p.many_heads;
   p.many_parts = (p.group + p.many_heads - 1) / p.many_heads;
-  // A sequence or group of more than few_tokens takes many-row tiles, ceil(len /
-  // many_tokens) of them from place cu / many_tokens + cu / (few_tokens + 1) on,
-  // where each finds as many places as it needs before the next one's.
-  const int64_t many = T / p.many_tokens + T / (p.few_tokens + 1) + 1;
-  p.few_tiles = n;
-  p.many_tiles = T > p.few_tokens ? (int)many : 0;
-  p.few_groups = groups;
-  p.many_groups = groups && T > p.few_tokens ? (int)many : 0;
-  // Pieces: enough for two workgroups a compute unit.
-  const int64_t blocks = (int64_t)max_pages << (page_shift - 5), most = (blocks + kSharedLeast - 1) / kSharedLeast;
-  auto cut = [&](int64_t units, int64_t places) { return (int)std::max<int64_t>(1, std::min<int64_t>({places / std::max<int64_t>(units, 1), most, 32})); };
-  const int64_t each = (T + (int64_t)n - 1) / n, wide = groups ? (T + (int64_t)groups - 1) / groups : 0;
-  p.few_splits = cut((int64_t)n * heads * p.few_parts, 256);
-  p.many_splits = p.many_tiles ? cut(n * ((each + p.many_tokens - 1) / p.many_tokens) * heads * p.many_parts, 512) : 1;
-  p.few_cuts = groups ? cut((int64_t)groups * heads * p.few_parts, 512) : 0;
-  p.many_cuts = p.many_groups ? cut(groups * ((wide + p.many_tokens - 1) / p.many_tokens) * heads * p.many_parts, 512) : 0;
-  p.shared_places = std::max(p.few_cuts, p.many_cuts);
-  p.places = p.shared_places + std::max(p.few_splits, p.many_splits);
+  // Sequences of more than few_tokens take ceil(len / many_tokens) many-row tiles,
+  // from place cu / many_tokens + b on, or + cu / (few_tokens + 1) where that
+  // makes fewer places: each finds as many as it needs before the next one's.
+  const int64_t by_tokens = T / (p.few_tokens + 1) + 1;
+  p.by_tokens = by_tokens < n;
+  p.many_tiles = T > p.few_tokens ? (int)(T / p.many_tokens + std::min<int64_t>(by_tokens, n)) : 0;
+  // Pieces of sequences' own keys, as in plan_attend: one workgroup of few rows a
+  // compute unit, two of many; none where the tables show few blocks.
+  const int64_t blocks = (int64_t)max_pages << (page_shift - 5), each = ((int64_t)T + n - 1) / n;
+  const int64_t few = (int64_t)n * heads * p.few_parts, many = (each + p.many_tokens - 1) / p.many_tokens * n * heads * p.many_parts;
+  const auto cut = [&](int64_t units, int64_t places, int64_t least) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({places / std::max<int64_t>(units, 1), (blocks + least - 1) / least, 32}));
+  };
+  p.few_splits = cut(few, 256, kSharedLeast);
+  p.many_splits = p.many_tiles && blocks > 24 ? cut(many, 512, kManyLeast) : 1;
+  // The line: two workgroups a compute unit, but no more than there can be work for,
+  // every row a tile of as many blocks as the tables have.
+  const int64_t wide = groups && T > p.few_tokens ? (2 * (T / p.many_tokens) + groups) * (int64_t)p.many_parts : 0;
+  p.ranges = (int)std::min<int64_t>(std::max(1, 512 / heads), ((int64_t)groups * p.few_parts + wide) * (2 + blocks / 4));
+  p.slot_rows = T > p.few_tokens ? kManyRows : kFewRows;
+  const size_t rows = (size_t)T * q_heads;
+  p.cut = groups ? 2 * rows * (QDR_DIM + 2) : 0;
+  p.few_pieces = p.cut + (size_t)p.ranges * heads * 2 * p.slot_rows * (QDR_DIM + 2);
+  p.many_pieces = p.few_pieces + (p.few_splits > 1 ? (size_t)few * p.few_splits * kFewRows * (QDR_DIM + 2) : 0);
+  p.info = p.many_pieces + (p.many_splits > 1 ? (size_t)p.many_tiles * heads * p.many_parts * p.many_splits * kManyRows * (QDR_DIM + 2) : 0);
+  p.floats = p.info + (size_t)T * p.few_parts * 2 * 4;
   return p;
 }
 
@@ -494,7 +502,6 @@ qdr_status qdr_kv_attend_shared(qdr_kv *kv, const int32_t *pages, int32_t max_pa
   s.a.q_heads = q_heads;
   s.a.scale_log2 = scale_log2;
   s.a.part = static_cast<float *>(workspace);
-  s.stats = s.a.part + (size_t)T * q_heads * plan.places * QDR_DIM;
   s.group_cu = group_cu;
   s.shared = shared;
   s.groups = groups;

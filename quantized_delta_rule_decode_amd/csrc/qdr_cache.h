@@ -89,28 +89,37 @@ hipError_t launch_compact(const CompactArgs &, hipStream_t);
 // ---- attention behind shared prefixes (qdr_attend_shared.hip)
 // Rows (tokens x query heads of a key head) go through the keys in the two kinds
 // of tiles of qdr_attend.  The rows of a group, which are consecutive, are dealt
-// to tiles as if they were one sequence's, and go through the shared keys; the
-// rows of each sequence go through its own.  Every pass leaves its rows' maximum,
-// sum and unnormalised result in a place of the workspace, and a last launch
-// joins each row's.
-constexpr int kSharedWaves = 4, kSharedLeast = 8;   // of a few-row tile; fewest blocks of a piece
+// to tiles as if they were one sequence's and go through the shared keys; the
+// rows of each sequence go through its own, a workgroup a tile or a piece of its
+// keys, as there.
+// The groups' tiles of a key head, with what their blocks cost, are laid end to
+// end in a line that is cut into `ranges` equal parts, one a workgroup, which goes
+// through the tiles, or pieces of tiles, of its part: groups of any sizes and
+// prefixes fill the compute units.  A tile that was cut, or whose rows have
+// shared keys too, leaves its rows' maximum, sum and unnormalised result in the
+// workspace, and a last launch joins them.
+constexpr int kSharedWaves = 4, kSharedLeast = 8;   // of a workgroup; fewest blocks of a piece of few rows
 struct SharedPlan {
-  int group;                                   // query heads a key head
+  int group;                                 // query heads a key head
   int few_heads, few_tokens, few_parts;
   int many_heads, many_tokens, many_parts;
-  int few_tiles, many_tiles;                   // of sequences (few: one each)
-  int few_groups, many_groups;                 // of groups
-  int few_splits, many_splits;                 // pieces of a sequence's own keys
-  int few_cuts, many_cuts;                     // pieces of the shared keys
-  int shared_places, places;                   // of a row: of shared keys first, then its own
+  int few_splits, many_splits;               // pieces of the keys of sequences' tiles
+  int many_tiles;                            // places of many-row tiles of sequences
+  bool by_tokens;                            // a sequence's place goes by the tokens before it, not by the sequences
+  int ranges;                                // parts of the line, at most; 0: no groups
+  int slot_rows;                             // rows of a piece of a cut tile of the line: 16 where no tile has more
+  // places in the workspace, in floats: whole tiles' results by row, of shared
+  // and own keys ([T * q_heads][130] each); the line's cut tiles' by workgroup
+  // (two each: of its first tile and its last, [slot_rows][130]); few and many
+  // rows' by piece ([16] and [128][130]); each token's passes
+  size_t cut, few_pieces, many_pieces, info, floats;
 };
 SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max_pages, int page_shift);
 
 struct SharedArgs {
-  AttendArgs a;          // part: [T * q_heads][places][128]
+  AttendArgs a;          // part: the workspace
   const int32_t *group_cu, *shared;
   int32_t groups;
-  float *stats;          // [T * q_heads][places][2]: maximum, sum
 };
 hipError_t launch_attend_shared(const SharedArgs &, const SharedPlan &, int kind, hipStream_t);
 

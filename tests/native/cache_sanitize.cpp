@@ -361,16 +361,20 @@ static int attend() {
             void *ws = (void *)((uintptr_t)space & ~(uintptr_t)15);
             CHECK(call(i, i, g, h, x, 1.0f, x, ws, need, n, T, m) == QDR_OK);
             const qdr::SharedPlan &p = shared_plan;
-            CHECK(p.places >= 1 && p.places <= 64 && p.shared_places >= p.few_cuts && p.shared_places >= p.many_cuts && p.places - p.shared_places >= p.few_splits &&
-                  p.places - p.shared_places >= p.many_splits && p.few_splits >= 1 && p.many_splits >= 1);
-            CHECK(g == 0 || (p.few_cuts >= 1 && (p.many_groups == 0 || p.many_cuts >= 1)));
-            CHECK(need == (size_t)T * h * p.places * 130 * 4 && (char *)shared_args.stats == (char *)ws + (size_t)T * h * p.places * 512);
+            const size_t rows = (size_t)T * h;
+            CHECK((p.ranges >= 1) == (g > 0) && p.ranges * 2 <= 512 && p.few_splits >= 1 && p.few_splits <= 32 && p.many_splits >= 1 && p.many_splits <= 32);
+            CHECK(p.slot_rows == 128 || (p.slot_rows == 16 && T <= p.few_tokens));
+            CHECK(p.cut == (g ? 2 * rows * 130 : 0) && p.few_pieces == p.cut + (size_t)p.ranges * 2 * 2 * p.slot_rows * 130 && p.floats == p.info + (size_t)T * p.few_parts * 8);
+            CHECK(p.many_pieces == p.few_pieces + (p.few_splits > 1 ? (size_t)n * 2 * p.few_parts * p.few_splits * 16 * 130 : 0));
+            CHECK(p.info == p.many_pieces + (p.many_splits > 1 ? (size_t)p.many_tiles * 2 * p.many_parts * p.many_splits * 128 * 130 : 0));
+            CHECK((p.many_tiles > 0) == (T > p.few_tokens));
+            CHECK(need == p.floats * 4 && p.info % 4 == 0 && shared_args.a.part == ws);
             CHECK(p.few_heads * p.few_parts >= p.group && p.many_heads * p.many_parts >= p.group && p.few_heads * p.few_tokens <= 16 && p.many_heads * p.many_tokens <= 128);
-            CHECK(p.few_tiles == n && (T <= p.few_tokens) == (p.many_tiles == 0));
+            CHECK(p.many_parts <= p.few_parts && p.many_tokens >= p.few_tokens);
           }
   CHECK(qdr_kv_attend_shared_workspace(&kv, 0, 5, 1, 2, 9, &need) == QDR_OK && need == 0);
   CHECK(call(nullptr, nullptr, 1, 2, x, 1.0f, x, nullptr, 0, 0, 5) == QDR_OK && call(nullptr, nullptr, 1, 2, x, 1.0f, x, nullptr, 0, 5, 0) == QDR_OK);
-  CHECK(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 4, 9, &need) == QDR_OK && need <= sizeof mem);
+  CHECK(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 4, 9, &need) == QDR_OK && need > 0);
   CHECK(call(i, i, 1, 4, x, 1.0f, x, mem, need) == QDR_OK && call(nullptr, nullptr, 0, 4, x, 1.0f, x, mem, need) == QDR_OK);
   REFUSED(qdr_kv_attend_shared_workspace(nullptr, 2, 5, 1, 4, 9, &need), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 4, 9, nullptr), QDR_E_INVAL);
@@ -378,9 +382,8 @@ static int attend() {
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 4, -9, &need), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 3, 9, &need), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 1 << 27, 1, 2, 9, &need), QDR_E_INVAL);      // launch too large
-  REFUSED(qdr_kv_attend_shared_workspace(&kv, 1 << 23, 5, 1, 2, 9, &need), QDR_E_INVAL);
+  REFUSED(qdr_kv_attend_shared_workspace(&kv, 1 << 24, 5, 1, 2, 9, &need), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1 << 24, 2, 9, &need), QDR_E_INVAL);
-  REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1 << 23, 2, 9, &need), QDR_E_INVAL);
   REFUSED(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 1 << 25, 9, &need), QDR_E_INVAL);
   CHECK(qdr_kv_attend_shared_workspace(&kv, 2, 5, 1, 4, 9, &need) == QDR_OK);
   REFUSED(qdr_kv_attend_shared(nullptr, i, 9, i, i, 2, 5, i, i, 1, 4, x, 1.0f, x, mem, need, nullptr), QDR_E_INVAL);

@@ -159,16 +159,19 @@ def test_attend_shared_bad_counts(torch_dev):
     good = s.run(torch)
     s.check(torch, good)
     first, second = slice(s.lead, s.lead + 4), slice(s.lead + 4, s.lead + 25)
+    # (where keys are cut follows from every length, so the others may round differently)
+    ref, room = reference(torch, s.q[s.rows], s.k, s.v, s.lens, s.contexts, 0.11)
+    fits = lambda o, rows: ((o[rows].double() - ref[rows.start - s.lead:rows.stop - s.lead]).abs() <= room[rows.start - s.lead:rows.stop - s.lead]).all()
     for shared in ([-1, 100], [67, 100], [2 ** 31 - 1, 100], [32 * 100, 100]):
         s.args[4] = i32(torch, shared)
         o = s.run(torch)
         assert s.cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH
-        assert (o[first] == 0).all() and torch.equal(o[second], good[second])
+        assert (o[first] == 0).all() and fits(o, second)
     # only the first has that many older tokens
     s.args[4] = i32(torch, [66, 100])
     o = s.run(torch)
     assert s.cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH
-    assert (o[s.lead + 1:s.lead + 4] == 0).all() and torch.equal(o[second], good[second]) and (o[s.lead] != 0).any()
+    assert (o[s.lead + 1:s.lead + 4] == 0).all() and fits(o, second) and (o[s.lead] != 0).any()
     s.args[4] = i32(torch, [64, 100])
     for at, ctx in ((0, -1), (0, 10 ** 6), (4, 19), (4, 2 ** 31 - 1)):
         context = list(s.contexts)
@@ -177,9 +180,9 @@ def test_attend_shared_bad_counts(torch_dev):
         o = s.run(torch)
         assert s.cache.qdr_kv_poll_device_error() == qdr.DEVERR_LENGTH
         if at == 0:
-            assert (o[first] == 0).all() and torch.equal(o[second], good[second])
+            assert (o[first] == 0).all() and fits(o, second)
         else:
-            assert (o[s.lead + 5:s.lead + 25] == 0).all() and torch.equal(o[first], good[first])
+            assert (o[s.lead + 5:s.lead + 25] == 0).all() and fits(o, first)
     s.args[2] = i32(torch, s.contexts)
     # pairs out of order or range: nothing outside the rows is touched
     for bad in ([0, 5, 3], [-1, 3, 5], [0, 3, 6], [3, 0, 5], [0, -2 ** 31, 5], [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]):
