@@ -115,16 +115,17 @@ qdr_status check_apart(const Span *in, int ins, const Span *out, int outs) {
 
 // Parts of an assignment's workspace, in bytes.
 struct AssignSpace {
-  size_t pages, counts, rows;   // of [num_pages], [tiles] and [m]
+  size_t pages, counts, rows;   // of [num_pages], [tiles] and [m][8]
   size_t total() const { return 3 * pages + counts + rows; }
 };
 AssignSpace assign_space(const qdr_kv *kv, int32_t m) {
-  return {up((size_t)kv->desc.num_pages * 4), up((size_t)qdr::book_tiles(kv->desc.num_pages) * 4), up((size_t)m * 4)};
+  return {up((size_t)kv->desc.num_pages * 4), up((size_t)qdr::book_tiles(kv->desc.num_pages) * 4), up((size_t)m * 32)};
 }
 struct CompactSpace {
   size_t pages, counts, moves;
   size_t total() const { return 2 * pages + counts + moves; }
 };
+constexpr int kMoveGroups = 2048;   // workgroups of all moves: eight on each compute unit
 CompactSpace compact_space(const qdr_kv *kv) {
   return {up((size_t)kv->desc.num_pages * 4), up((size_t)qdr::book_tiles(kv->desc.num_pages) * 4), 256};
 }
@@ -442,7 +443,7 @@ qdr_status qdr_kv_compact(qdr_kv *kv, const int32_t *refs, const int32_t *pages,
   QDR_TRY(check_device(kv->device));
   const Span in[] = {{refs, total}, {pages, entries}}, out[] = {{moved, total}, {new_refs, total}, {new_pages, entries}};
   QDR_TRY(check_apart(in, 2, out, 3));
-  QDR_TRY(check_groups(entries / 256 + 1));
+  QDR_TRY(check_groups(entries / 256 + 1 + kMoveGroups));
   const CompactSpace space = compact_space(kv);
   QDR_TRY(check_workspace(workspace, workspace_bytes, space.total()));
   char *ws = static_cast<char *>(workspace);
@@ -461,7 +462,7 @@ qdr_status qdr_kv_compact(qdr_kv *kv, const int32_t *refs, const int32_t *pages,
   a.counts = reinterpret_cast<int32_t *>(ws + 2 * space.pages);
   a.moves = reinterpret_cast<int32_t *>(ws + 2 * space.pages + space.counts);
   a.parts = parts_of(a.page_bytes);
-  a.groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(2048, total / 2 * a.parts));
+  a.groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kMoveGroups, total / 2 * a.parts));
   return launched(qdr::launch_compact(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -66,7 +66,8 @@ struct AssignArgs {
   int32_t *first;                // [num_pages] first row that keeps the page in part
   int32_t *free;                 // [num_pages] the free pages, lowest first
   int32_t *counts;               // [tiles] free pages of a tile of pages
-  int32_t *offset;               // [m] the row's first place in `free`; -1: an empty row
+  int32_t *offset;               // [m][8] the row's first place in `free` (-1: an empty row), its tokens, the kept
+                                 // ones, the page behind its full ones (-1: none), and whether that one stays its own
   int32_t parts;                 // workgroups that copy a row's last page
 };
 hipError_t launch_assign(const AssignArgs &, hipStream_t);
@@ -80,8 +81,8 @@ struct CompactArgs {
   int32_t *moved, *new_refs, *new_pages;
   // workspace
   int32_t *counts;               // [tiles] free pages of a tile of pages
-  int32_t *src, *dst;            // [num_pages] each: pages that move, by the used pages before them, and where to
-  int32_t *moves;                // [2] how many, and where src begins
+  int32_t *src, *dst;            // [num_pages] each: pages that move, by the used pages before them, and where to; dst[p] of a page that moves: its place in src
+  int32_t *moves;                // [3] how many, where src begins, and the number of used pages
   int32_t parts, groups;         // workgroups of a move; of all moves
 };
 hipError_t launch_compact(const CompactArgs &, hipStream_t);
