@@ -59,7 +59,7 @@ __device__ __forceinline__ Share share_of(const SharedArgs &S, const SharedPlan 
   r.first = c0;
   r.len = r.bad || none ? 0 : ce - c0;
   // sequences that fill tiles by themselves gain nothing, and would leave partial results
-  const bool together = r.end - r.begin >= 2 && r.len < (int64_t)(r.end - r.begin) * plan.many_tokens;
+  const bool together = plan.ranges > 0 && r.end - r.begin >= 2 && r.len < (int64_t)(r.end - r.begin) * plan.many_tokens;
   r.blocks = r.len > 0 && together ? tokens / kBlock : 0;
   return r;
 }
@@ -100,19 +100,25 @@ struct Item {
   int position;        // of row 0; kMostContext: every row sees every key
   int begin, blocks;   // blocks of keys: a sequence's own begin there; a group's
   int flags;
+  int members;         // a group's sequences
 };
 constexpr int kFew = 1, kPrefix = 2, kSkipped = 4, kPooled = 8;   // kPooled: its rows have shared keys too
 
-// What a tile and each of its blocks cost, in 0.1 us of a workgroup (two a
-// compute unit): 128 rows and 32 keys are bound by issue, few rows by memory.
-constexpr int kTileCost = 60, kLeastCost = 100, kHalfCost = 400;   // (the last two of a workgroup)
+// What a workgroup, a tile and each of its blocks cost, in 0.1 us.
+constexpr int kGroupCost = 60, kTileCost = 60, kLeastCost = 100;   // (the last: least of a part)
 template <int KIND>
-__device__ __forceinline__ double block_cost(int flags) { return flags & kFew ? (KIND == 8 ? 8.0 : 14.0) : 8.0; }
+__device__ __forceinline__ double block_cost(int flags) { return flags & kFew ? (KIND == 8 ? 8.0 : 14.0) : 13.0; }
 template <int KIND>
 __device__ __forceinline__ double tile_cost(int flags, int blocks) { return kTileCost + blocks * block_cost<KIND>(flags); }
+// What `blocks` of keys of a sequence of `len` tokens' own cost a key head.
+template <int KIND>
+__device__ __forceinline__ double own_cost(const SharedPlan &plan, double len, double blocks) {
+  const bool few = len <= plan.few_tokens;
+  return few ? plan.few_parts * blocks * (KIND == 8 ? 4.0 : 7.0) : ceil(len * plan.many_inverse) * plan.many_parts * blocks * block_cost<KIND>(0);
+}
 
 __device__ __forceinline__ Item item_of_group(const SharedArgs &S, const SharedPlan &plan, int i) {
-  Item t{0, 0, 0, 0, 0, 0, 0, 0, 0};
+  Item t{};
   if (i >= S.groups) return t;
   const Share share = share_of(S, plan, S.group_cu[i], S.group_cu[i + 1], S.shared[i]);
   t.b = share.begin;
@@ -120,6 +126,7 @@ __device__ __forceinline__ Item item_of_group(const SharedArgs &S, const SharedP
   t.len = share.blocks ? share.len : 0;
   t.position = kMostContext;
   t.blocks = share.blocks;
+  t.members = share.end - share.begin;
   const bool few = t.len <= plan.few_tokens;
   t.flags = kPrefix | (few ? kFew : 0);
   t.tiles = t.len == 0 ? 0 : few ? plan.few_parts : (t.len + plan.many_tokens - 1) / plan.many_tokens * plan.many_parts;
@@ -128,7 +135,7 @@ __device__ __forceinline__ Item item_of_group(const SharedArgs &S, const SharedP
 
 __device__ __forceinline__ Item item_of_sequence(const SharedArgs &S, const SharedPlan &plan, int b) {
   const KvArgs &P = S.a.kv;
-  Item t{0, 0, 0, 0, 0, 0, 0, 0, 0};
+  Item t{};
   const int s = P.cu[b], e = P.cu[b + 1], ctx = P.context[b];
   Share share{false, 0, 0, 0, 0, 0, 0};
   if (S.groups > 0) {
@@ -158,16 +165,17 @@ constexpr int kDone = 16, kPieces = 128;
 // The line of the groups' work, cut into ranges of `step` (rounded down to whole costs,
 // the same everywhere).
 struct Line {
-  double total, step, inverse;
+  double total, own, step, inverse;   // own: the cost of sequences' own keys
   int ranges, range;       // of the workgroup
   double a, b;             // its part
 };
-// Parts: of kLeastCost at least; half as many as there are places for (one
-// workgroup a compute unit, which leaves half the partial results) where they
-// then are no longer than kHalfCost.
-__device__ __forceinline__ int ranges_of(int most, double total) {
-  const double half = fmin((double)((most + 1) / 2), ceil(total * (1.0 / kLeastCost)));
-  return (int)fmin((double)most, fmax(half, ceil(total * (1.0 / kHalfCost))));
+// Parts of a line of length C, while the sequences' workgroups (A in all) have
+// the other of M places: both end at once where (G + C / x) (M - x) = A with G a
+// workgroup's cost, and no part is shorter than kLeastCost.
+__device__ __forceinline__ int ranges_of(int most, double total, double own) {
+  const double b = 0.5 * (own + total - (double)kGroupCost * most);
+  const double x = (sqrt(b * b + (double)kGroupCost * most * total) - b) * (1.0 / kGroupCost);
+  return (int)fmax(fmin(fmin((double)most, ceil(x)), ceil(total * (1.0 / kLeastCost))), 1.0);
 }
 __device__ __forceinline__ double range_begin(const Line &line, int r) { return r < line.ranges ? floor(r * line.step) : line.total; }
 __device__ __forceinline__ int range_at(const Line &line, double x) {
@@ -182,7 +190,7 @@ struct Job {
   Tile t;
   int lo, hi;
   int flags;               // of the item; kAlone: the rows' only pass; kCut: one of several over the tile
-  float *whole, *cell;     // results by row, and of the workgroup's cut tile
+  size_t whole, cell;      // places in the workspace: results by row, and of the workgroup's cut tile
   Passes *info, passes;    // of the tile's first token, and what to write there (NULL: another workgroup does)
   int info_step;
 };
@@ -195,7 +203,8 @@ struct Scratch {
     FewShared<kSharedWaves> few;
   };
   Item items[kItems];
-  double sums[4];
+  double sums[4][2];
+  int2 at;                 // item and tile where the part begins in it
   double base;             // where this chunk of items begins in the line
   SharedArgs args;
   SharedPlan plan;
@@ -203,22 +212,28 @@ struct Scratch {
   Job job;
 };
 
-// Sum over the threads before this one, of 256; *all: over every thread.
-__device__ __forceinline__ double sum_before(double x, double *lds, double *all) {
+// Sum of x over the threads before this one, of 256; *all and *all_y: of x and y
+// over every thread.
+__device__ __forceinline__ double sum_before(double x, double y, double (*lds)[2], double *all, double *all_y) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   double s = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(s, d);
-    if (lane >= d) s += y;
+    const double before = __shfl_up(s, d);
+    if (lane >= d) s += before;
+    y += __shfl_xor(y, d);
   }
   __syncthreads();
-  if (lane == 63) lds[w] = s;
+  if (lane == 63) {
+    lds[w][0] = s;
+    lds[w][1] = y;
+  }
   __syncthreads();
   double before = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) before += i < w ? lds[i] : 0.0;
-  *all = lds[0] + lds[1] + lds[2] + lds[3];
+  for (int i = 0; i < 4; ++i) before += i < w ? lds[i][0] : 0.0;
+  *all = lds[0][0] + lds[1][0] + lds[2][0] + lds[3][0];
+  *all_y = lds[0][1] + lds[1][1] + lds[2][1] + lds[3][1];
   return before + s - x;
 }
 
@@ -252,8 +267,8 @@ __device__ __forceinline__ void make_job(const SharedArgs &S, const SharedPlan &
   job.lo = r0 == line.range ? 0 : cut(line.a);
   job.hi = r1 == line.range ? blocks : cut(line.b);
   job.flags = flags | (r0 == r1 ? 0 : kCut);
-  job.whole = S.a.part;
-  job.cell = S.a.part + plan.cut + (size_t)((line.range * P.heads + kvh) * 2 + (r0 == line.range)) * plan.slot_rows * kCell;
+  job.whole = 0;
+  job.cell = plan.cut + (size_t)((line.range * P.heads + kvh) * 2 + (r0 == line.range)) * plan.slot_rows * kCell;
   // each token's passes are written down once
   Passes *info = (Passes *)(S.a.part + plan.info);
   job.info = kvh == 0 && line.range == r0 ? info + (size_t)(t.first + t.token) * plan.few_parts + part : nullptr;
@@ -286,13 +301,47 @@ __device__ __forceinline__ bool make_piece(const SharedArgs &S, const SharedPlan
   job.lo = it.begin + split * each;
   job.hi = min(job.lo + each, it.begin + blocks);
   job.flags = it.flags | (alone ? kAlone : 0) | (pieces == 1 ? 0 : kCut);
-  job.whole = S.a.part + plan.cut / 2;
-  job.cell = S.a.part + (few ? plan.few_pieces : plan.many_pieces) + ((((size_t)tile * P.heads + kvh) * parts + part) * splits + split) * ((few ? kFewRows : kManyRows) * kCell);
+  job.whole = plan.cut / 2;
+  job.cell = (few ? plan.few_pieces : plan.many_pieces) + ((((size_t)tile * P.heads + kvh) * parts + part) * splits + split) * ((few ? kFewRows : kManyRows) * kCell);
   Passes *info = (Passes *)(S.a.part + plan.info) + (size_t)P.T * plan.few_parts;
   job.info = kvh == 0 && split == 0 ? info + (size_t)(t.first + token) * plan.few_parts + part : nullptr;
   job.passes = {pieces == 1 ? 0 : tile, pieces - 1, 0, (it.flags & (kFew | kPooled)) | (alone ? kDone : 0) | (pieces == 1 ? 0 : kPieces)};
   job.info_step = plan.few_parts;
   return true;
+}
+
+// Where a pass leaves its rows, read from the job when its tile is done.
+struct Results {
+  uint16_t *o;
+  float *part;         // by row, or by the tile's rows
+  int flags;
+  bool keys;
+  __device__ __forceinline__ float *place(size_t at, int row) const { return part + (flags & kCut ? (size_t)row : at / kD) * kCell; }
+  // channels c .. c + 3 of a row
+  __device__ __forceinline__ void put(size_t at, int row, int c, f32x4 y, float sum) const {
+    if (flags & kAlone) {
+      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      *(u32x2_a4 *)(o + at + c) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+    } else if (keys) {
+      float *to = place(at, row) + c;
+      *(f32x2 *)to = (f32x2){y[0], y[1]};
+      *(f32x2 *)(to + 2) = (f32x2){y[2], y[3]};
+    }
+  }
+  __device__ __forceinline__ void note(size_t at, int row, float m, float sum) const {
+    if (!(flags & kAlone)) *(f32x2 *)(place(at, row) + kD) = (f32x2){m, sum};
+  }
+};
+__device__ __forceinline__ Results results_of(const AttendArgs &A, const Job &job) {
+  asm volatile("" ::: "memory");       // not before the tile, which has no registers for it
+  Results r;
+  r.o = A.o;
+  r.flags = scalar(job.flags);
+  r.keys = scalar(job.lo) < scalar(job.hi);
+  // (from the kernel's argument: the compiler knows that as global memory)
+  const size_t at = r.flags & kCut ? job.cell : job.whole;
+  r.part = A.part + ((size_t)(uint32_t)scalar((int)(at >> 32)) << 32 | (uint32_t)scalar((int)at));
+  return r;
 }
 
 template <int KIND>
@@ -317,39 +366,25 @@ __device__ __forceinline__ void pass(const AttendArgs &A, int kvh, Scratch<KIND>
     p.row = tid * t.heads;
     sh.job.info[(size_t)tid * sh.job.info_step] = p;
   }
-  const volatile Job &job = sh.job;
-  auto place = [&](size_t at, int row) { return job.flags & kCut ? job.cell + (size_t)row * kCell : job.whole + at / kD * kCell; };
-  // channels c .. c + 3 of a row
-  auto put = [&](size_t at, int row, int c, f32x4 y, float sum) {
-    if (job.flags & kAlone) {
-      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-      *(u32x2_a4 *)(A.o + at + c) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
-    } else if (job.lo < job.hi) {
-      float *to = place(at, row) + c;
-      *(f32x2 *)to = (f32x2){y[0], y[1]};
-      *(f32x2 *)(to + 2) = (f32x2){y[2], y[3]};
-    }
-  };
-  auto note = [&](size_t at, int row, float m, float sum) {
-    if (!(job.flags & kAlone)) *(f32x2 *)(place(at, row) + kD) = (f32x2){m, sum};
-  };
   if (scalar(sh.job.flags) & kFew) {
     FewOut<kSharedWaves> out;
     few_tile<KIND, kSharedWaves, KIND == 8>(A, t, tid, kvh, lo, hi, sh.few, out);
+    const Results to = results_of(A, sh.job);
     if (!out.row) return;
 #pragma unroll
-    for (int y = 0; y < 8 / kSharedWaves; ++y) put(out.at, l & 15, 16 * (8 / kSharedWaves * w + y) + 4 * g, out.o[y], out.sum);
-    if (w == 0 && g == 0) note(out.at, l & 15, out.m, out.sum);
+    for (int y = 0; y < 8 / kSharedWaves; ++y) to.put(out.at, l & 15, 16 * (8 / kSharedWaves * w + y) + 4 * g, out.o[y], out.sum);
+    if (w == 0 && g == 0) to.note(out.at, l & 15, out.m, out.sum);
   } else {
     ManyOut out;
     many_tile<KIND, true>(A, t, tid, kvh, lo, hi, sh.many, out);
+    const Results to = results_of(A, sh.job);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       if (!out.row[c]) continue;
       const int row = 32 * w + 16 * c + (l & 15);
 #pragma unroll
-      for (int d = 0; d < 8; ++d) put(out.at[c], row, 16 * d + 4 * g, out.o[c][d], out.sum[c]);
-      if (g == 0) note(out.at[c], row, out.m[c], out.sum[c]);
+      for (int d = 0; d < 8; ++d) to.put(out.at[c], row, 16 * d + 4 * g, out.o[c][d], out.sum[c]);
+      if (g == 0) to.note(out.at[c], row, out.m[c], out.sum[c]);
     }
   }
 }
@@ -396,7 +431,7 @@ __global__ void __launch_bounds__(256, 2) k_attend_shared(SharedArgs S, SharedPl
     sh.args = S;
     sh.plan = plan;
     sh.base = 0;
-    sh.line.total = 0;
+    sh.line.total = sh.line.own = 0;
   }
   __syncthreads();
   // Every workgroup of the line makes it by itself, 256 groups at a time: once
@@ -410,15 +445,24 @@ __global__ void __launch_bounds__(256, 2) k_attend_shared(SharedArgs S, SharedPl
     double all = 0;
     bool here = true;
     if (line_part) {
+      double own = 0, all_own = 0;
+      if (c == 0)
+        for (int b = tid; b < sh.args.a.kv.n; b += 256) {
+          const KvArgs &P = sh.args.a.kv;
+          const int len = min(max(P.cu[b + 1] - P.cu[b], 0), P.T), ctx = min(max(P.context[b], 0), room_of(P));
+          own += len == 0 ? 0.0 : kGroupCost + own_cost<KIND>(sh.plan, len, ctx >> 5);
+        }
       Item mine = item_of_group(sh.args, sh.plan, (c < chunks ? c : c - chunks) * kItems + tid);
-      const double before = sum_before(mine.tiles * tile_cost<KIND>(mine.flags, mine.blocks), sh.sums, &all);
+      if (c < chunks && mine.tiles > 0) own -= mine.members * own_cost<KIND>(sh.plan, (double)mine.len / mine.members, mine.blocks);
+      const double before = sum_before(mine.tiles * tile_cost<KIND>(mine.flags, mine.blocks), own, sh.sums, &all, &all_own);
       if (c < chunks) {
         if (tid == 0) {
           Line line = sh.line;
           line.total += all;
+          line.own += all_own;
           if (c + 1 == chunks) {
             const int range = blockIdx.x / sh.args.a.kv.heads;
-            line.ranges = ranges_of(sh.plan.ranges, line.total);
+            line.ranges = ranges_of(sh.plan.ranges, line.total, line.own);
             line.step = line.total / line.ranges;
             line.inverse = line.ranges / line.total;
             line.range = range;
@@ -434,19 +478,21 @@ __global__ void __launch_bounds__(256, 2) k_attend_shared(SharedArgs S, SharedPl
       }
       here = sh.base + all > sh.line.a;
       if (here) {
+        // the first group that ends behind the part's beginning, and from there on
+        const double into = sh.line.a - (sh.base + before), each = tile_cost<KIND>(mine.flags, mine.blocks);
         mine.start = sh.base + before;
         sh.items[tid] = mine;
-        __syncthreads();
-        // the first group that ends behind the part's beginning, and from there on
-#pragma unroll 1
-        for (int step = kItems / 2; step > 0; step >>= 1)
-          if (sh.items[x + step].start <= sh.line.a) x += step;
-        if (sh.items[x].start < sh.line.a) {
-          const double each = tile_cost<KIND>(sh.items[x].flags, sh.items[x].blocks), into = sh.line.a - sh.items[x].start;
+        if (into >= 0 && into < mine.tiles * each) {
           k = (int)(into / each);
           if (k * each > into) --k;
           if ((k + 1) * each <= into) ++k;
+          sh.at = make_int2(tid, k);
+        } else if (tid == 0 && into < 0) {
+          sh.at = make_int2(0, 0);
         }
+        __syncthreads();
+        x = sh.at.x;
+        k = sh.at.y;
         x = scalar(x);
         k = scalar(k);
       }
@@ -490,10 +536,12 @@ __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan pl
   for (int i = 0; i < OWN; ++i) {
     const int64_t row = ((int64_t)blockIdx.x * 4 + scalar((int)threadIdx.x >> 6)) * OWN + i;
     const int64_t token = row / A.q_heads;
-    if (token < begin || token >= end) continue;
+    if (token >= P.T) continue;
     const int head = (int)(row - token * A.q_heads), kvh = head / plan.group, h = head - kvh * plan.group;
     const Passes *shared = (const Passes *)(A.part + plan.info) + token * plan.few_parts, *own = shared + (size_t)P.T * plan.few_parts;
-    Passes o = own[0], s{0, -1, 0, 0};
+    // (all that is read before the cells, at once)
+    Passes o = own[0], first = shared[0], s{0, -1, 0, 0};
+    if (token < begin || token >= end) continue;
     if (o.flags & kDone && plan.few_parts == 1) {
       if (OWN > 1) i += min((int64_t)(OWN - 1 - i), (int64_t)A.q_heads - 1 - head);   // and the token's other rows are
       continue;
@@ -506,7 +554,7 @@ __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan pl
       p.row += h - part * heads;
     };
     if (o.flags & kPooled) {
-      s = shared[0];
+      s = first;
       at_part(shared, s);
     }
     at_part(own, o);
@@ -577,6 +625,7 @@ template <int KIND>
 hipError_t attend_shared(const SharedArgs &s, const SharedPlan &p, hipStream_t st) {
   const int places = p.ranges + s.a.kv.n * p.few_parts * p.few_splits + p.many_tiles * p.many_parts * p.many_splits;
   hipLaunchKernelGGL(k_attend_shared<KIND>, dim3((uint32_t)places * (uint32_t)s.a.kv.heads + 1), dim3(256), 0, st, s, p);
+  if (p.ranges == 0 && p.few_splits == 1 && p.many_splits == 1) return hipGetLastError();   // nothing to join
   // eight rows a wave where there are many: most are done, or have few passes
   const int64_t rows = (int64_t)s.a.kv.T * s.a.q_heads;
   if (rows > 8192) hipLaunchKernelGGL(k_join_shared<8>, dim3((uint32_t)((rows + 31) / 32)), dim3(256), 0, st, s, p);

@@ -167,6 +167,7 @@ SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max
   p.few_parts = (p.group + p.few_heads - 1) / p.few_heads;
   p.many_heads = std::min(p.group, kManyRows);
   p.many_tokens = kManyRows / p.many_heads;
+  p.many_inverse = 1.0f / p.many_tokens;
   p.many_parts = (p.group + p.many_heads - 1) / p.many_heads;
   // Sequences of more than few_tokens take ceil(len / many_tokens) many-row tiles,
   // from place cu / many_tokens + b on, or + cu / (few_tokens + 1) where that
@@ -183,13 +184,20 @@ SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max
   };
   p.few_splits = cut(few, 256, kSharedLeast);
   p.many_splits = p.many_tiles && blocks > 24 ? cut(many, 512, kManyLeast) : 1;
+  // Groups' rows go through shared keys together where that can save reading
+  // kLeastSaved blocks of a key head: the line and the join of its results cost
+  // some 10 us.  Measured per call (us, together / each by itself), 8-bit, 8 key
+  // heads, one group of 700 tokens a sequence behind 16384: 2 sequences (4096
+  // blocks less) 27.9 / 22.2, 4 (12288) 28.5 / 30.1, 8 40.4 / 46.2, 64 66.6 / 233;
+  // behind 8192: 8 31.3 / 31.4; behind 2048: 8 24.9 / 17.1.
+  const bool together = groups && (int64_t)std::max(n - groups, 0) * heads * blocks >= kLeastSaved;
   // The line: two workgroups a compute unit, but no more than there can be work for,
   // every row a tile of as many blocks as the tables have.
-  const int64_t wide = groups && T > p.few_tokens ? (2 * (T / p.many_tokens) + groups) * (int64_t)p.many_parts : 0;
-  p.ranges = (int)std::min<int64_t>(std::max(1, 512 / heads), ((int64_t)groups * p.few_parts + wide) * (2 + blocks / 4));
+  const int64_t wide = T > p.few_tokens ? (2 * (T / p.many_tokens) + groups) * (int64_t)p.many_parts : 0;
+  p.ranges = !together ? 0 : (int)std::min<int64_t>(std::max(1, 512 / heads), ((int64_t)groups * p.few_parts + wide) * (2 + blocks / 4));
   p.slot_rows = T > p.few_tokens ? kManyRows : kFewRows;
   const size_t rows = (size_t)T * q_heads;
-  p.cut = groups ? 2 * rows * (QDR_DIM + 2) : 0;
+  p.cut = together ? 2 * rows * (QDR_DIM + 2) : 0;
   p.few_pieces = p.cut + (size_t)p.ranges * heads * 2 * p.slot_rows * (QDR_DIM + 2);
   p.many_pieces = p.few_pieces + (p.few_splits > 1 ? (size_t)few * p.few_splits * kFewRows * (QDR_DIM + 2) : 0);
   p.info = p.many_pieces + (p.many_splits > 1 ? (size_t)p.many_tiles * heads * p.many_parts * p.many_splits * kManyRows * (QDR_DIM + 2) : 0);

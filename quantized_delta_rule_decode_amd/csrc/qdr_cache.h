@@ -100,14 +100,16 @@ hipError_t launch_compact(const CompactArgs &, hipStream_t);
 // shared keys too, leaves its rows' maximum, sum and unnormalised result in the
 // workspace, and a last launch joins them.
 constexpr int kSharedWaves = 4, kSharedLeast = 8;   // of a workgroup; fewest blocks of a piece of few rows
+constexpr int kLeastSaved = 12288;                  // blocks of a key head
 struct SharedPlan {
   int group;                                 // query heads a key head
   int few_heads, few_tokens, few_parts;
   int many_heads, many_tokens, many_parts;
+  float many_inverse;                        // 1 / many_tokens
   int few_splits, many_splits;               // pieces of the keys of sequences' tiles
   int many_tiles;                            // places of many-row tiles of sequences
   bool by_tokens;                            // a sequence's place goes by the tokens before it, not by the sequences
-  int ranges;                                // parts of the line, at most; 0: no groups
+  int ranges;                                // parts of the line, at most; 0: each sequence goes by itself
   int slot_rows;                             // rows of a piece of a cut tile of the line: 16 where no tile has more
   // places in the workspace, in floats: whole tiles' results by row, of shared
   // and own keys ([T * q_heads][130] each); the line's cut tiles' by workgroup

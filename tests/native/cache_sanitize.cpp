@@ -362,9 +362,10 @@ static int attend() {
             CHECK(call(i, i, g, h, x, 1.0f, x, ws, need, n, T, m) == QDR_OK);
             const qdr::SharedPlan &p = shared_plan;
             const size_t rows = (size_t)T * h;
-            CHECK((p.ranges >= 1) == (g > 0) && p.ranges * 2 <= 512 && p.few_splits >= 1 && p.few_splits <= 32 && p.many_splits >= 1 && p.many_splits <= 32);
+            const bool together = g > 0 && n > g && (int64_t)(n - g) * 2 * m * 2 >= qdr::kLeastSaved;
+            CHECK((p.ranges >= 1) == together && p.ranges * 2 <= 512 && p.few_splits >= 1 && p.few_splits <= 32 && p.many_splits >= 1 && p.many_splits <= 32);
             CHECK(p.slot_rows == 128 || (p.slot_rows == 16 && T <= p.few_tokens));
-            CHECK(p.cut == (g ? 2 * rows * 130 : 0) && p.few_pieces == p.cut + (size_t)p.ranges * 2 * 2 * p.slot_rows * 130 && p.floats == p.info + (size_t)T * p.few_parts * 8);
+            CHECK(p.cut == (together ? 2 * rows * 130 : 0) && p.few_pieces == p.cut + (size_t)p.ranges * 2 * 2 * p.slot_rows * 130 && p.floats == p.info + (size_t)T * p.few_parts * 8);
             CHECK(p.many_pieces == p.few_pieces + (p.few_splits > 1 ? (size_t)n * 2 * p.few_parts * p.few_splits * 16 * 130 : 0));
             CHECK(p.info == p.many_pieces + (p.many_splits > 1 ? (size_t)p.many_tiles * 2 * p.many_parts * p.many_splits * 128 * 130 : 0));
             CHECK((p.many_tiles > 0) == (T > p.few_tokens));

@@ -23,7 +23,7 @@ def torch_dev():
 class Scene:
     """Groups (prefix, [(new, tail), ...]) over a cache whose unused rows are not finite."""
 
-    def __init__(self, torch, groups, page, heads, q_heads, kind, seed=3, alone=()):
+    def __init__(self, torch, groups, page, heads, q_heads, kind, seed=3, alone=(), wide=True):
         self.lens, self.contexts, self.shared, self.group_cu, ks, vs, spans = [], [], [], [0], [], [], []
         every = list(groups) + [(0, [x]) for x in alone]
         for p, rows in every:
@@ -41,6 +41,8 @@ class Scene:
             self.group_cu.append(self.group_cu[-1] + len(rows))
         n = len(self.lens)
         width = max([-(-c // page) for c in self.contexts] + [1])
+        if wide and n > len(groups):   # tables that show enough keys for the groups' rows to go together
+            width = max(width, -(-12288 * 32 // ((n - len(groups)) * heads * page)))
         need = sum(-(-c // page) for c in self.contexts)
         order = np.random.default_rng(seed).permutation(need + 3).tolist()
         table, b = [[-1] * width for _ in range(n)], 0
@@ -95,10 +97,11 @@ SCENES = [
 
 
 @pytest.mark.parametrize("kind", [INT8, BF16])
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("groups,page,q_heads,heads,alone", SCENES, ids=str)
-def test_attend_shared(torch_dev, kind, groups, page, q_heads, heads, alone):
+def test_attend_shared(torch_dev, kind, groups, page, q_heads, heads, alone, wide):
     torch = torch_dev
-    s = Scene(torch, groups, page, heads, q_heads, kind, alone=alone)
+    s = Scene(torch, groups, page, heads, q_heads, kind, alone=alone, wide=wide)
     o = s.run(torch)
     s.check(torch, o)
     assert s.cache.qdr_kv_poll_device_error() == 0
@@ -117,6 +120,16 @@ def test_attend_shared_long(torch_dev, kind, members):
     """A batch behind a long prefix, cut into many pieces."""
     torch = torch_dev
     s = Scene(torch, [(9000, [(1, 1 + 13 * i % 90) for i in range(members)])], 64, 2, 8, kind)
+    s.check(torch, s.run(torch))
+    assert s.cache.qdr_kv_poll_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", [INT8, BF16])
+@pytest.mark.parametrize("groups", [255, 256, 257, 600])
+def test_attend_shared_many_groups(torch_dev, kind, groups):
+    """More groups than a workgroup has at hand, some of them of one sequence, empty, or without whole blocks."""
+    torch = torch_dev
+    s = Scene(torch, [(64 + 32 * (i % 5) - 60 * (i % 7 == 3), [(1 + (i % 50 == 7) * 8, 9 + i % 40)] * (i % 4)) for i in range(groups)], 32, 1, 2, kind)
     s.check(torch, s.run(torch))
     assert s.cache.qdr_kv_poll_device_error() == 0
 
@@ -219,13 +232,14 @@ def test_attend_shared_non_finite(torch_dev, kind, members):
             assert hit[:, 4:].isnan().sum() == members * 4
 
 
+@pytest.mark.parametrize("width", [12, 1600])      # entries of a table: each sequence by itself, or all together
 @pytest.mark.parametrize("kind", [INT8, BF16])
-def test_fork_write_attend(torch_dev, kind):
+def test_fork_write_attend(torch_dev, kind, width):
     """A run as a server makes it: a prompt is written, forks into samples, and
     for some steps each sample's tokens are turned, written and attended to, the
     shared pages once; captured as graphs (two tables in turn) and eagerly."""
     torch, page, heads, q_heads, prompt, m, steps = torch_dev, 32, 2, 8, 150, 5, 6
-    width, total = 12, 40
+    total = 40
     freq, amplitude = qdr.qdr_rotary_frequencies(qdr.ROTARY_TURNS, 128, 10000.0, 4.0, 64.0, 1.0, 4.0)
     rot = qdr.Rotary(freq, qdr.ROTARY_HALF, amplitude)
     g0 = torch.Generator("cuda").manual_seed(8)
