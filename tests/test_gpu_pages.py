@@ -331,6 +331,57 @@ def test_pages_beyond_32_bits(torch_dev):
     assert torch.equal(x[:2], last) and table.tolist() == [[1]] and outs[1][:3].tolist() == [1, 1, 5]
 
 
+def test_pages_captured(torch_dev):
+    """A compaction, copies of pages and of slots in one graph: every replay takes
+    the numbers that its inputs hold by then, with eager calls between replays."""
+    torch, total, heads, n = torch_dev, 40, 2, 6
+    r = random.Random(9)
+    (a, x), (b, y) = a_cache(torch, total, 32, heads, BF16, 1), a_cache(torch, 7, 32, heads, BF16, 2)
+    pool = qdr.Pool(n, 1, [32], np.ones((1, D), np.float32))
+    S = torch.randn((n, 1, D, D), generator=torch.Generator("cuda").manual_seed(4), device="cuda")
+    slots = i32(torch, list(range(n)))
+    refs, table = i32(torch, [0] * total), i32(torch, [[-1] * 5] * 3)
+    outs = [torch.empty_like(refs), torch.empty_like(refs), torch.empty_like(table)]
+    pairs = [i32(torch, [-1, -1, -1]) for _ in range(4)]
+    ws = torch.empty(a.qdr_kv_compact_workspace(), dtype=torch.uint8, device="cuda")
+
+    def calls():
+        a.qdr_kv_compact(refs, table, *outs, workspace=ws)
+        a.qdr_kv_copy(pairs[0], pairs[1], to=b)
+        pool.qdr_slot_copy(pairs[2], pairs[3])
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        calls()
+    for i in range(4):
+        held_now = [r.choice((0, 1, 2)) for _ in range(total)]
+        rows = [[r.randrange(-1, total) for _ in range(5)] for _ in range(3)]
+        src, dst, s, d = r.sample(range(total), 3), r.sample(range(7), 3), r.sample(range(3), 3), r.sample(range(3, 6), 3)
+        for to, values in zip([refs, table, *pairs], [held_now, rows, src, dst, s, d]):
+            to.copy_(i32(torch, values))
+        pool.qdr_pack(slots, S * (i + 1))
+        raw = [pool.qdr_read_raw(k) for k in range(n)]
+        moved, new_refs, tables = compacted(held_now, rows)
+        want, other = x.clone(), y.clone()
+        for p, to in enumerate(moved):
+            if to >= 0 and to != p:
+                want[to] = x[p]
+        for p, q in zip(src, dst):
+            other[q] = want[p]
+        torch.cuda.synchronize()
+        if i == 2:
+            calls()
+        else:
+            g.replay()
+        torch.cuda.synchronize()
+        assert [z.tolist() for z in outs] == [moved, new_refs, tables], f"turn {i}"
+        assert torch.equal(x, want) and torch.equal(y, other), f"turn {i}"
+        for p, q in zip(s, d):
+            assert np.array_equal(pool.qdr_read_raw(q), raw[p])
+        assert a.qdr_kv_poll_device_error() == 0 and b.qdr_kv_poll_device_error() == 0 and pool.qdr_poll_device_error() == 0
+
+
 def test_pages_refusals(torch_dev):
     torch = torch_dev
     cache, _ = a_cache(torch, 4, 32, 1, INT8)
