@@ -231,7 +231,10 @@ __device__ __forceinline__ u32x4 quantise(const float *x, float *scale) {
 // first rows are on their way.  A key row's thread has 16 channels in a row; what
 // they are paired with in the half layout are 16 others of the same row, which
 // it reads a second time (from the cache) rather than trade them between lanes.
-// Queries go as in qdr_rotary.hip.
+// Queries go as in qdr_rotary.hip.  Bound by memory: 16391 tokens of 5 prompts, 32
+// query and 8 key heads, bfloat16: 77 us for 403 MB (5.2 TB/s) when the queries
+// stayed in the caches, with qdr_kv_read of it all 112.5 us a pass and 106.7 now.
+// 64 single tokens: 8 us, latency.
 template <int KIND>
 __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
   constexpr int E = KIND / 8, kPasses = 4;
@@ -258,9 +261,8 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
 
   if (!keys) {
     const int h0 = (part - A.kv_parts) * A.query_heads, heads = min(A.query_heads, A.q_heads - h0);
-    const int rows = (at.hi - at.lo) * heads, p = tid & 7;
-    const bool turns = 2 * p < A.rotary.channels / 8, halves = turns && A.rotary.layout == 0;
-    const int c0 = halves ? 8 * p : 16 * p, c1 = halves ? pairs + 8 * p : 16 * p + 8;
+    const int rows = (at.hi - at.lo) * heads;
+    const Units u = units_of(A.rotary.channels, A.rotary.layout, tid & 7);
     for (int base = 0; base < rows; base += 32 * kPasses) {
       u32x4 a[kPasses], b[kPasses];
       int tok[kPasses], head[kPasses];
@@ -271,8 +273,8 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
         head[i] = h0 + row - tok[i] * heads;
         tok[i] += at.lo;
         const size_t from = (size_t)(at.token0 + tok[i]) * A.q_stride + (size_t)head[i] * kD;
-        a[i] = *(const u32x4_a4 *)(A.q + from + c0);
-        b[i] = *(const u32x4_a4 *)(A.q + from + c1);
+        a[i] = read_once(A.q + from + u.c0);
+        b[i] = read_once(A.q + from + u.c1);
       }
       if (base == 0) make_table();
 #pragma unroll
@@ -280,25 +282,17 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
         if (base + 32 * i + (tid >> 3) >= rows) continue;
         if (!at.fits) {
           a[i] = b[i] = (u32x4){0, 0, 0, 0};
-        } else if (turns) {
-          CosSin w[8];
+        } else if (u.turn0) {
           float x[16];
-          pairs_of(table[tok[i]], p, w);
           widen16(a[i], x);
           widen16(b[i], x + 8);
-          if (A.rotary.layout == 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) turn(x[e], x[8 + e], w[e], &x[e], &x[8 + e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) turn(x[2 * e], x[2 * e + 1], w[e], &x[2 * e], &x[2 * e + 1]);
-          }
+          turn_units(u, table[tok[i]], x);
           a[i] = narrow16(x);
           b[i] = narrow16(x + 8);
         }
         const size_t to = ((size_t)(at.token0 + tok[i]) * A.q_heads + head[i]) * kD;
-        *(u32x4_a4 *)(A.q_out + to + c0) = a[i];
-        *(u32x4_a4 *)(A.q_out + to + c1) = b[i];
+        write_past(A.q_out + to + u.c0, a[i]);
+        write_past(A.q_out + to + u.c1, b[i]);
       }
     }
     return;
@@ -346,7 +340,8 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
         if (!turns[i]) continue;
         CosSin w[8];
         float y[8], unused;
-        pairs_of(table[in ? r : at.lo], unit_pairs[i], w);
+        pairs_of(table[in ? r : at.lo], 2 * unit_pairs[i], w);
+        pairs_of(table[in ? r : at.lo], 2 * unit_pairs[i] + 1, w + 4);
         widen16(other[i], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -356,7 +351,8 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
       }
     } else if (turns[0]) {   // (and with it turns[1])
       CosSin w[8];
-      pairs_of(table[in ? r : at.lo], seg, w);
+      pairs_of(table[in ? r : at.lo], 2 * seg, w);
+      pairs_of(table[in ? r : at.lo], 2 * seg + 1, w + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) turn(x[2 * e], x[2 * e + 1], w[e], &x[2 * e], &x[2 * e + 1]);
     }

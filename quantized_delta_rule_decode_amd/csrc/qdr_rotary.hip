@@ -2,8 +2,13 @@
 // A workgroup takes some tokens of up to 128 heads, about 128 rows (token,
 // head): the pairs' sines and cosines are made once a token, in LDS, while the
 // rows are on their way, and each is used by every head.  Eight threads a row,
-// sixteen channels each, which hold whole pairs in both layouts: 8 pairs are
-// channels 8 p .. and channels/2 + 8 p .., or 16 p ...  Bound by memory.
+// two units of eight channels each (units_of).
+// Bound by memory: 16385 tokens of 32 heads, bfloat16, 64 channels in pairs:
+// 46.5 us for 268 MB (5.8 TB/s; a copy of 4 GiB reaches 5.4).  A thread's two
+// units next to each other instead took 49.0, or 64 with stores past the caches
+// (each filled half a line); as here without those stores and loads 50.8.  One
+// token of 8 heads: 2.3 us of kernel, 6.5 a call.  fp32 stays in the caches (a
+// store fills half of each 32 bytes).
 #include "qdr_rotary.h"
 
 namespace qdr {
@@ -19,8 +24,8 @@ struct Eight;
 template <>
 struct Eight<true> {
   u32x4 w;
-  __device__ __forceinline__ void load(const void *x, size_t at) { w = *(const u32x4_a4 *)((const uint16_t *)x + at); }
-  __device__ __forceinline__ void store(void *y, size_t at) const { *(u32x4_a4 *)((uint16_t *)y + at) = w; }
+  __device__ __forceinline__ void load(const void *x, size_t at) { w = read_once((const uint16_t *)x + at); }
+  __device__ __forceinline__ void store(void *y, size_t at) const { write_past((uint16_t *)y + at, w); }
   __device__ __forceinline__ void get(float *x) const { widen16(w, x); }
   __device__ __forceinline__ void set(const float *x) { w = narrow16(x); }
 };
@@ -51,9 +56,8 @@ __global__ void __launch_bounds__(256) k_rotate(RotateArgs A) {
   const int tid = threadIdx.x, part = blockIdx.x % A.head_parts;
   const int t0 = (int)(blockIdx.x / A.head_parts) * A.tokens, h0 = part * A.part_heads;
   const int tokens = min(A.tokens, A.T - t0), heads = min(A.part_heads, A.heads - h0);
-  const int rows = tokens * heads, p = tid & 7, pairs = A.rotary.channels >> 1;
-  const bool turns = 2 * p < A.rotary.channels / 8, halves = turns && A.rotary.layout == 0;
-  const int c0 = halves ? 8 * p : 16 * p, c1 = halves ? pairs + 8 * p : 16 * p + 8;
+  const int rows = tokens * heads, pairs = A.rotary.channels >> 1;
+  const Units u = units_of(A.rotary.channels, A.rotary.layout, tid & 7);
   bool ready = false;
   for (int base = 0; base < rows; base += 32 * kPasses) {
     Eight<BF16> a[kPasses], b[kPasses];
@@ -64,8 +68,8 @@ __global__ void __launch_bounds__(256) k_rotate(RotateArgs A) {
       tok[i] = row / heads;
       head[i] = h0 + row - tok[i] * heads;
       const size_t at = (size_t)(t0 + tok[i]) * A.x_stride + (size_t)head[i] * kD;
-      a[i].load(A.x, at + c0);
-      b[i].load(A.x, at + c1);
+      a[i].load(A.x, at + u.c0);
+      b[i].load(A.x, at + u.c1);
     }
     if (!ready) {
       const int pair = tid & 63;
@@ -82,25 +86,17 @@ __global__ void __launch_bounds__(256) k_rotate(RotateArgs A) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       if (base + 32 * i + (tid >> 3) >= rows) continue;
-      if (turns) {
-        CosSin w[8];
+      if (u.turn0) {
         float x[16];
-        pairs_of(table[tok[i]], p, w);
         a[i].get(x);
         b[i].get(x + 8);
-        if (A.rotary.layout == 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) turn(x[e], x[8 + e], w[e], &x[e], &x[8 + e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) turn(x[2 * e], x[2 * e + 1], w[e], &x[2 * e], &x[2 * e + 1]);
-        }
+        turn_units(u, table[tok[i]], x);
         a[i].set(x);
         b[i].set(x + 8);
       }
       const size_t at = (size_t)(t0 + tok[i]) * A.y_stride + (size_t)head[i] * kD;
-      a[i].store(A.y, at + c0);
-      b[i].store(A.y, at + c1);
+      a[i].store(A.y, at + u.c0);
+      b[i].store(A.y, at + u.c1);
     }
   }
 }
