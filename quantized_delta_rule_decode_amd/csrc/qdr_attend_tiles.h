@@ -380,8 +380,8 @@ __device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int
 // The weights are rounded to bfloat16 once here, 2^-8 of each at most, which
 // averages out over the keys (relative error of the result 0.0021, of which
 // its own rounding is 0.0017); a second part would add half the products again.
-// 4 sequences of 1024 new tokens, 8192 cached, 32 query and 8 key heads: 518 us
-// for 357 GFLOP, 690 TFLOP/s.  For 64 keys and 32 rows a wave has 1024 cycles of
+// 4 sequences of 1024 new tokens, 8192 cached, 32 query and 8 key heads: 483 us
+// for 357 GFLOP, 740 TFLOP/s (what follows was measured at 518).  For 64 keys and 32 rows a wave has 1024 cycles of
 // products and about 1600 of vector instructions, 1000 of them exponentials;
 // the matrix cores are busy 33% of the time and the vector units 39%, seldom
 // together, and the operands take 3/4 of the LDS bandwidth.  Tried and slower:
@@ -390,6 +390,12 @@ __device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int
 // registers; 930 us), wave priorities around the products (596).
 constexpr float kSlack = 8.0f;
 
+// 8 bits: a value's scale that is not finite (its vector had a NaN or an infinity)
+// enters as 0, so that rows that do not see it need no select for every weight (three
+// instructions, a seventh of the pass), and the rows that see it, all of whose
+// channels it makes NaN, get that by their sum.  4 x 1024 new tokens over 8192, 8-bit:
+// 695 us with the selects, 670 so; two copies of the weights' code, one with them,
+// 990 (spills).
 template <int KIND>
 struct ManyIn {
   u32x4 k[KIND == 8 ? 2 : 4], v[KIND == 8 ? 2 : 4];
@@ -401,6 +407,7 @@ template <int KIND>
 struct ManyShared {
   u32x4 k[2][8][64], v[2][8][64];    // [block of the pair]
   f32x4 scale[2][2][8];              // [block][keys, values]
+  uint32_t odd[2];                   // [block] tokens whose values' scale is not finite, and 0 above
 };
 
 // What a tile's pass over keys leaves: lane (g, i16) of wave w has, of rows 32 w +
@@ -484,7 +491,12 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
         to.k[y][2 * w + 1][l] = widen(in.k[y][2], in.k[y][3]).w;
         to.v[y][2 * w][l] = widen(in.v[y][0], in.v[y][1]).w;
         to.v[y][2 * w + 1][l] = widen(in.v[y][2], in.v[y][3]).w;
-        if (w == y) ((float *)to.scale[y])[l] = in.scale;
+        if (w == y) {
+          const bool odd = l >= 32 && !(fabsf(in.scale) < INFINITY);
+          const uint32_t tokens = (uint32_t)(__ballot(odd) >> 32);
+          ((float *)to.scale[y])[l] = odd ? 0.0f : in.scale;
+          if (l == 0) to.odd[y] = in.left[y] < kBlock ? tokens & ((1u << max(in.left[y], 0)) - 1u) : tokens;
+        }
       } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -555,6 +567,16 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
             if (key >= (i < 2 ? left0 : left1) || (block + (i >> 1)) * kBlock + key > limit[c]) s[c][i][r] = kNone;
           }
     }
+    if (KIND == 8) {
+      const uint32_t odd0 = __builtin_amdgcn_readfirstlane(now.odd[0]), odd1 = __builtin_amdgcn_readfirstlane(now.odd[1]);
+      if (odd0 | odd1) {
+        asm volatile("");
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if ((odd0 && block * kBlock + __builtin_ctz(odd0) <= limit[c]) || (odd1 && (block + 1) * kBlock + __builtin_ctz(odd1) <= limit[c]))
+            sum[c] = __builtin_nanf("");
+      }
+    }
     Frag pf[2][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -585,9 +607,7 @@ __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, in
         }
         if (KIND == 8) {
           const f32x4 by = now.scale[i >> 1][1][4 * (i & 1) + g];
-          // a masked key's scale is not looked at
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p[r] = masked && s[c][i][r] == kNone ? 0.0f : p[r] * by[r];
+          p *= by;
         }
         pf[c][i >> 1].u[2 * (i & 1)] = pack_bf16(p[0], p[1]);
         pf[c][i >> 1].u[2 * (i & 1) + 1] = pack_bf16(p[2], p[3]);
