@@ -1,8 +1,21 @@
 // qdr_attend_shared.hip -- attention of new tokens over the paged cache where
 // sequences share their first tokens: a group's rows go through the shared keys
 // together, every sequence's rows through its own, in one launch whose
-// workgroups have equal parts of the groups' work or a sequence's tile; a second one joins what each
-// row's passes left (qdr_cache.h).
+// workgroups have equal parts of the groups' work or a sequence's tile; a second
+// one joins what each row's passes left (qdr_cache.h).  With m, s and y a pass's
+// maximum, sum of weights and unnormalised result: M = max m,
+// o = sum 2^(m - M) y / sum 2^(m - M) s.
+//
+// 64 sequences with up to 700 tokens each behind 16384 shared ones, 32 and 8 heads,
+// 8-bit: 62 to 64 us (every sequence by itself 233): 54 for the passes (17.7 GFLOP and
+// 108 MB, 15 or 20 us at the card's rates), in which the vector units are
+// busy half of the time and the matrix cores a sixth, the rest being the start of
+// the line, a part's first blocks and results that leave at its end; 8 for the
+// join of 32 MB of results, fp32 because each is one of many that are added.
+// 32 sequences of up to 100 new tokens behind 4 prefixes of up to 4100, 32 and 8
+// heads, bfloat16: 261 us for 140 GFLOP, 535 TFLOP/s, the rate of the many-row
+// loop (qdr_attend_tiles.h) less the parts' ends.  Two sequences behind 300: 12 us,
+// two launches' latency.
 #include "qdr_attend_tiles.h"
 #include "qdr_cache.h"
 
@@ -104,8 +117,11 @@ struct Item {
 };
 constexpr int kFew = 1, kPrefix = 2, kSkipped = 4, kPooled = 8;   // kPooled: its rows have shared keys too
 
-// What a workgroup, a tile and each of its blocks cost, in 0.1 us.
-constexpr int kGroupCost = 60, kTileCost = 60, kLeastCost = 100;   // (the last: least of a part)
+// What a workgroup, a tile and each of its blocks cost, in 0.1 us, with the
+// results they leave.  64 sequences behind 16384 tokens, 8-bit and bfloat16, and
+// 8 x 8 of four new tokens behind 2048 (us a call): 60 and 60 63.2, 75.5, 52.8; 100
+// and 60 61.3, 73.8, 52.2; 140 and 60 61.3, 64.0, 49.1; 140 and 100 61.8, 63.8, 48.1.
+constexpr int kGroupCost = 140, kTileCost = 100, kLeastCost = 100;   // (the last: least of a part)
 template <int KIND>
 __device__ __forceinline__ double block_cost(int flags) { return flags & kFew ? (KIND == 8 ? 8.0 : 14.0) : 13.0; }
 template <int KIND>
