@@ -7,11 +7,11 @@
 // o = sum 2^(m - M) y / sum 2^(m - M) s.
 //
 // 64 sequences with up to 700 tokens each behind 16384 shared ones, 32 and 8 heads,
-// 8-bit: 62 to 64 us (every sequence by itself 233): 54 for the passes (17.7 GFLOP and
+// 8-bit: 62 to 64 us (every sequence by itself 233): 56 for the passes (17.7 GFLOP and
 // 108 MB, 15 or 20 us at the card's rates), in which the vector units are
 // busy half of the time and the matrix cores a sixth, the rest being the start of
 // the line, a part's first blocks and results that leave at its end; 8 for the
-// join of 32 MB of results, fp32 because each is one of many that are added.
+// join of 27 MB of results, fp32 because each is one of many that are added.
 // 32 sequences of up to 100 new tokens behind 4 prefixes of up to 4100, 32 and 8
 // heads, bfloat16: 261 us for 140 GFLOP, 535 TFLOP/s, the rate of the many-row
 // loop (qdr_attend_tiles.h) less the parts' ends.  Two sequences behind 300: 12 us,
