@@ -350,6 +350,30 @@ def test_attend_values_that_are_not_finite(torch_dev, kind, rows):
             assert ((got.double() - ref[row, 2:]).abs() <= room[row, 2:]).all()
 
 
+@pytest.mark.parametrize("rows", [1, 40, 150])
+def test_attend_values_of_no_weight_that_are_not_finite(torch_dev, rows):
+    """Some 8-bit vectors of values that are NaN, several in a block and one in each
+    of two neighbouring ones, behind keys whose weights underflow: still NaN for the
+    rows that see any, in their head, and nothing for the others."""
+    torch = torch_dev
+    H, c, Q = 2, 300, 4
+    cache, pages, k, v = fill(torch, [c], 32, H, INT8)
+    q = torch.ones((rows, Q, D), dtype=torch.bfloat16, device="cuda")
+    cu, ctx = i32(torch, [0, rows]), i32(torch, [c])
+    clean, o = torch.empty_like(q), torch.empty_like(q)
+    cache.qdr_kv_attend(pages, cu, ctx, q, clean, scale=1.0)
+    assert torch.isfinite(clean).all()
+    first = c - 1 if rows == 1 else c - 30
+    for at in {first, c - 1, c - 2, c - 3} if rows > 1 else {first}:
+        kk, vv = torch.full((1, H, D), -60.0, dtype=torch.bfloat16, device="cuda"), v[at:at + 1].bfloat16()   # a score of -7680
+        vv[0, 1, 5] = float("nan")
+        cache.qdr_kv_write(pages, i32(torch, [0, 1]), i32(torch, [at + 1]), kk, vv)
+    cache.qdr_kv_attend(pages, cu, ctx, q, o, scale=1.0)
+    seen = max(rows - 30, 0)
+    assert torch.equal(o[:seen], clean[:seen])
+    assert o[seen:, 2:].isnan().all() and torch.isfinite(o[:, :2]).all()
+
+
 @pytest.mark.parametrize("kind", [INT8, BF16])
 def test_attend_graphs_and_streams(torch_dev, kind):
     """The cache as a decode loop uses it, captured: write the token, attend.
