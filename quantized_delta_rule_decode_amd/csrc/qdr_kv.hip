@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
           widen16(b[i], x + 8);
           turn_units(u, table[tok[i]], x);
           a[i] = narrow16(x);
-          b[i] = narrow16(x + 8);
+          if (u.turn1) b[i] = narrow16(x + 8);
         }
         const size_t to = ((size_t)(at.token0 + tok[i]) * A.q_heads + head[i]) * kD;
         write_past(A.q_out + to + u.c0, a[i]);
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
     } else if (in) {
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        *(u32x4 *)(blk + ((tile * 4 + half * 2 + p) * 64 + g * 16 + key) * 16) = narrow16(x + 8 * p);
+        *(u32x4 *)(blk + ((tile * 4 + half * 2 + p) * 64 + g * 16 + key) * 16) = turns[p] ? narrow16(x + 8 * p) : unwiden16(x + 8 * p);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         *(uint16_t *)&to[channel_at<E>(16 * seg + i) + 2 * pos] = (uint16_t)(v0[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));

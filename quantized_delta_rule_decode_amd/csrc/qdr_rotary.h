@@ -123,5 +123,13 @@ __device__ __forceinline__ u32x4 narrow16(const float *x) {
   for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
   return w;
 }
+// widen16's inverse: channels that do not turn keep every bit (rounding would
+// quiet a NaN).
+__device__ __forceinline__ u32x4 unwiden16(const float *x) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(x[2 * i]) >> 16 | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
+  return w;
+}
 
 }  // namespace qdr

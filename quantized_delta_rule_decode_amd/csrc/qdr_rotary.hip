@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) k_rotate(RotateArgs A) {
         b[i].get(x + 8);
         turn_units(u, table[tok[i]], x);
         a[i].set(x);
-        b[i].set(x + 8);
+        if (u.turn1) b[i].set(x + 8);
       }
       const size_t at = (size_t)(t0 + tok[i]) * A.y_stride + (size_t)head[i] * kD;
       a[i].store(A.y, at + u.c0);
