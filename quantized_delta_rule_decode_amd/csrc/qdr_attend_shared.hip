@@ -174,9 +174,9 @@ __device__ __forceinline__ Item item_of_sequence(const SharedArgs &S, const Shar
 // of the part in their tile.
 struct Passes {
   int r0, r1, row;
-  int flags;           // kFew, kPooled, kPieces; kDone: o is written
+  uint32_t flags;      // kFew, kPooled, kPieces; kDone: o is written; passes over own keys: the sequence above
 };
-constexpr int kDone = 16, kPieces = 128;
+constexpr int kDone = 16, kPieces = 128, kSequenceShift = 8;   // (n is under 2^24)
 
 // The line of the groups' work, cut into ranges of `step` (rounded down to whole costs,
 // the same everywhere).
@@ -288,7 +288,7 @@ __device__ __forceinline__ void make_job(const SharedArgs &S, const SharedPlan &
   // each token's passes are written down once
   Passes *info = (Passes *)(S.a.part + plan.info);
   job.info = kvh == 0 && line.range == r0 ? info + (size_t)(t.first + t.token) * plan.few_parts + part : nullptr;
-  job.passes = {r0, r1, 0, flags & kFew};
+  job.passes = {r0, r1, 0, (uint32_t)(flags & kFew)};
   job.info_step = plan.few_parts;
 }
 
@@ -321,7 +321,8 @@ __device__ __forceinline__ bool make_piece(const SharedArgs &S, const SharedPlan
   job.cell = (few ? plan.few_pieces : plan.many_pieces) + ((((size_t)tile * P.heads + kvh) * parts + part) * splits + split) * ((few ? kFewRows : kManyRows) * kCell);
   Passes *info = (Passes *)(S.a.part + plan.info) + (size_t)P.T * plan.few_parts;
   job.info = kvh == 0 && split == 0 ? info + (size_t)(t.first + token) * plan.few_parts + part : nullptr;
-  job.passes = {pieces == 1 ? 0 : tile, pieces - 1, 0, (it.flags & (kFew | kPooled)) | (alone ? kDone : 0) | (pieces == 1 ? 0 : kPieces)};
+  const int kept = (it.flags & (kFew | kPooled)) | (alone ? kDone : 0) | (pieces == 1 ? 0 : kPieces);
+  job.passes = {pieces == 1 ? 0 : tile, pieces - 1, 0, (uint32_t)kept | (uint32_t)it.b << kSequenceShift};
   job.info_step = plan.few_parts;
   return true;
 }
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan pl
     const int head = (int)(row - token * A.q_heads), kvh = head / plan.group, h = head - kvh * plan.group;
     const Passes *shared = (const Passes *)(A.part + plan.info) + token * plan.few_parts, *own = shared + (size_t)P.T * plan.few_parts;
     // (all that is read before the cells, at once)
-    Passes o = own[0], first = shared[0], s{0, -1, 0, 0};
+    Passes o = own[0], first = shared[0], s{0, -1, 0, 0u};
     if (token < begin || token >= end) continue;
     if (o.flags & kDone && plan.few_parts == 1) {
       if (OWN > 1) i += min((int64_t)(OWN - 1 - i), (int64_t)A.q_heads - 1 - head);   // and the token's other rows are
@@ -575,7 +576,10 @@ __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan pl
     }
     at_part(own, o);
     if (o.flags & kDone) continue;
-    // (counts out of order leave rows without)
+    // Counts out of order leave rows without passes, whose places hold what an
+    // earlier call left: a row is written where its sequence has it in this one.
+    const int b = (int)(o.flags >> kSequenceShift), at_b = min(b, P.n - 1), c0 = P.cu[at_b], c1 = P.cu[at_b + 1];
+    const bool has = b < P.n && c0 >= 0 && c0 <= token && token < c1 && c1 <= P.T;
     const bool pieces = o.flags & kPieces;
     auto bad = [&](const Passes &p) { return p.r0 < 0 || p.r0 > p.r1 || p.r1 >= plan.ranges || p.row < 0 || p.row >= plan.slot_rows; };
     const bool own_few = o.flags & kFew;
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(256) k_join_shared(SharedArgs S, SharedPlan pl
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += __shfl_xor(y[j], 32);
-    if (half) continue;
+    if (half || !has) continue;
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     *(u32x2_a4 *)(A.o + row * kD + 4 * l) = (u32x2){pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
   }
