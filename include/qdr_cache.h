@@ -71,8 +71,10 @@ qdr_status qdr_rotary_destroy(qdr_rotary *rotary);
  * (and, divided by amplitude^2, its inverse).
  * x, y: row t at t * stride elements, [heads][128] in a row; x_stride, y_stride
  * from heads*128 to 2^30.  y may be x with the same stride; other overlaps race.
- * fp32, or bfloat16 (y rounded to nearest even, strides even).  T up to 2^30,
- * heads up to 2^17. */
+ * fp32, or bfloat16 (y rounded to nearest even, strides even).  heads up to 2^17.
+ * A workgroup takes min(32, 128 / heads) tokens, at least one, of up to 128 heads,
+ * and a call of 2^24 workgroups or more is refused: 2^29 tokens of one to four
+ * heads, 2^26 of 32. */
 qdr_status qdr_rotate(qdr_rotary *rotary, const int32_t *positions, int32_t T, int32_t heads, const float *x,
                       int64_t x_stride, float *y, int64_t y_stride, void *stream);
 qdr_status qdr_rotate_bf16(qdr_rotary *rotary, const int32_t *positions, int32_t T, int32_t heads,

@@ -149,8 +149,7 @@ qdr_status make_shared(const qdr_kv *kv, int32_t n, int32_t T, int32_t groups, i
   QDR_TRY(check_groups(few));
   QDR_TRY(check_groups(many));
   QDR_TRY(check_groups((few + many + plan->ranges) * heads + 1));
-  QDR_TRY(check_groups(((int64_t)T + 3) / 4 * heads));
-  QDR_TRY(check_groups((int64_t)T * q_heads / 4));
+  QDR_TRY(check_groups((int64_t)T * q_heads / 4));   // of the join: four rows a workgroup, the most that it takes
   *bytes = plan->floats * sizeof(float);
   return QDR_OK;
 }
