@@ -64,11 +64,12 @@ qdr_status qdr_rotary_destroy(qdr_rotary *rotary);
 
 /* Rows turned by their positions: the pair (a, b) of row t becomes
  *   amplitude (a cos p f - b sin p f,  a sin p f + b cos p f),  p = positions[t].
- * The angle is right to 2^-32 of a turn at any int32 position where f is at most
+ * The angle is right to 2^-31 of a turn at any int32 position where f is at most
  * a turn a token (multiples of a turn are dropped in whole numbers), and to as
- * many times that as f has turns a token above; products are fp32.  A negative position
- * turns back: with the positions negated the call is the rotation's gradient
- * (and, divided by amplitude^2, its inverse).
+ * many times that as f has turns a token above.  Its sine and cosine, times
+ * amplitude, are fp32, off by 6 x 2^-24 |amplitude| at most, and so are products
+ * and sums.  A negative position turns back: with the positions negated the call
+ * is the rotation's gradient (and, divided by amplitude^2, its inverse).
  * x, y: row t at t * stride elements, [heads][128] in a row; x_stride, y_stride
  * from heads*128 to 2^30.  y may be x with the same stride; other overlaps race.
  * fp32, or bfloat16 (y rounded to nearest even, strides even).  heads up to 2^17.

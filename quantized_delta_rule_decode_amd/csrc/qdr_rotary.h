@@ -2,10 +2,13 @@
 //
 // A pair's frequency is kept as turns a token in 64-bit fixed point, modulo
 // one turn: position times it, in 64-bit wrap-around integers, is the angle
-// modulo one turn with no rounding that grows with the position.  Its upper 32
-// bits (2^-32 of a turn, 1.5e-9 radians) go through Taylor's series on an
-// eighth of a turn to either side of the nearest quarter, whose first left-out
-// terms are under 2^-28 there.
+// modulo one turn, off by position times what the frequency was rounded by (2^-63
+// of a turn at most up to a turn a token: 2^-32 at 2^31).  It is rounded to 32
+// bits (2^-33 of a turn; 2^-31 in all, 2.9e-9 radians).  What is left of it to
+// either side of the nearest quarter, an eighth of a turn at most, becomes fp32
+// radians (2^-24 of itself twice, and the constant) and goes through Taylor's
+// series, whose first left-out terms are under 2^-28 there: sine and cosine are
+// off by 6 x 2^-24 at most, the product with the amplitude among it.
 #pragma once
 
 #include "qdr_cache.h"
