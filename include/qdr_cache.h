@@ -126,9 +126,9 @@ qdr_status qdr_slot_copy(qdr_pool *pool, const int32_t *src_slots, const int32_t
  * rows with one parent), ends (no row with it as parent) or begins (parent -1).
  *   - Its full pages (kept / page_tokens of them) are the parent's.
  *   - A last page in part is the parent's for the first row (lowest j) that
- *     keeps it in part, where no row of new_pages holds it as a full page and
- *     the program does not hold it; other rows get a copy of its tokens (in
- *     whole blocks of 32) in a free page.
+ *     keeps it in part, where no row keeps it as a full page and the program
+ *     does not hold it; other rows get a copy of its tokens (in whole blocks of
+ *     32) in a free page.  (Rows count here that then run out of pages.)
  *   - Then come free pages for the rest.  Rows get free pages in the order of j
  *     and of their tokens, lowest first; pages given up by this call are free
  *     in the next.
