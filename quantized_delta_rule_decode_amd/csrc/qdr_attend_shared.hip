@@ -115,7 +115,7 @@ struct Item {
   int flags;
   int members;         // a group's sequences
 };
-constexpr int kFew = 1, kPrefix = 2, kSkipped = 4, kPooled = 8;   // kPooled: its rows have shared keys too
+constexpr int kFew = 1, kSkipped = 4, kPooled = 8;   // kPooled: its rows have shared keys too
 
 // What a workgroup, a tile and each of its blocks cost, in 0.1 us, with the
 // results they leave.  64 sequences behind 16384 tokens, 8-bit and bfloat16, and
@@ -144,7 +144,7 @@ __device__ __forceinline__ Item item_of_group(const SharedArgs &S, const SharedP
   t.blocks = share.blocks;
   t.members = share.end - share.begin;
   const bool few = t.len <= plan.few_tokens;
-  t.flags = kPrefix | (few ? kFew : 0);
+  t.flags = few ? kFew : 0;
   t.tiles = t.len == 0 ? 0 : few ? plan.few_parts : (t.len + plan.many_tokens - 1) / plan.many_tokens * plan.many_parts;
   return t;
 }
