@@ -168,7 +168,7 @@ qdr_status qdr_kv_compact(qdr_kv *kv, const int32_t *refs, const int32_t *pages,
 /* ---- attention behind shared prefixes ---- */
 
 /* qdr_kv_attend where sequences share their first tokens, whose keys and values
- * are then read once a group instead of once a sequence.  group_cu: int32
+ * can then be read once a group instead of once a sequence (see below).  group_cu: int32
  * [groups+1], the sequences of group i are group_cu[i] .. group_cu[i+1]-1; a
  * sequence in no group shares nothing.  shared: int32 [groups]: the cache holds
  * the same at positions below shared[i] for every sequence of the group (the

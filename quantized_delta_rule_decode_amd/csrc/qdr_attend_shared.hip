@@ -7,15 +7,19 @@
 // o = sum 2^(m - M) y / sum 2^(m - M) s.
 //
 // 64 sequences with up to 700 tokens each behind 16384 shared ones, 32 and 8 heads,
-// 8-bit: 62 to 64 us (every sequence by itself 233): 56 for the passes (17.7 GFLOP and
+// 8-bit: 62 to 65 us (every sequence by itself 233): 57 for the passes (17.7 GFLOP and
 // 108 MB, 15 or 20 us at the card's rates), in which the vector units are
-// busy half of the time and the matrix cores a sixth, the rest being the start of
+// busy half of the time and the matrix cores a fifth, the rest being the start of
 // the line, a part's first blocks and results that leave at its end; 8 for the
 // join of 27 MB of results, fp32 because each is one of many that are added.
-// 32 sequences of up to 100 new tokens behind 4 prefixes of up to 4100, 32 and 8
-// heads, bfloat16: 261 us for 140 GFLOP, 535 TFLOP/s, the rate of the many-row
-// loop (qdr_attend_tiles.h) less the parts' ends.  Two sequences behind 300: 12 us,
-// two launches' latency.
+// bfloat16 75 us for 208 MB over changing keys (55 and 8 where the caches hold them).
+// 32 sequences of up to 20 new tokens behind 4 prefixes of up to 4100, 32 and 8
+// heads: bfloat16 100 us for 27 GFLOP, 8-bit 105: passes 68 and 75, join 32.  Of up
+// to 100: 264 and 329 us for 140 GFLOP (529 and 425 TFLOP/s), none of it together
+// (share_of): every sequence's rows go through the prefix by themselves, as in
+// qdr_kv_attend, in tiles that sequences of 50 to 100 tokens fill to about 85%, and
+// an empty line and a join that finds every row done cost some 5 us.  Two sequences
+// behind 300: 12 us, two launches' latency.
 #include "qdr_attend_tiles.h"
 #include "qdr_cache.h"
 
@@ -71,7 +75,15 @@ __device__ __forceinline__ Share share_of(const SharedArgs &S, const SharedPlan 
   r.bad = !order || (!none && (tokens < 0 || tokens > room || !counts || ctx > room || (int64_t)ctx - (c1 - c0) < tokens));
   r.first = c0;
   r.len = r.bad || none ? 0 : ce - c0;
-  // sequences that fill tiles by themselves gain nothing, and would leave partial results
+  // Sequences that fill tiles by themselves go so: dealt together their rows would
+  // take fewer tiles (those of 33 tokens of four heads a key head half as many), but
+  // leave partial results to join.  Measured (us a call, by themselves / together), 32
+  // and 8 heads, bfloat16, then 8-bit, tokens of each sequence; 4 groups of 8 behind
+  // 4100: 32 201 / 172, 240 / 181; 33 162 / 166, 202 / 179; 64 256 / 278, 315 / 286;
+  // 100 314 / 379, 393 / 422; 250 634 / 919, 766 / 1039; 50 to 100 264 / 276, 329 / 298.
+  // 8 behind 16384: 32 108 / 119, 125 / 128; 33 177 / 138, 219 / 156; 65 311 / 216,
+  // 394 / 247; 100 319 / 305, 402 / 340; 250 585 / 633, 724 / 777.  So the rule holds
+  // for long chunks, and loses just above a whole number of tiles and with 8 bits.
   const bool together = plan.ranges > 0 && r.end - r.begin >= 2 && r.len < (int64_t)(r.end - r.begin) * plan.many_tokens;
   r.blocks = r.len > 0 && together ? tokens / kBlock : 0;
   return r;

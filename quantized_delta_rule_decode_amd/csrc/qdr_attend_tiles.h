@@ -153,11 +153,12 @@ __device__ __forceinline__ void add_not_finite(const uint8_t *blk, int first_key
 }
 
 // ---- few rows: up to 16 (one token of up to 16 heads, a few tokens of fewer)
-// Eight waves take every eighth block of 32 keys, each with its own running
-// maximum, straight from memory into operands; they meet in LDS at the end.
-// Bound by memory: 64 requests of 8192 cached tokens (ragged), 8 heads, 8-bit:
-// 155 us for 0.85 GB, 5.5 TB/s.  A block is on its way while another is taken;
-// one request of 777 keys: 9 us, the latency of page, block, and the exchange.
+// The waves (eight in qdr_attend.hip, four in qdr_attend_shared.hip) take blocks
+// of 32 keys in turn, each with its own running maximum, straight from memory into
+// operands; they meet in LDS at the end.  Bound by memory with eight: 64 requests
+// of up to 8192 cached tokens (ragged), 8 heads, 8-bit: 151 us for 0.81 GB, 5.4
+// TB/s.  A block is on its way while another is taken; one request of 777 keys:
+// 9 us, the latency of page, block, and the exchange.
 // Up to sixteen rows it beats the many-row loop at every length (one sequence's
 // 4 new tokens and 777, 8192, 65536 cached: 10.5, 15.5, 48 us against 29, 26, 66).
 template <int KIND>
@@ -380,20 +381,22 @@ __device__ __forceinline__ void few_tile(const AttendArgs &A, const Tile &t, int
 // The weights are rounded to bfloat16 once here, 2^-8 of each at most, which
 // averages out over the keys (relative error of the result 0.0021, of which
 // its own rounding is 0.0017); a second part would add half the products again.
-// 4 sequences of 1024 new tokens, 8192 cached, 32 query and 8 key heads: 483 us
-// for 357 GFLOP, 740 TFLOP/s (what follows was measured at 518).  For 64 keys and 32 rows a wave has 1024 cycles of
-// products and about 1600 of vector instructions, 1000 of them exponentials;
-// the matrix cores are busy 33% of the time and the vector units 39%, seldom
-// together, and the operands take 3/4 of the LDS bandwidth.  Tried and slower:
-// the next block's scores between the current one's exponentials (688 us),
-// 64 rows a wave with one wave a SIMD (the accumulators leave the vector
-// registers; 930 us), wave priorities around the products (596).
+// 4 sequences of 1024 new tokens, caches of up to 8192 with them (ragged), 32
+// query and 8 key heads, calls queued back to back: bfloat16 470 us for 356
+// GFLOP, 760 TFLOP/s, 8-bit 548; caches of 8192 each 562 and 656 for 515.  For 64
+// keys and 32 rows a wave has 1024 cycles of products and about 1600 of vector
+// instructions, 1000 of them exponentials; the matrix cores are busy 37% of the
+// time and the vector units 44%, seldom together, and the operands take 3/4 of
+// the LDS bandwidth.  Tried and slower, when the first took 560: the next block's
+// scores between the current one's exponentials (688 us), 64 rows a wave with one
+// wave a SIMD (the accumulators leave the vector registers; 930 us), wave
+// priorities around the products (596).
 constexpr float kSlack = 8.0f;
 
 // 8 bits: a value's scale that is not finite (its vector had a NaN or an infinity)
 // enters as 0, so that rows that do not see it need no select for every weight (three
 // instructions, a seventh of the pass), and the rows that see it, all of whose
-// channels it makes NaN, get that by their sum.  4 x 1024 new tokens over 8192, 8-bit:
+// channels it makes NaN, get that by their sum.  4 x 1024 new tokens, caches of 8192 each:
 // 695 us with the selects, 670 so; two copies of the weights' code, one with them,
 // 990 (spills).
 template <int KIND>
@@ -421,9 +424,11 @@ struct ManyOut {
 
 // Blocks lo .. hi of a tile's keys, by thread tid.  STEPS: the operands are read
 // four at a time, eight on their way while four are used, as they are written
-// here.  Left to itself the compiler does nearly so where it has all registers
-// (4 x 1024 new tokens over 8192: 386 us, in steps 398), and where it has not reads
-// each where it is used, and waits for it (behind shared prefixes 457, in steps 406).
+// here.  Left to itself the compiler does nearly so where it has all registers,
+// and where it has not reads each where it is used.  It matters little now (us,
+// left to itself / in steps): 4 x 1024 new tokens as above 469 / 459, 8-bit 547 /
+// 543; behind shared prefixes 32 sequences of 250 new tokens 627 / 627, 8-bit 766 /
+// 753, of up to 100 262 / 263 and 335 / 329, of 20 123 / 121 and 129 / 128.
 template <int KIND, bool STEPS>
 __device__ __forceinline__ void many_tile(const AttendArgs &A, const Tile &t, int tid, int kvh, int lo, int hi, ManyShared<KIND> (&sh)[2], ManyOut &out) {
   const KvArgs &P = A.kv;

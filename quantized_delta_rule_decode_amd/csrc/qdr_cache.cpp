@@ -174,8 +174,10 @@ SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max
   const int64_t by_tokens = T / (p.few_tokens + 1) + 1;
   p.by_tokens = by_tokens < n;
   p.many_tiles = T > p.few_tokens ? (int)(T / p.many_tokens + std::min<int64_t>(by_tokens, n)) : 0;
-  // Pieces of sequences' own keys, as in plan_attend: one workgroup of few rows a
-  // compute unit, two of many; none where the tables show few blocks.
+  // Pieces of sequences' own keys: one workgroup of few rows a compute unit, two of
+  // many, of kSharedLeast and kManyLeast blocks at least.  (Simpler than plan_attend,
+  // which leaves few rows uncut up to 32 blocks and cuts longer pieces above 64
+  // tiles: here they stand beside the line.)
   const int64_t blocks = (int64_t)max_pages << (page_shift - 5), each = ((int64_t)T + n - 1) / n;
   const int64_t few = (int64_t)n * heads * p.few_parts, many = (each + p.many_tokens - 1) / p.many_tokens * n * heads * p.many_parts;
   const auto cut = [&](int64_t units, int64_t places, int64_t least) {
@@ -185,10 +187,17 @@ SharedPlan plan_shared(int n, int T, int groups, int q_heads, int heads, int max
   p.many_splits = p.many_tiles && blocks > 24 ? cut(many, 512, kManyLeast) : 1;
   // Groups' rows go through shared keys together where that can save reading
   // kLeastSaved blocks of a key head: the line and the join of its results cost
-  // some 10 us.  Measured per call (us, together / each by itself), 8-bit, 8 key
-  // heads, one group of 700 tokens a sequence behind 16384: 2 sequences (4096
-  // blocks less) 27.9 / 22.2, 4 (12288) 28.5 / 30.1, 8 40.4 / 46.2, 64 66.6 / 233;
-  // behind 8192: 8 31.3 / 31.4; behind 2048: 8 24.9 / 17.1.
+  // some 10 us.  What is saved is taken from the tables' width (only the device knows
+  // the shared counts) and from n - groups, as if no group were empty and no sequence
+  // in none.  Measured per call (us, together / each by itself), one group of 700
+  // tokens a sequence, tables as wide as that takes, 8 key heads, 8-bit, then
+  // bfloat16; behind 2048: 8 sequences (4760 blocks less) 25.1 / 18.7, 24.6 / 19.4;
+  // 8192: 4 (6648) 23.5 / 22.1, 28.5 / 22.9; 8 (15512) 31.1 / 31.5, 35.6 / 30.0; 16384:
+  // 2 (4264) 27.8 / 22.7, 38.5 / 23.4; 4 (12792) 28.6 / 30.4, 39.1 / 30.2; 1024: 32
+  // (13144) 28.5 / 25.3, 31.9 / 30.9; 4096: 32 (36952) 31.5 / 48.9, 37.1 / 50.6; 2 key
+  // heads, 4096: 32 (9238) 27.3 / 22.8, 27.3 / 25.3.  So with bfloat16 it comes somewhat
+  // early, and with tables that are wider than need be it takes the first of each pair
+  // where the second is the smaller.
   const bool together = groups && (int64_t)std::max(n - groups, 0) * heads * blocks >= kLeastSaved;
   // The line: two workgroups a compute unit, but no more than there can be work for,
   // every row a tile of as many blocks as the tables have.
@@ -320,7 +329,14 @@ qdr_status qdr_kv_write_rotary(qdr_kv *kv, qdr_rotary *rotary, const int32_t *pa
   a.q_stride = q_stride;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  // a block's table serves several heads, where blocks alone make enough workgroups
+  // A block's table serves several heads, where whole blocks alone make enough
+  // workgroups, and the other way round for queries, of which a single token has
+  // few.  Measured per call (us), 32 and 8 heads, 8-bit; 1 and 4 key heads a
+  // workgroup: 600 tokens of 5 prompts 10.6 and 13.9, 2000 18.0 and 16.7, 4100 27.7 and
+  // 25.7, 16391 80 and 72 (bfloat16 83 and 81); 64 single tokens 9.8 and 12.6 (1024,
+  // which this rule leaves at one, 77 and 50).  8 and 32 query heads: 256 single tokens
+  // 25.2 and 21.3, 1024 95 and 77, 4096 251 and 174; 64 times 9 tokens 12.4 and 17.1;
+  // 600 of 5 prompts 10.8 and 28.5, 16391 72 and 86.
   const bool prompts = T / qdr::kBlock >= 128;
   a.kv_heads = prompts ? 4 : 1;
   a.kv_parts = (kv->desc.num_heads + a.kv_heads - 1) / a.kv_heads;

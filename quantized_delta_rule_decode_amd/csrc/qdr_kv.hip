@@ -234,7 +234,9 @@ __device__ __forceinline__ u32x4 quantise(const float *x, float *scale) {
 // Queries go as in qdr_rotary.hip.  Bound by memory: 16391 tokens of 5 prompts, 32
 // query and 8 key heads, bfloat16: 77 us for 403 MB (5.2 TB/s) when the queries
 // stayed in the caches, with qdr_kv_read of it all 112.5 us a pass and 106.7 now.
-// 64 single tokens: 8 us, latency.
+// (8-bit, 472 MB: 101.5.)  64 single tokens: 8 us of kernel (bfloat16 7), the latency
+// of counts, context, page and rows one after the other, and a token's values leave
+// byte by byte.
 template <int KIND>
 __global__ void __launch_bounds__(256) k_kv_write_rotary(RotaryWriteArgs A) {
   constexpr int E = KIND / 8, kPasses = 4;

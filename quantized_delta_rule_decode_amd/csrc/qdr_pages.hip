@@ -23,11 +23,13 @@ constexpr int kCountedTiles = 2;
 // parts ... of 32 KiB, eight loads of 16 B a thread on their way at once.  What
 // is written goes past the caches (a page is larger than what they would keep of
 // it, and the lines it would push out are the sources of the other pieces), and
-// with ONCE what is read, too, which no other pair reads.  Measured per call (us:
-// plain, stores past the caches, loads, both): 1200 pages of 128 KiB copied 68.7,
-// 64.3, 64.8, 62.3; 40 slots of 3 MiB 59.3, 51.4, 53.2, 50.2; 760 pages moved
-// together 52.1, 42.7, 43.2, 44.5; 256 samples forked from 32 requests, whose
-// last pages are read up to sixteen times, 25.7, 23.5, 30.2, 27.8.
+// with ONCE what is read, too.  Measured per call over changing pages (us: plain,
+// loads past the caches, stores, both): 1200 pages of 128 KiB copied 69.6, 65.6,
+// 64.7, 63.0; 40 slots of 3 MiB 59.2, 54.2, 52.0, 49.7; 760 pages moved together 52.9,
+// 47.0, 46.9, 45.1; 256 samples forked from 32 requests, whose last pages are read up
+// to sixteen times, 27.1, 31.6, 24.2, 27.1.  Copies take both, for pairs that each have
+// a source of their own; where sources repeat, which their callers may ask for, that
+// costs: 16 states of 3 MiB to 128 slots 92, 140, 91, 143, 4 to 40 29, 35, 31, 38.
 template <bool ONCE>
 __device__ __forceinline__ void copy_bytes(const uint8_t *from, uint8_t *to, uint64_t bytes, int part, int parts) {
   for (uint64_t at = (uint64_t)part * kPiece; at < bytes; at += (uint64_t)parts * kPiece) {
