@@ -182,15 +182,15 @@ qdr_status qdr_kv_compact(qdr_kv *kv, const int32_t *refs, const int32_t *pages,
  * Whether shared keys are read once a group is decided by what that can save.
  * The call does so where (n - groups) x num_heads x (blocks of 32 tokens that
  * max_pages pages have) is 12288 or more: empty groups, as in arrays of a fixed
- * shape, count against it, and tables wider than the prefix for it.  Then a group
- * goes together that has two sequences or more and whose sequences bring fewer
- * than 128 / (q_heads / num_heads) tokens on average.  Elsewhere each sequence
- * reads the shared keys by itself, as in qdr_kv_attend.  The results are the same
- * but for rounding: the weights of shared keys that a group reads together have
- * two parts (2^-16) if the group's rows (tokens x q_heads / num_heads) are up to
- * 16 and one (2^-8) if they are more, all others those that qdr_kv_attend gives
- * the sequence.  T x q_heads has to be below 2^26.  Everything else is as in
- * qdr_kv_attend. */
+ * shape, count against it, and sequences in no group and tables wider than the
+ * prefix for it.  Then a group goes together that has two sequences or more and
+ * whose sequences bring fewer tokens on average than 128 / (q_heads / num_heads)
+ * (rounded down, at least 1).  Elsewhere each sequence reads the shared keys by
+ * itself, as in qdr_kv_attend.  The results are the same but for rounding: the
+ * weights of shared keys that a group reads together have two parts (2^-16) if the
+ * group's rows (tokens x q_heads / num_heads) are up to 16 and one (2^-8) if they
+ * are more, all others those that qdr_kv_attend gives the sequence.  T x q_heads
+ * has to be below 2^26.  Everything else is as in qdr_kv_attend. */
 qdr_status qdr_kv_attend_shared_workspace(const qdr_kv *kv, int32_t n, int32_t T, int32_t groups, int32_t q_heads,
                                           int32_t max_pages, size_t *bytes);
 qdr_status qdr_kv_attend_shared(qdr_kv *kv, const int32_t *pages, int32_t max_pages, const int32_t *cu,

@@ -83,14 +83,11 @@ def test_the_bound_tells_one_part_from_two(kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", [INT8, BF16])
-@pytest.mark.parametrize("wide", [True, False])
-@pytest.mark.parametrize("groups", FEW + [[(150, [(1, 3 + i) for i in range(9)])], [(90, [(4, 4 + i) for i in range(3)])]], ids=str)
+@pytest.mark.parametrize("wide,groups", [(True, x) for x in FEW] + [(False, x) for x in FEW + [[(150, [(1, 3 + i) for i in range(9)])], [(90, [(4, 4 + i) for i in range(3)])]]], ids=str)
 def test_few_rows_have_their_weights_in_two_parts(torch_dev, kind, wide, groups):
     """Groups of up to 16 rows a key head; and, where tables are narrow and every
     sequence goes by itself, sequences of up to 16 of any group."""
     torch, page = torch_dev, weights.PAGE
-    if wide and any(sum(m for m, _ in rows) > 4 for _, rows in groups):
-        pytest.skip("one part where more rows go through the shared keys together")
     lens, contexts, k, v, q = few_calls(groups)
     n, width = len(lens), max(-(-c // page) for c in contexts)
     if wide:
